@@ -66,6 +66,10 @@ enum {
 #define SPEC_FLAG_ZERO_RESIDUAL 2u /* rejection left no positive residual     */
 #define SPEC_FLAG_NONFINITE 4u     /* a used logits row held inf / NaN        */
 #define SPEC_FLAG_BAD_TOKEN 8u     /* a proposal outside [0, V)               */
+/* Per-sequence flag bits of the forward-pass and tree calls.  A sequence so
+ * flagged is skipped: its outputs and its cache rows are left as they were. */
+#define SPEC_FLAG_BAD_STATE 16u /* a length, padding, count, index or offset out of range */
+#define SPEC_FLAG_BAD_TREE 32u  /* n_nodes outside [0, T], or a parent that is no earlier node */
 
 /* Values of the realignment error word. */
 #define SPEC_REALIGN_OK 0
@@ -382,6 +386,147 @@ SPEC_API int spec_round_sample(const void *target_logits, spec_dtype dt, float t
                       int32_t *n_accept, int32_t *n_emit, float *out_residual, uint32_t *flags,
                       int32_t *len_new, int32_t *pad_new, int32_t *width_new, int32_t *err,
                       void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The forward pass around a round: what makes the KV the realignment moves
+ * and the hidden states the logits come from.  The calls work on one layer of
+ * a cache [L, 2, N, H, S, D] in the layouts above: a left-padded batch
+ * (N = B), or a ragged pool with idx [B] naming each sequence's row (pad NULL
+ * = 0 everywhere).  Hq query heads share the H key heads: query head h reads
+ * key head h / (Hq / H).
+ *
+ * A round feeds each sequence T nodes: node 0 is the last committed token
+ * (position len - 1), the others are proposals.  A chain's node j is proposal
+ * j - 1, as in the verification calls; in a tree node i > 0 has a parent
+ * before it.  n_nodes [B] int32 (or NULL = T) are real; nothing is written
+ * for the others.  The keys and values of a chain go to the slots the
+ * realignment expects, W - 1 + j = pad + len - 1 + j.  Those of a tree are
+ * staged in a block staged [L, 2, B, H, T, D] of their own until the accepted
+ * path is known, and spec_commit_tree then copies that path to those slots.
+ *
+ * flags [B] uint32 (or NULL): SPEC_FLAG_BAD_STATE / SPEC_FLAG_BAD_TREE or 0.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Most nodes of a round (a node's mask is one 64-bit word). */
+#define SPEC_MAX_NODES 64
+/* Largest head size of the forward-pass calls. */
+#define SPEC_MAX_HEAD_DIM 256
+
+/*
+ * Masks and depths of drafted trees, once per round for every layer.
+ * parent [B, T] int32: -1 for node 0, else an earlier node.  mask [B, T]
+ * uint64: bit a of mask[b, i] is set for node i itself and its ancestors;
+ * depth [B, T] int32: edges to the root.  Both are 0 for nodes past n_nodes
+ * and for the whole of a sequence flagged SPEC_FLAG_BAD_TREE.
+ */
+SPEC_API int spec_tree_plan(int B, int T, const int32_t *parent, const int32_t *n_nodes, uint64_t *mask,
+                   int32_t *depth, uint32_t *flags, void *cuda_stream);
+
+/*
+ * Queries, keys and values of a round, from the fused projection to where
+ * attention reads them.  qkv [B, T, Hq + 2H, D]: the query heads, the key
+ * heads, the value heads of each node.  For every query and key head x:
+ *   y = x * (mean(x^2) + eps)^-1/2 * weight     (weight [D]; NULL: y = x)
+ *   (y_i, y_j) <- (y_i cos a - y_j sin a, y_j cos a + y_i sin a)
+ * over the pairs (i, j = i + R/2), or (2i, 2i + 1) if `interleaved`, of the
+ * first R dimensions, a = position * inv_freq[i] (inv_freq [R/2] fp32, taken
+ * as exact; R = 0: no rotation).  Node i of sequence b has position
+ * len[b] - 1 + depth[b, i] (depth NULL: i).  fp32 inside, rounded once.
+ * q_out [B, T, Hq, D] gets the queries.  Keys and values go to `staged`
+ * [L, 2, B, H, T, D] at node i, or with staged NULL to cache slot
+ * pad + len - 1 + i.  Flagged: len < 1, pad < 0, a slot past S, an index
+ * outside [0, N); and, where the cache is written, a repeated index.
+ * qkv and q_out must not overlap.
+ */
+SPEC_API int spec_append_round(const void *qkv, spec_dtype dt, int B, int T, int Hq, void *kv, int L, int N, int H,
+                      int S, int D, int layer, const int32_t *len, const int32_t *pad, const int32_t *idx,
+                      const int32_t *n_nodes, const int32_t *depth, void *staged, const void *q_weight,
+                      const void *k_weight, float eps, const float *inv_freq, int R, int interleaved,
+                      void *q_out, uint32_t *flags, void *cuda_stream);
+
+/*
+ * The same for packed prompts, or pieces of prompts: sequence b's tokens are
+ * rows cu[b] .. cu[b + 1] - 1 of qkv [M, Hq + 2H, D] (cu [B + 1] int32, not
+ * descending, within [0, M]; rows outside it are left alone), at positions
+ * start[b], start[b] + 1, ... (start NULL: 0).  Keys and values go to slots
+ * pad + position.  A cu that descends anywhere flags every sequence.
+ */
+SPEC_API int spec_append_prompt(const void *qkv, spec_dtype dt, int M, int Hq, void *kv, int L, int N, int H, int S,
+                       int D, int layer, int B, const int32_t *cu, const int32_t *start, const int32_t *pad,
+                       const int32_t *idx, const void *q_weight, const void *k_weight, float eps,
+                       const float *inv_freq, int R, int interleaved, void *q_out, uint32_t *flags,
+                       void *cuda_stream);
+
+/* Workspace of spec_attend_round (does not depend on B or S; 256-byte
+ * aligned, zero-filled before its first use, zero counters after each call). */
+SPEC_API size_t spec_attend_workspace_bytes(int T, int Hq, int H, int D);
+
+/*
+ * Attention of a round: q [B, T, Hq, D] -> out [B, T, Hq, D],
+ *   out = sum_j e^(scale q.k_j) v_j / sum_j e^(scale q.k_j)
+ * over the cached prefix (positions 0 .. len - 2, slots pad ..) and the nodes
+ * a < n_nodes with bit a of tree_mask[b, i] set (tree_mask [B, T] uint64;
+ * NULL: a chain, a <= i).  The nodes' keys and values are read from `staged`,
+ * or with staged NULL from slots pad + len - 1 ..  A query that sees nothing
+ * (len 1, mask 0) gives zeros.  Slots no query of the sequence sees may hold
+ * anything.  T = 1 is plain decoding.  scale > 0.  Statistics and sums are
+ * fp32; the same inputs give the same bits.  q and out must not
+ * overlap.
+ */
+SPEC_API int spec_attend_round(const void *q, spec_dtype dt, int B, int T, int Hq, const void *kv, int L, int N,
+                      int H, int S, int D, int layer, const int32_t *len, const int32_t *pad,
+                      const int32_t *idx, const int32_t *n_nodes, const uint64_t *tree_mask,
+                      const void *staged, float scale, void *out, uint32_t *flags, void *workspace,
+                      size_t workspace_bytes, void *cuda_stream);
+
+/*
+ * Causal attention of packed prompts, or pieces of prompts, over the cache
+ * that spec_append_prompt filled: token i of sequence b (row cu[b] + i of
+ * q [M, Hq, D]) sees positions 0 .. start[b] + i, slots pad ..
+ */
+SPEC_API int spec_attend_prompt(const void *q, spec_dtype dt, int M, int Hq, const void *kv, int L, int N, int H,
+                       int S, int D, int layer, int B, const int32_t *cu, const int32_t *start,
+                       const int32_t *pad, const int32_t *idx, float scale, void *out, uint32_t *flags,
+                       void *cuda_stream);
+
+/* Workspace of spec_verify_tree (256-byte aligned; no initial value). */
+SPEC_API size_t spec_tree_workspace_bytes(int B);
+
+/*
+ * Greedy verification of drafted trees (greedy_commit along a path).  From
+ * the root, the argmax t of the current node's row (lowest index among equal
+ * maxima, NaN above every number) is committed; the walk goes on at the
+ * lowest child that proposed t, and ends when there is none, when
+ * t == eos_id, or when remaining[b] tokens are committed.  A chain gives what
+ * spec_verify_greedy gives.
+ *
+ * target_logits [B, T, V], tokens [B, T] int32 (node 0's is not looked at),
+ * parent [B, T] as in spec_tree_plan; out_tokens [B, T] the committed tokens
+ * and path [B, T] the nodes whose rows they are (path[0] = 0), -1 after the
+ * last; n_emit [B] their number; n_accept [B] those that a child proposed.
+ * Only rows on the path are needed.  A flagged sequence commits nothing
+ * (n_emit = n_accept = 0).
+ */
+SPEC_API int spec_verify_tree(const void *target_logits, spec_dtype dt, int B, int T, int V, const int32_t *tokens,
+                     const int32_t *parent, const int32_t *n_nodes, int32_t eos_id,
+                     const int32_t *remaining, int32_t *out_tokens, int32_t *path, int32_t *n_accept,
+                     int32_t *n_emit, uint32_t *flags, void *workspace, size_t workspace_bytes,
+                     void *cuda_stream);
+
+/*
+ * The accepted path's keys and values, from the staged block
+ * [L, 2, B, H, T, D] to the cache [L, 2, N, H, S, D]: rows path[b, 0 ..
+ * n_emit[b]) of every slab go to slots pad + len - 1 ..  (len, pad: the
+ * round's).  The cache is then as after a round on a chain, ready for
+ * spec_realign_kv or spec_commit_ragged with this n_emit.  Flagged: a count
+ * or path entry outside [0, T], a slot past S, a bad or repeated index.  The
+ * two blocks must not overlap.  B <= 65535.
+ */
+SPEC_API int spec_commit_tree(const void *staged, void *kv, spec_dtype dt, int L, int B, int T, int N, int H, int S,
+                     int D, const int32_t *len, const int32_t *pad, const int32_t *path,
+                     const int32_t *n_emit, const int32_t *idx, uint32_t *flags, void *cuda_stream);
 
 #ifdef __cplusplus
 }

@@ -39,3 +39,18 @@ from .api import (  # noqa: F401
     spec_workspace_bytes,
 )
 from .graph import RoundGraph  # noqa: F401,E402
+from .forward import (  # noqa: F401,E402
+    FLAG_BAD_STATE,
+    FLAG_BAD_TREE,
+    MAX_HEAD_DIM,
+    MAX_NODES,
+    spec_append_prompt,
+    spec_append_round,
+    spec_attend_prompt,
+    spec_attend_round,
+    spec_attend_workspace_bytes,
+    spec_commit_tree,
+    spec_tree_plan,
+    spec_tree_workspace_bytes,
+    spec_verify_tree,
+)

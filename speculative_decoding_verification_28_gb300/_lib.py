@@ -51,6 +51,22 @@ SIGNATURES["spec_repad_gather"] = ([_vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32
 SIGNATURES["spec_unpad_scatter"] = ([_vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
                                      _vp, _vp, _sz, _vp], _i32)
 
+SIGNATURES["spec_tree_plan"] = ([_i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp], _i32)
+SIGNATURES["spec_append_round"] = ([_vp, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
+                                    _vp, _vp, _vp, _vp, _vp, _f32, _vp, _i32, _i32, _vp, _vp, _vp], _i32)
+SIGNATURES["spec_append_prompt"] = ([_vp, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp,
+                                     _vp, _vp, _vp, _vp, _f32, _vp, _i32, _i32, _vp, _vp, _vp], _i32)
+SIGNATURES["spec_attend_workspace_bytes"] = ([_i32, _i32, _i32, _i32], _sz)
+SIGNATURES["spec_attend_round"] = ([_vp, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp,
+                                    _vp, _vp, _vp, _f32, _vp, _vp, _vp, _sz, _vp], _i32)
+SIGNATURES["spec_attend_prompt"] = ([_vp, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp,
+                                     _vp, _vp, _f32, _vp, _vp, _vp], _i32)
+SIGNATURES["spec_tree_workspace_bytes"] = ([_i32], _sz)
+SIGNATURES["spec_verify_tree"] = ([_vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp,
+                                   _vp, _vp, _sz, _vp], _i32)
+SIGNATURES["spec_commit_tree"] = ([_vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
+                                   _vp, _vp], _i32)
+
 _lib = None
 
 

@@ -1,0 +1,300 @@
+// attend_common.cuh -- how attention's work is split over CTAs and joined
+// again, shared by its two kernels (attend_simt.cu, attend_tc.cu).
+//
+// A unit is (sequence, key head, group of query rows); its keys are cut into
+// tiles.  The query rows of a key head are packed token-major: row r is token
+// r / G, query head h * G + r % G, so the G heads that share a key head read
+// its keys once.  A round's tiles are those of the cached prefix and one for
+// the nodes; the tiles of all units, laid end to end, are dealt out in equal
+// contiguous runs to the CTAs.  Every CTA finds its run by itself from the
+// lengths on the device, so no host value and no extra launch is needed, and
+// a ragged batch is as balanced as a uniform one.  A unit cut by a run's end
+// leaves its parts (unnormalised sums, running maximum, weight sum) in the
+// workspace; the last CTA to arrive joins them in part order, so results do
+// not depend on which that was.
+#pragma once
+
+#include "forward.h"
+#include "spec_common.cuh"
+
+namespace spec {
+
+constexpr int kAttendCtas = 152;  // CTAs of a round's launch: one per SM
+constexpr int kMinTiles = 2;      // smallest run worth a CTA of its own
+
+struct Unit {
+    int b, h;
+    int row0, n_rows;      // first query row of the unit within its sequence, and how many
+    Seq seq;
+    int tile, tile_end;    // this CTA's tiles of the unit
+    int n_tiles;           // tiles of the unit
+    int part, n_parts;     // place among the unit's parts
+    int first_cta;         // CTA that has part 0
+};
+
+// tiles of one sequence's unit, and units of the sequence per key head
+struct Shape {
+    int tile_keys;  // keys of a tile
+    int unit_rows;  // query rows of a unit
+    int G;          // query rows of a token
+};
+__device__ __forceinline__ int round_tiles(const Seq &s, const Shape &sh)
+{
+    return (s.prefix + sh.tile_keys - 1) / sh.tile_keys + 1;
+}
+__device__ __forceinline__ int unit_groups(const Seq &s, const Shape &sh)
+{
+    return (int)(((long long)s.n * sh.G + sh.unit_rows - 1) / sh.unit_rows);
+}
+__device__ __forceinline__ long long round_weight(const Seq &s, const Shape &sh, int H)
+{
+    return (long long)H * unit_groups(s, sh) * round_tiles(s, sh);
+}
+
+// The run of this CTA: filled by the whole CTA, read by every role.
+struct Run {
+    long long begin, end;  // tiles, over all sequences
+    long long per;         // tiles of a full run
+    long long seq_begin;   // first tile of sequence b
+    int b;                 // sequence that holds `begin`
+};
+
+// Exclusive prefix of v over the block; total in *total.  s: one value per warp.
+template <int THREADS>
+__device__ long long block_exclusive(long long v, long long *s, long long *total)
+{
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    long long x = v;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const long long o = __shfl_up_sync(0xFFFFFFFFu, x, m);
+        if (lane >= m)
+            x += o;
+    }
+    if (lane == 31)
+        s[w] = x;
+    __syncthreads();
+    long long before = 0, sum = 0;
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) {
+        if (i < w)
+            before += s[i];
+        sum += s[i];
+    }
+    *total = sum;
+    return before + x - v;
+}
+
+// Every thread takes a contiguous range of sequences; s_run is complete after
+// the caller's next __syncthreads.  CTA 0 writes the flags.
+template <int THREADS>
+__device__ void find_run(const AttendArgs &a, const Shape &sh, long long *s_scan, Run *s_run)
+{
+    const int per_thread = (a.seq.B + THREADS - 1) / THREADS;
+    const int b0 = threadIdx.x * per_thread, b1 = min(a.seq.B, b0 + per_thread);
+    long long w = 0;
+    for (int b = b0; b < b1; ++b) {
+        const Seq s = load_seq(a.seq, a.cache.N, a.cache.S, b);
+        w += round_weight(s, sh, a.cache.H);
+        if (blockIdx.x == 0 && a.flags)
+            a.flags[b] = s.ok ? 0u : SPEC_FLAG_BAD_STATE;
+    }
+    long long total;
+    long long at = block_exclusive<THREADS>(w, s_scan, &total);
+    const long long even = (total + gridDim.x - 1) / gridDim.x;
+    const long long per = even < kMinTiles ? kMinTiles : even;
+    const long long begin = per * blockIdx.x;
+    if (threadIdx.x == 0) {
+        s_run->per = per;
+        s_run->begin = begin < total ? begin : total;
+        s_run->end = begin + per < total ? begin + per : total;
+    }
+    if (begin < total && at <= begin && begin < at + w) {  // one thread holds it
+        for (int b = b0; b < b1; ++b) {
+            const long long wb = round_weight(load_seq(a.seq, a.cache.N, a.cache.S, b), sh, a.cache.H);
+            if (begin < at + wb) {
+                s_run->b = b;
+                s_run->seq_begin = at;
+                break;
+            }
+            at += wb;
+        }
+    }
+}
+
+// The units of a run, in order; each role of a CTA walks its own copy.
+struct UnitWalk {
+    const AttendArgs *a;
+    Shape sh;
+    Run run;
+    long long pos;
+    long long weight;
+    int loaded;  // sequence held in `cur`, or -1
+    Seq cur;
+    __device__ UnitWalk(const AttendArgs &args, const Shape &shape, const Run &r)
+        : a(&args), sh(shape), run(r), pos(r.begin), weight(0), loaded(-1)
+    {
+    }
+    __device__ bool next(Unit &u)
+    {
+        if (pos >= run.end)
+            return false;
+        while (true) {
+            if (loaded != run.b) {
+                cur = load_seq(a->seq, a->cache.N, a->cache.S, run.b);
+                weight = round_weight(cur, sh, a->cache.H);
+                loaded = run.b;
+            }
+            if (pos < run.seq_begin + weight)
+                break;
+            run.seq_begin += weight;
+            ++run.b;  // ends: run.end is at most the tiles of all sequences
+        }
+        const int tiles = round_tiles(cur, sh), groups = unit_groups(cur, sh);
+        const long long off = pos - run.seq_begin;
+        const int which = (int)(off / tiles), t0 = (int)(off - (long long)which * tiles);
+        const long long left = run.end - pos;
+        u.b = run.b;
+        u.h = which / groups;
+        u.row0 = (which - u.h * groups) * sh.unit_rows;
+        u.n_rows = min(sh.unit_rows, cur.n * sh.G - u.row0);
+        u.seq = cur;
+        u.tile = t0;
+        u.tile_end = tiles - t0 < left ? tiles : t0 + (int)left;
+        u.n_tiles = tiles;
+        const long long g0 = pos - t0;  // the unit's first tile
+        const long long first = g0 / run.per, last = (g0 + tiles - 1) / run.per;
+        u.first_cta = (int)first;
+        u.n_parts = (int)(last - first) + 1;
+        u.part = (int)((long long)blockIdx.x - first);
+        pos += u.tile_end - t0;
+        return true;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// parts in the workspace
+// ---------------------------------------------------------------------------
+// [counters: one per CTA, zero between calls] [slots: two per CTA, one for the
+// unit that it finishes for others or passes on, one for the unit that starts
+// in it and is cut]; a slot is ROWS x D sums, ROWS maxima (base 2), ROWS sums.
+constexpr size_t kPartHead = 1024;
+static_assert(kAttendCtas * sizeof(int) <= kPartHead, "one counter per CTA");
+template <int ROWS>
+__host__ __device__ inline size_t part_floats(int D)
+{
+    return (size_t)ROWS * D + 2 * ROWS;
+}
+template <int ROWS>
+__device__ __forceinline__ float *part_slot(const AttendArgs &a, int cta, int part)
+{
+    float *slots = reinterpret_cast<float *>(static_cast<char *>(a.ws) + kPartHead);
+    return slots + (size_t)(2 * cta + (part == 0 ? 1 : 0)) * part_floats<ROWS>(a.cache.D);
+}
+__device__ __forceinline__ int *part_counter(const AttendArgs &a, int cta)
+{
+    return static_cast<int *>(a.ws) + cta;
+}
+
+// place of row r of a unit in q and out, in elements
+__device__ __forceinline__ long long row_place(const AttendArgs &a, const Unit &u, int r)
+{
+    const int t = (u.row0 + r) / a.G, g = u.row0 + r - t * a.G;
+    return ((u.seq.tok0 + t) * a.Hq + (long long)u.h * a.G + g) * a.cache.D;
+}
+
+template <typename T>
+__device__ __forceinline__ T round_to(float x);
+template <>
+__device__ __forceinline__ float round_to<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half round_to<__half>(float x) { return __float2half_rn(x); }
+
+// The CTA that covers prompt unit blockIdx.x of key head blockIdx.y: units are
+// numbered from the last sequence's last rows down, so that the longest of a
+// sequence start first.  Every warp finds it from cu; false: no such unit.
+__device__ inline bool prompt_unit(const AttendArgs &a, const Shape &sh, Unit &u)
+{
+    const int lane = threadIdx.x & 31;
+    long long left = blockIdx.x;
+    unsigned broken = 0;
+    int b = -1, which = 0;
+    for (int c = 0; c < a.seq.B; c += 32) {
+        const int i = a.seq.B - 1 - (c + lane);
+        long long groups = 0;
+        bool bad = false;
+        if (i >= 0) {
+            groups = unit_groups(load_seq(a.seq, a.cache.N, a.cache.S, i), sh);
+            bad = a.seq.cu[i + 1] < a.seq.cu[i];
+        }
+        broken |= __ballot_sync(0xFFFFFFFFu, bad);
+        long long x = groups;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const long long o = __shfl_up_sync(0xFFFFFFFFu, x, m);
+            if (lane >= m)
+                x += o;
+        }
+        const unsigned hit = __ballot_sync(0xFFFFFFFFu, left >= 0 && left < x);
+        if (b < 0 && hit) {
+            const int l = __ffs(hit) - 1;
+            b = a.seq.B - 1 - (c + l);
+            which = (int)(__shfl_sync(0xFFFFFFFFu, x, l) - 1 - left);  // last group first
+        }
+        left -= __shfl_sync(0xFFFFFFFFu, x, 31);
+    }
+    if (blockIdx.x == 0 && blockIdx.y == 0 && a.flags)
+        for (int i = threadIdx.x; i < a.seq.B; i += blockDim.x)
+            a.flags[i] = !broken && load_seq(a.seq, a.cache.N, a.cache.S, i).ok ? 0u : SPEC_FLAG_BAD_STATE;
+    if (b < 0 || broken)
+        return false;
+    u.b = b;
+    u.h = blockIdx.y;
+    u.seq = load_seq(a.seq, a.cache.N, a.cache.S, b);
+    u.row0 = which * sh.unit_rows;
+    u.n_rows = min(sh.unit_rows, u.seq.n * sh.G - u.row0);
+    const int keys = u.seq.prefix + (u.row0 + u.n_rows - 1) / sh.G + 1;  // seen by the last row
+    u.tile = 0;
+    u.n_tiles = u.tile_end = (keys + sh.tile_keys - 1) / sh.tile_keys;
+    u.part = u.first_cta = 0;
+    u.n_parts = 1;
+    return true;
+}
+
+// Joins a unit's parts: O = sum 2^(m_p - m) O_p / sum 2^(m_p - m) l_p.  Called
+// by NT threads of which this is thread t, after every part was seen.  A row
+// that no part saw anything for (every l zero) gives zeros.
+template <typename T, int ROWS, int NT>
+__device__ void join_parts(const AttendArgs &a, const Unit &u, int t)
+{
+    const int D = a.cache.D, rows = u.n_rows;
+    T *out = reinterpret_cast<T *>(a.out);
+    const int cols = (D + 3) / 4;
+    for (int w = t; w < rows * cols; w += NT) {
+        const int r = w / cols, c = (w - r * cols) * 4;
+        float m = -INFINITY;
+        for (int p = 0; p < u.n_parts; ++p)
+            m = fmaxf(m, __ldcg(part_slot<ROWS>(a, u.first_cta + p, p) + (size_t)ROWS * D + r));
+        const float m0 = m == -INFINITY ? 0.0f : m;
+        float o[4] = {0, 0, 0, 0}, l = 0.0f;
+        for (int p = 0; p < u.n_parts; ++p) {
+            const float *slot = part_slot<ROWS>(a, u.first_cta + p, p);
+            const float f = exp2f(__ldcg(slot + (size_t)ROWS * D + r) - m0);
+            l = fmaf(f, __ldcg(slot + (size_t)ROWS * D + ROWS + r), l);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < D)
+                    o[e] = fmaf(f, __ldcg(slot + (size_t)r * D + c + e), o[e]);
+        }
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        T *dst = out + row_place(a, u, r) + c;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < D)
+                dst[e] = round_to<T>(o[e] * inv);
+    }
+}
+
+}  // namespace spec
