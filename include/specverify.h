@@ -71,6 +71,8 @@ enum {
 #define SPEC_FLAG_BAD_STATE 16u /* a length, padding, count, index or offset out of range */
 #define SPEC_FLAG_BAD_TREE 32u  /* n_nodes outside [0, T], or a parent that is no earlier node */
 
+#define SPEC_FLAG_TIMEOUT 64u   /* a bounded wait gave up (never expected): output undefined */
+
 /* Values of the realignment error word. */
 #define SPEC_REALIGN_OK 0
 #define SPEC_REALIGN_CAPACITY 1 /* new width W' > S: nothing was moved     */
@@ -405,7 +407,7 @@ SPEC_API int spec_round_sample(const void *target_logits, spec_dtype dt, float t
  * staged in a block staged [L, 2, B, H, T, D] of their own until the accepted
  * path is known, and spec_commit_tree then copies that path to those slots.
  *
- * flags [B] uint32 (or NULL): SPEC_FLAG_BAD_STATE / SPEC_FLAG_BAD_TREE or 0.
+ * flags [B] uint32 (or NULL): SPEC_FLAG_BAD_STATE / _BAD_TREE / _TIMEOUT or 0.
  * ---------------------------------------------------------------------------
  */
 

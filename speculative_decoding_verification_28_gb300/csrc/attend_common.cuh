@@ -22,7 +22,7 @@ namespace spec {
 constexpr int kAttendCtas = 152;  // CTAs of a round's launch: one per SM
 constexpr int kMinTiles = 2;      // smallest run worth a CTA of its own
 
-struct Unit {
+struct AttendUnit {
     int b, h;
     int row0, n_rows;      // first query row of the unit within its sequence, and how many
     Seq seq;
@@ -135,7 +135,7 @@ struct UnitWalk {
         : a(&args), sh(shape), run(r), pos(r.begin), weight(0), loaded(-1)
     {
     }
-    __device__ bool next(Unit &u)
+    __device__ bool next(AttendUnit &u)
     {
         if (pos >= run.end)
             return false;
@@ -197,7 +197,7 @@ __device__ __forceinline__ int *part_counter(const AttendArgs &a, int cta)
 }
 
 // place of row r of a unit in q and out, in elements
-__device__ __forceinline__ long long row_place(const AttendArgs &a, const Unit &u, int r)
+__device__ __forceinline__ long long row_place(const AttendArgs &a, const AttendUnit &u, int r)
 {
     const int t = (u.row0 + r) / a.G, g = u.row0 + r - t * a.G;
     return ((u.seq.tok0 + t) * a.Hq + (long long)u.h * a.G + g) * a.cache.D;
@@ -215,7 +215,7 @@ __device__ __forceinline__ __half round_to<__half>(float x) { return __float2hal
 // The CTA that covers prompt unit blockIdx.x of key head blockIdx.y: units are
 // numbered from the last sequence's last rows down, so that the longest of a
 // sequence start first.  Every warp finds it from cu; false: no such unit.
-__device__ inline bool prompt_unit(const AttendArgs &a, const Shape &sh, Unit &u)
+__device__ inline bool prompt_unit(const AttendArgs &a, const Shape &sh, AttendUnit &u)
 {
     const int lane = threadIdx.x & 31;
     long long left = blockIdx.x;
@@ -267,7 +267,7 @@ __device__ inline bool prompt_unit(const AttendArgs &a, const Shape &sh, Unit &u
 // by NT threads of which this is thread t, after every part was seen.  A row
 // that no part saw anything for (every l zero) gives zeros.
 template <typename T, int ROWS, int NT>
-__device__ void join_parts(const AttendArgs &a, const Unit &u, int t)
+__device__ void join_parts(const AttendArgs &a, const AttendUnit &u, int t)
 {
     const int D = a.cache.D, rows = u.n_rows;
     T *out = reinterpret_cast<T *>(a.out);

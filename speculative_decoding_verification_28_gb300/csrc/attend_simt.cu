@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(AttendArgs a)
     const Shape sh{kSimtKeys, kSimtRows, a.G};
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
 
-    Unit u;
+    AttendUnit u;
     bool have;
     if constexpr (PROMPT) {
         have = prompt_unit(a, sh, u);
@@ -304,14 +304,15 @@ cudaError_t launch_simt_t(const AttendArgs &a, cudaStream_t st)
 
 size_t attend_workspace(int T, int Hq, int H, int D)
 {
-    (void)T;
-    (void)Hq;
-    (void)H;
-    return align256(kPartHead + 2 * kAttendCtas * part_floats<kSimtRows>(D) * sizeof(float));
+    const size_t simt = align256(kPartHead + 2 * kAttendCtas * part_floats<kSimtRows>(D) * sizeof(float));
+    const size_t tc = D == 64 || D == 128 ? attend_tc_workspace(T, Hq, H, D) : 0;
+    return simt > tc ? simt : tc;
 }
 
 cudaError_t launch_attend(const AttendArgs &a, spec_dtype dt, cudaStream_t st)
 {
+    if (attend_tc_takes(a, dt))
+        return launch_attend_tc(a, dt, st);
     switch (dt) {
     case SPEC_F32:
         return launch_simt_t<float>(a, st);
