@@ -462,7 +462,9 @@ SPEC_API int spec_append_prompt(const void *qkv, spec_dtype dt, int M, int Hq, v
                        void *cuda_stream);
 
 /* Workspace of spec_attend_round (does not depend on B or S; 256-byte
- * aligned, zero-filled before its first use, zero counters after each call). */
+ * aligned; its first SPEC_ATTEND_ZERO bytes zero before its first use, and
+ * again after each call). */
+#define SPEC_ATTEND_ZERO 1024
 SPEC_API size_t spec_attend_workspace_bytes(int T, int Hq, int H, int D);
 
 /*
@@ -508,8 +510,8 @@ SPEC_API size_t spec_tree_workspace_bytes(int B);
  * parent [B, T] as in spec_tree_plan; out_tokens [B, T] the committed tokens
  * and path [B, T] the nodes whose rows they are (path[0] = 0), -1 after the
  * last; n_emit [B] their number; n_accept [B] those that a child proposed.
- * Only rows on the path are needed.  A flagged sequence commits nothing
- * (n_emit = n_accept = 0).
+ * Only rows on the path are read.  A flagged sequence commits nothing
+ * (n_emit = n_accept = 0).  B <= 65535.
  */
 SPEC_API int spec_verify_tree(const void *target_logits, spec_dtype dt, int B, int T, int V, const int32_t *tokens,
                      const int32_t *parent, const int32_t *n_nodes, int32_t eos_id,

@@ -40,6 +40,7 @@ from .api import (  # noqa: F401
 )
 from .graph import RoundGraph  # noqa: F401,E402
 from .forward import (  # noqa: F401,E402
+    ATTEND_ZERO,
     FLAG_BAD_STATE,
     FLAG_BAD_TREE,
     MAX_HEAD_DIM,

@@ -269,7 +269,7 @@ int spec_verify_tree(const void *target_logits, spec_dtype dt, int B, int T, int
         return SPEC_EDTYPE;
     if (B == 0)
         return SPEC_OK;
-    if (!target_logits || !tokens || !parent || !out_tokens || !path || !n_accept || !n_emit)
+    if (!target_logits || !tokens || !parent || !out_tokens || !path || !n_accept || !n_emit || B > 65535)
         return SPEC_EINVAL;
     if (!aligned(target_logits, dtype_bytes(dt)) || !int_arrays_ok(tokens, parent, n_nodes, remaining, out_tokens) ||
         !int_arrays_ok(path, n_accept, n_emit, flags, nullptr))

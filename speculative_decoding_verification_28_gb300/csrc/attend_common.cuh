@@ -178,7 +178,7 @@ struct UnitWalk {
 // [counters: one per CTA, zero between calls] [slots: two per CTA, one for the
 // unit that it finishes for others or passes on, one for the unit that starts
 // in it and is cut]; a slot is ROWS x D sums, ROWS maxima (base 2), ROWS sums.
-constexpr size_t kPartHead = 1024;
+constexpr size_t kPartHead = SPEC_ATTEND_ZERO;
 static_assert(kAttendCtas * sizeof(int) <= kPartHead, "one counter per CTA");
 template <int ROWS>
 __host__ __device__ inline size_t part_floats(int D)

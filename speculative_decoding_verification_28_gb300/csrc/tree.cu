@@ -75,28 +75,97 @@ cudaError_t launch_tree_plan(int B, int T, const int32_t *parent, const int32_t 
 // greedy verification
 // ---------------------------------------------------------------------------
 constexpr int kTreeThreads = 256;
+constexpr int kTreeCluster = 8;       // most CTAs of a sequence
+constexpr int kTreeMinChunk = 2048;   // fewest elements of a row worth a CTA
 
-size_t tree_workspace(int B) { return align256((size_t)(B > 0 ? B : 0) * 8); }
+// per sequence: the CTAs' candidates of a step, for two steps in turn
+size_t tree_workspace(int B) { return align256((size_t)(B > 0 ? B : 0) * 2 * kTreeCluster * 8); }
 
-// argmax key of a row: largest value, lowest index, NaN above all
-template <typename T>
-__device__ uint64_t row_key(const T *row, int lo, int hi)
+__device__ __forceinline__ void cluster_sync()
 {
-    uint64_t key = 0;
-    for (int i = lo + threadIdx.x; i < hi; i += kTreeThreads) {
-        const uint64_t k = argmax_key(Storage<T>::at(row, i), (uint32_t)i);
-        key = k > key ? k : key;
-    }
-    return key;
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// One CTA walks one sequence: the row of the node it stands on, its argmax,
-// the lowest child that proposed that token.
+// argmax key (largest value, lowest index, NaN above all) of elements
+// [lo, hi) of a row, in thread 0.  As in chain verification a vector's
+// elements are looked at only when its NaN-propagating maximum beats the
+// thread's best, and a chunk that holds a NaN is gone over again exactly.
 template <typename T>
-__global__ void __launch_bounds__(kTreeThreads) verify_tree_kernel(TreeArgs a)
+__device__ uint64_t row_key(const T *row, int lo, int hi, uint64_t *s_red)
+{
+    constexpr int VEC = Storage<T>::kVec;
+    constexpr int UNROLL = 8;
+    const ChunkSplit<T> cs(row, lo, hi);
+    const int t = threadIdx.x;
+    float best = -INFINITY;
+    uint32_t bidx = 0xFFFFFFFFu;
+    bool nan = false;
+    auto see = [&](int i) {
+        const float x = Storage<T>::at(row, i);
+        nan |= x != x;
+        if (bidx == 0xFFFFFFFFu || x > best) {
+            best = x;
+            bidx = (uint32_t)i;
+        }
+    };
+    for (int i = lo + t; i < cs.head_end; i += kTreeThreads)  // all of an element-aligned row's chunk at worst
+        see(i);
+    const T *body = row + cs.head_end;
+    for (int base = t; base < cs.nvec; base += UNROLL * kTreeThreads) {
+        uint4 r[UNROLL];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+            if (base + u * kTreeThreads < cs.nvec)
+                r[u] = ld_stream16(body + (size_t)(base + u * kTreeThreads) * VEC);
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int vi = base + u * kTreeThreads;
+            if (vi >= cs.nvec)
+                break;
+            const float vm = vec_max<T>(r[u]);
+            nan |= vm != vm;
+            if (bidx == 0xFFFFFFFFu || vm > best) {
+                float f[VEC];
+                Storage<T>::unpack(r[u], f);
+                int e = 0;
+#pragma unroll
+                for (int q = VEC - 1; q >= 0; --q)
+                    e = f[q] == vm ? q : e;
+                best = vm;
+                bidx = (uint32_t)(cs.head_end + vi * VEC + e);
+            }
+        }
+    }
+    for (int i = cs.tail_beg + t; i < hi; i += kTreeThreads)
+        see(i);
+    uint64_t key = bidx == 0xFFFFFFFFu ? 0 : argmax_key(best, bidx);
+    if (__syncthreads_or(nan)) {
+        key = 0;
+        for (int i = lo + t; i < hi; i += kTreeThreads) {
+            const uint64_t k = argmax_key(Storage<T>::at(row, i), (uint32_t)i);
+            key = k > key ? k : key;
+        }
+    }
+    return block_max_u64_to0(key, s_red);
+}
+
+// A cluster walks one sequence.  Each step reads one row, the node's it
+// stands on, a chunk to a CTA; the CTAs' candidates meet in global memory
+// across one cluster barrier, and every CTA then knows the argmax and with it
+// the next node.  So only the rows of the path are read (V * sizeof(T) bytes
+// each, HBM), and a step costs a load, a reduction and the barrier: with few
+// sequences that latency times the longest path is the call's time.
+// Two candidate slots in turn are enough: a CTA writes a slot again only
+// after the barrier of the step between, which every CTA reaches after
+// reading it.
+template <typename T>
+__global__ void __launch_bounds__(kTreeThreads) verify_tree_kernel(TreeArgs a, int chunk)
 {
     __shared__ uint64_t s_red[kTreeThreads / 32];
-    const int b = blockIdx.x, lane = threadIdx.x & 31;
+    const int b = blockIdx.y, rank = blockIdx.x, n_cta = gridDim.x, lane = threadIdx.x & 31;
+    uint64_t *cand = static_cast<uint64_t *>(a.ws) + (size_t)b * 2 * kTreeCluster;
     const int n = a.n_nodes ? a.n_nodes[b] : a.T;
     const int rem = a.remaining ? a.remaining[b] : 0x7FFFFFFF;
     bool ok = n >= 0 && n <= a.T;
@@ -113,10 +182,22 @@ __global__ void __launch_bounds__(kTreeThreads) verify_tree_kernel(TreeArgs a)
     ok = __all_sync(0xFFFFFFFFu, ok);
     int emit = 0, accept = 0, at = 0;
     int out_t[2] = {-1, -1}, out_p[2] = {-1, -1};  // entry lane + 32 s
-    bool live = ok && n > 0 && rem > 0;
+    bool live = ok && n > 0 && rem > 0;  // the same in every thread of the cluster
+    const int lo = rank * chunk, hi = min(a.V, lo + chunk);
     while (live) {
         const T *row = reinterpret_cast<const T *>(a.logits) + ((size_t)b * a.T + at) * a.V;
-        const int t = (int)key_index(block_max_u64(row_key<T>(row, 0, a.V), s_red));
+        const uint64_t mine = lo < hi ? row_key<T>(row, lo, hi, s_red) : 0;
+        uint64_t *slot = cand + (emit & 1) * kTreeCluster;
+        if (threadIdx.x == 0)
+            __stcg(slot + rank, mine);
+        cluster_sync();
+        uint64_t key = lane < n_cta ? __ldcg(slot + lane) : 0;
+#pragma unroll
+        for (int m = kTreeCluster / 2; m > 0; m >>= 1) {
+            const uint64_t o = shfl_xor_u64(key, m);
+            key = o > key ? o : key;
+        }
+        const int t = (int)__shfl_sync(0xFFFFFFFFu, key_index(key), 0);
 #pragma unroll
         for (int s = 0; s < 2; ++s)
             if (emit == lane + 32 * s) {
@@ -124,14 +205,14 @@ __global__ void __launch_bounds__(kTreeThreads) verify_tree_kernel(TreeArgs a)
                 out_p[s] = at;
             }
         ++emit;
-        const unsigned lo = __ballot_sync(0xFFFFFFFFu, up[0] == at && tok[0] == t);
-        const unsigned hi = __ballot_sync(0xFFFFFFFFu, up[1] == at && tok[1] == t);
-        const int child = lo ? __ffs(lo) - 1 : hi ? __ffs(hi) + 31 : -1;
+        const unsigned l32 = __ballot_sync(0xFFFFFFFFu, up[0] == at && tok[0] == t);
+        const unsigned h32 = __ballot_sync(0xFFFFFFFFu, up[1] == at && tok[1] == t);
+        const int child = l32 ? __ffs(l32) - 1 : h32 ? __ffs(h32) + 31 : -1;
         accept += child >= 0;
         live = child >= 0 && emit < rem && !(a.eos >= 0 && t == a.eos);
         at = child;
     }
-    if (threadIdx.x < 32) {
+    if (rank == 0 && threadIdx.x < 32) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const int i = lane + 32 * s;
@@ -151,18 +232,33 @@ __global__ void __launch_bounds__(kTreeThreads) verify_tree_kernel(TreeArgs a)
 
 cudaError_t launch_verify_tree(const TreeArgs &a, spec_dtype dt, cudaStream_t st)
 {
+    int c = kTreeCluster;
+    while (c > 1 && (long long)c * kTreeMinChunk > a.V)
+        c /= 2;
+    const int chunk = ((a.V + c - 1) / c + 63) & ~63;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)c;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)c, (unsigned)a.B);
+    cfg.blockDim = dim3(kTreeThreads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaError_t e;
     switch (dt) {
     case SPEC_F32:
-        verify_tree_kernel<float><<<(unsigned)a.B, kTreeThreads, 0, st>>>(a);
+        e = cudaLaunchKernelEx(&cfg, verify_tree_kernel<float>, a, chunk);
         break;
     case SPEC_BF16:
-        verify_tree_kernel<__nv_bfloat16><<<(unsigned)a.B, kTreeThreads, 0, st>>>(a);
+        e = cudaLaunchKernelEx(&cfg, verify_tree_kernel<__nv_bfloat16>, a, chunk);
         break;
     default:
-        verify_tree_kernel<__half><<<(unsigned)a.B, kTreeThreads, 0, st>>>(a);
+        e = cudaLaunchKernelEx(&cfg, verify_tree_kernel<__half>, a, chunk);
         break;
     }
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------

@@ -14,7 +14,6 @@ so captured graphs share none and may be replayed side by side.
 from __future__ import annotations
 
 import functools
-import math
 
 import torch
 
@@ -24,10 +23,10 @@ from .api import _DT, _check, _need
 FLAG_BAD_STATE, FLAG_BAD_TREE = 16, 32
 MAX_NODES = 64
 MAX_HEAD_DIM = 256
+ATTEND_ZERO = 1024
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent from builds without CUDA
 
 
 def _streamed(fn):
@@ -44,49 +43,62 @@ def _streamed(fn):
     return call
 
 
-class _On:
-    """The current stream of the tensors' device, with that device current."""
+def _call(fn, dev, *args):
+    """fn(*args, the current stream of dev), with dev the current device."""
+    if torch.cuda.current_device() == dev.index:
+        rc = fn(*args, _raw_stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev.index))
+    if rc:
+        _check(rc)
 
-    __slots__ = ("stream", "guard")
 
-    def __init__(self, device):
-        self.stream = torch.cuda.current_stream(device)
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _at(t, dtype, name, dev, shape):
+    """Address of a tensor that is what it has to be (None: null)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _need(t, dtype, name, dev, shape)  # says what is wrong
+    return t.data_ptr()
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.stream.cuda_stream
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _out(t, shape, dtype, dev, name):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _at(t, dtype, name, dev, shape)
+    return t
 
 
 _scratch = {}
 
 
-def _ws(given, kind, nbytes, device, stream, zero):
-    """Scratch of at least nbytes for the current stream, cleared when new if
-    the kernel needs it."""
+def _ws(given, kind, nbytes, device, head):
+    """Scratch of at least nbytes for the current stream; when new, its first
+    `head` bytes are cleared."""
     if given is not None:
         buf = getattr(given, "buf", given)
         _need(buf, torch.uint8, "workspace", device)
         return buf
-    make = torch.zeros if zero else torch.empty
-    if torch.cuda.is_current_stream_capturing():
-        return make(nbytes, dtype=torch.uint8, device=device)
-    key = kind, device.index, stream.cuda_stream
-    buf = _scratch.get(key)
-    if buf is None or buf.numel() < nbytes:
-        buf = _scratch[key] = make(nbytes, dtype=torch.uint8, device=device)
+    capturing = torch.cuda.is_current_stream_capturing()
+    if not capturing:
+        key = kind, device.index, _raw_stream(device.index)
+        buf = _scratch.get(key)
+        if buf is not None and buf.numel() >= nbytes:
+            return buf
+    buf = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if head:
+        buf[:head].zero_()
+    if not capturing:
+        _scratch[key] = buf
     return buf
 
 
 def _cache(kv, layer):
     if kv.dim() != 6 or kv.shape[1] != 2:
         raise ValueError("kv must be [L, 2, N, H, S, D]")
-    _need(kv, None, "kv")
+    if not kv.is_cuda or not kv.is_contiguous():
+        _need(kv, None, "kv")
     if kv.dtype not in _DT:
         raise ValueError(f"unsupported kv dtype {kv.dtype}")
     L, _, N, H, S, D = kv.shape
@@ -95,17 +107,13 @@ def _cache(kv, layer):
     return kv.device, L, N, H, S, D
 
 
-def _out(t, shape, dtype, dev, name):
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need(t, dtype, name, dev, shape)
-    return t
-
-
 def _rows(idx, B, N, dev):
-    _need(idx, torch.int32, "idx", dev, (B,))
     if idx is None and B > N:
         raise ValueError(f"{B} sequences in a cache of {N} rows: pass idx")
+    return _at(idx, _I32, "idx", dev, (B,))
+
+
+_I32 = torch.int32
 
 
 @_streamed
@@ -114,31 +122,30 @@ def spec_tree_plan(parent, n_nodes=None, mask=None, depth=None, flags=None):
     flags [B] int32)."""
     B, T = parent.shape
     dev = parent.device
-    _need(parent, torch.int32, "parent", dev)
-    _need(n_nodes, torch.int32, "n_nodes", dev, (B,))
+    _need(parent, _I32, "parent", dev)
+    n = _at(n_nodes, _I32, "n_nodes", dev, (B,))
     mask = _out(mask, (B, T), torch.int64, dev, "mask")
-    depth = _out(depth, (B, T), torch.int32, dev, "depth")
-    flags = _out(flags, (B,), torch.int32, dev, "flags")
-    with _On(dev) as st:
-        _check(_lib.load().spec_tree_plan(B, T, _ptr(parent), _ptr(n_nodes), _ptr(mask), _ptr(depth), _ptr(flags), st))
+    depth = _out(depth, (B, T), _I32, dev, "depth")
+    flags = _out(flags, (B,), _I32, dev, "flags")
+    _call(_lib.load().spec_tree_plan, dev, B, T, parent.data_ptr(), n, mask.data_ptr(), depth.data_ptr(),
+          flags.data_ptr())
     return mask, depth, flags
 
 
 def _append_common(qkv, kv, layer, inv_freq, q_weight, k_weight, lead):
     dev, L, N, H, S, D = _cache(kv, layer)
-    _need(qkv, kv.dtype, "qkv", dev)
-    heads = qkv.shape[-2]
-    if qkv.dim() != lead + 2 or qkv.shape[-1] != D or heads <= 2 * H:
+    dt = kv.dtype
+    shape = qkv.shape
+    if len(shape) != lead + 2 or shape[-1] != D or shape[-2] <= 2 * H:
         raise ValueError(f"qkv must end in [Hq + 2 * {H}, {D}]")
-    for w, nm in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        _need(w, kv.dtype, nm, dev, (D,))
-    R = 0
+    inv, R = None, 0
     if inv_freq is not None:
         _need(inv_freq, torch.float32, "inv_freq", dev)
-        R = 2 * inv_freq.numel()
+        inv, R = inv_freq.data_ptr(), 2 * inv_freq.numel()
         if R > D:
             raise ValueError(f"inv_freq turns {R} of {D} dimensions")
-    return dev, (L, N, H, S, D), heads - 2 * H, R
+    return (dev, dt, (L, N, H, S, D), shape[-2] - 2 * H, _at(qkv, dt, "qkv", dev, shape),
+            _at(q_weight, dt, "q_weight", dev, (D,)), _at(k_weight, dt, "k_weight", dev, (D,)), inv, R)
 
 
 @_streamed
@@ -148,21 +155,16 @@ def spec_append_round(qkv, kv, layer, length, pad, inv_freq, q_weight=None, k_we
     and keys, rotation, keys and values to the cache kv [L, 2, N, H, S, D] (or
     to staged [L, 2, B, H, T, D]).  pad None: 0.
     -> (q_out [B, T, Hq, D], flags [B] int32)."""
-    dev, (L, N, H, S, D), Hq, R = _append_common(qkv, kv, layer, inv_freq, q_weight, k_weight, 2)
+    dev, dt, (L, N, H, S, D), Hq, x, qw, kw, inv, R = _append_common(qkv, kv, layer, inv_freq, q_weight, k_weight, 2)
     B, T = qkv.shape[:2]
-    _need(length, torch.int32, "length", dev, (B,))
-    _need(pad, torch.int32, "pad", dev, (B,))
-    _need(n_nodes, torch.int32, "n_nodes", dev, (B,))
-    _need(depth, torch.int32, "depth", dev, (B, T))
-    _need(staged, kv.dtype, "staged", dev, (L, 2, B, H, T, D))
-    _rows(idx, B, N, dev)
-    q_out = _out(q_out, (B, T, Hq, D), kv.dtype, dev, "q_out")
-    flags = _out(flags, (B,), torch.int32, dev, "flags")
-    with _On(dev) as st:
-        _check(_lib.load().spec_append_round(
-            _ptr(qkv), _DT[kv.dtype], B, T, Hq, _ptr(kv), L, N, H, S, D, layer, _ptr(length), _ptr(pad), _ptr(idx),
-            _ptr(n_nodes), _ptr(depth), _ptr(staged), _ptr(q_weight), _ptr(k_weight), eps, _ptr(inv_freq), R,
-            1 if interleaved else 0, _ptr(q_out), _ptr(flags), st))
+    rows = B,
+    q_out = _out(q_out, (B, T, Hq, D), dt, dev, "q_out")
+    flags = _out(flags, rows, _I32, dev, "flags")
+    _call(_lib.load().spec_append_round, dev, x, _DT[dt], B, T, Hq, kv.data_ptr(), L, N, H, S, D, layer,
+          _at(length, _I32, "length", dev, rows), _at(pad, _I32, "pad", dev, rows), _rows(idx, B, N, dev),
+          _at(n_nodes, _I32, "n_nodes", dev, rows), _at(depth, _I32, "depth", dev, (B, T)),
+          _at(staged, dt, "staged", dev, (L, 2, B, H, T, D)), qw, kw, eps, inv, R, 1 if interleaved else 0,
+          q_out.data_ptr(), flags.data_ptr())
     return q_out, flags
 
 
@@ -172,19 +174,14 @@ def spec_append_prompt(qkv, kv, layer, cu, pad, inv_freq, q_weight=None, k_weigh
     """spec_append_round for packed prompts: qkv [M, Hq + 2H, D], sequence b
     in rows cu[b] .. cu[b + 1] - 1 at positions start[b] ..
     -> (q_out [M, Hq, D], flags [B] int32)."""
-    dev, (L, N, H, S, D), Hq, R = _append_common(qkv, kv, layer, inv_freq, q_weight, k_weight, 1)
+    dev, dt, (L, N, H, S, D), Hq, x, qw, kw, inv, R = _append_common(qkv, kv, layer, inv_freq, q_weight, k_weight, 1)
     M, B = qkv.shape[0], cu.shape[0] - 1
-    _need(cu, torch.int32, "cu", dev, (B + 1,))
-    _need(pad, torch.int32, "pad", dev, (B,))
-    _need(start, torch.int32, "start", dev, (B,))
-    _rows(idx, B, N, dev)
-    q_out = _out(q_out, (M, Hq, D), kv.dtype, dev, "q_out")
-    flags = _out(flags, (B,), torch.int32, dev, "flags")
-    with _On(dev) as st:
-        _check(_lib.load().spec_append_prompt(
-            _ptr(qkv), _DT[kv.dtype], M, Hq, _ptr(kv), L, N, H, S, D, layer, B, _ptr(cu), _ptr(start), _ptr(pad),
-            _ptr(idx), _ptr(q_weight), _ptr(k_weight), eps, _ptr(inv_freq), R, 1 if interleaved else 0, _ptr(q_out),
-            _ptr(flags), st))
+    rows = B,
+    q_out = _out(q_out, (M, Hq, D), dt, dev, "q_out")
+    flags = _out(flags, rows, _I32, dev, "flags")
+    _call(_lib.load().spec_append_prompt, dev, x, _DT[dt], M, Hq, kv.data_ptr(), L, N, H, S, D, layer, B,
+          _at(cu, _I32, "cu", dev, (B + 1,)), _at(start, _I32, "start", dev, rows), _at(pad, _I32, "pad", dev, rows),
+          _rows(idx, B, N, dev), qw, kw, eps, inv, R, 1 if interleaved else 0, q_out.data_ptr(), flags.data_ptr())
     return q_out, flags
 
 
@@ -197,29 +194,23 @@ def spec_attend_round(q, kv, layer, length, pad, tree_mask=None, n_nodes=None, i
                       out=None, flags=None, workspace=None):
     """Attention of a round's queries q [B, T, Hq, D] over the cached prefix
     and the nodes each may see (tree_mask [B, T] int64 bit sets; None: a
-    chain).  scale None: 1 / sqrt(D).  workspace: zero-filled uint8 tensor of
-    spec_attend_workspace_bytes.  -> (out [B, T, Hq, D], flags [B] int32)."""
+    chain).  scale None: 1 / sqrt(D).  workspace: uint8 tensor of
+    spec_attend_workspace_bytes, its first ATTEND_ZERO bytes zero.  -> (out [B, T, Hq, D], flags [B] int32)."""
     dev, L, N, H, S, D = _cache(kv, layer)
-    _need(q, kv.dtype, "q", dev)
-    B, T, Hq, Dq = q.shape
+    dt, shape = kv.dtype, q.shape
+    B, T, Hq, Dq = shape
     if Dq != D:
         raise ValueError(f"q must be [B, T, Hq, {D}]")
-    _need(length, torch.int32, "length", dev, (B,))
-    _need(pad, torch.int32, "pad", dev, (B,))
-    _need(n_nodes, torch.int32, "n_nodes", dev, (B,))
-    _need(tree_mask, torch.int64, "tree_mask", dev, (B, T))
-    _need(staged, kv.dtype, "staged", dev, (L, 2, B, H, T, D))
-    _rows(idx, B, N, dev)
-    out = _out(out, (B, T, Hq, D), kv.dtype, dev, "out")
-    flags = _out(flags, (B,), torch.int32, dev, "flags")
+    rows = B,
+    out = _out(out, shape, dt, dev, "out")
+    flags = _out(flags, rows, _I32, dev, "flags")
     lib = _lib.load()
-    on = _On(dev)
-    with on as st:
-        ws = _ws(workspace, "attend", lib.spec_attend_workspace_bytes(T, Hq, H, D), dev, on.stream, True)
-        _check(lib.spec_attend_round(
-            _ptr(q), _DT[kv.dtype], B, T, Hq, _ptr(kv), L, N, H, S, D, layer, _ptr(length), _ptr(pad), _ptr(idx),
-            _ptr(n_nodes), _ptr(tree_mask), _ptr(staged), 1.0 / math.sqrt(D) if scale is None else scale, _ptr(out),
-            _ptr(flags), _ptr(ws), ws.numel(), st))
+    ws = _ws(workspace, "attend", lib.spec_attend_workspace_bytes(T, Hq, H, D), dev, ATTEND_ZERO)
+    _call(lib.spec_attend_round, dev, _at(q, dt, "q", dev, shape), _DT[dt], B, T, Hq, kv.data_ptr(), L, N, H, S, D,
+          layer, _at(length, _I32, "length", dev, rows), _at(pad, _I32, "pad", dev, rows), _rows(idx, B, N, dev),
+          _at(n_nodes, _I32, "n_nodes", dev, rows), _at(tree_mask, torch.int64, "tree_mask", dev, (B, T)),
+          _at(staged, dt, "staged", dev, (L, 2, B, H, T, D)), D ** -0.5 if scale is None else scale, out.data_ptr(),
+          flags.data_ptr(), ws.data_ptr(), ws.numel())
     return out, flags
 
 
@@ -228,21 +219,18 @@ def spec_attend_prompt(q, kv, layer, cu, pad, start=None, idx=None, scale=None, 
     """Causal attention of packed prompts q [M, Hq, D] over the cache that
     spec_append_prompt filled.  -> (out [M, Hq, D], flags [B] int32)."""
     dev, L, N, H, S, D = _cache(kv, layer)
-    _need(q, kv.dtype, "q", dev)
-    M, Hq, Dq = q.shape
+    dt, shape = kv.dtype, q.shape
+    M, Hq, Dq = shape
     if Dq != D:
         raise ValueError(f"q must be [M, Hq, {D}]")
     B = cu.shape[0] - 1
-    _need(cu, torch.int32, "cu", dev, (B + 1,))
-    _need(pad, torch.int32, "pad", dev, (B,))
-    _need(start, torch.int32, "start", dev, (B,))
-    _rows(idx, B, N, dev)
-    out = _out(out, (M, Hq, D), kv.dtype, dev, "out")
-    flags = _out(flags, (B,), torch.int32, dev, "flags")
-    with _On(dev) as st:
-        _check(_lib.load().spec_attend_prompt(
-            _ptr(q), _DT[kv.dtype], M, Hq, _ptr(kv), L, N, H, S, D, layer, B, _ptr(cu), _ptr(start), _ptr(pad),
-            _ptr(idx), 1.0 / math.sqrt(D) if scale is None else scale, _ptr(out), _ptr(flags), st))
+    rows = B,
+    out = _out(out, shape, dt, dev, "out")
+    flags = _out(flags, rows, _I32, dev, "flags")
+    _call(_lib.load().spec_attend_prompt, dev, _at(q, dt, "q", dev, shape), _DT[dt], M, Hq, kv.data_ptr(), L, N, H, S,
+          D, layer, B, _at(cu, _I32, "cu", dev, (B + 1,)), _at(start, _I32, "start", dev, rows),
+          _at(pad, _I32, "pad", dev, rows), _rows(idx, B, N, dev), D ** -0.5 if scale is None else scale,
+          out.data_ptr(), flags.data_ptr())
     return out, flags
 
 
@@ -257,27 +245,28 @@ def spec_verify_tree(target_logits, tokens, parent, n_nodes=None, eos_id=-1, rem
     and parent [B, T] int32 -> (out_tokens [B, T], path [B, T], n_accept [B],
     n_emit [B], flags [B]) int32."""
     B, T, V = target_logits.shape
-    dev = target_logits.device
+    dev, dt = target_logits.device, target_logits.dtype
     _need(target_logits, None, "target_logits", dev)
-    if target_logits.dtype not in _DT:
-        raise ValueError(f"unsupported logits dtype {target_logits.dtype}")
-    _need(tokens, torch.int32, "tokens", dev, (B, T))
-    _need(parent, torch.int32, "parent", dev, (B, T))
-    _need(n_nodes, torch.int32, "n_nodes", dev, (B,))
-    _need(remaining, torch.int32, "remaining", dev, (B,))
-    out_tokens = _out(out_tokens, (B, T), torch.int32, dev, "out_tokens")
-    path = _out(path, (B, T), torch.int32, dev, "path")
-    n_accept = _out(n_accept, (B,), torch.int32, dev, "n_accept")
-    n_emit = _out(n_emit, (B,), torch.int32, dev, "n_emit")
-    flags = _out(flags, (B,), torch.int32, dev, "flags")
+    if dt not in _DT:
+        raise ValueError(f"unsupported logits dtype {dt}")
+    rows, nodes = (B,), (B, T)
+    if out_tokens is None and path is None and n_accept is None and n_emit is None and flags is None:
+        # one block for the five outputs
+        block = torch.empty(B * (2 * T + 3), dtype=_I32, device=dev)
+        out_tokens, path, n_accept, n_emit, flags = block.split((B * T, B * T, B, B, B))
+        out_tokens, path = out_tokens.view(nodes), path.view(nodes)
+    else:
+        out_tokens = _out(out_tokens, nodes, _I32, dev, "out_tokens")
+        path = _out(path, nodes, _I32, dev, "path")
+        n_accept = _out(n_accept, rows, _I32, dev, "n_accept")
+        n_emit = _out(n_emit, rows, _I32, dev, "n_emit")
+        flags = _out(flags, rows, _I32, dev, "flags")
     lib = _lib.load()
-    on = _On(dev)
-    with on as st:
-        ws = _ws(workspace, "tree", max(256, lib.spec_tree_workspace_bytes(B)), dev, on.stream, False)
-        _check(lib.spec_verify_tree(
-            _ptr(target_logits), _DT[target_logits.dtype], B, T, V, _ptr(tokens), _ptr(parent), _ptr(n_nodes),
-            int(eos_id), _ptr(remaining), _ptr(out_tokens), _ptr(path), _ptr(n_accept), _ptr(n_emit), _ptr(flags),
-            _ptr(ws), ws.numel(), st))
+    ws = _ws(workspace, "tree", max(256, lib.spec_tree_workspace_bytes(B)), dev, 0)
+    _call(lib.spec_verify_tree, dev, target_logits.data_ptr(), _DT[dt], B, T, V, _at(tokens, _I32, "tokens", dev, nodes),
+          _at(parent, _I32, "parent", dev, nodes), _at(n_nodes, _I32, "n_nodes", dev, rows), int(eos_id),
+          _at(remaining, _I32, "remaining", dev, rows), out_tokens.data_ptr(), path.data_ptr(), n_accept.data_ptr(),
+          n_emit.data_ptr(), flags.data_ptr(), ws.data_ptr(), ws.numel())
     return out_tokens, path, n_accept, n_emit, flags
 
 
@@ -287,16 +276,12 @@ def spec_commit_tree(staged, kv, length, pad, path, n_emit, idx=None, flags=None
     slots in kv [L, 2, N, H, S, D].  length, pad: the round's.
     -> flags [B] int32."""
     dev, L, N, H, S, D = _cache(kv, 0)
+    dt = kv.dtype
     B, T = path.shape
-    _need(staged, kv.dtype, "staged", dev, (L, 2, B, H, T, D))
-    _need(length, torch.int32, "length", dev, (B,))
-    _need(pad, torch.int32, "pad", dev, (B,))
-    _need(path, torch.int32, "path", dev)
-    _need(n_emit, torch.int32, "n_emit", dev, (B,))
-    _rows(idx, B, N, dev)
-    flags = _out(flags, (B,), torch.int32, dev, "flags")
-    with _On(dev) as st:
-        _check(_lib.load().spec_commit_tree(
-            _ptr(staged), _ptr(kv), _DT[kv.dtype], L, B, T, N, H, S, D, _ptr(length), _ptr(pad), _ptr(path),
-            _ptr(n_emit), _ptr(idx), _ptr(flags), st))
+    rows = B,
+    flags = _out(flags, rows, _I32, dev, "flags")
+    _call(_lib.load().spec_commit_tree, dev, _at(staged, dt, "staged", dev, (L, 2, B, H, T, D)), kv.data_ptr(), _DT[dt],
+          L, B, T, N, H, S, D, _at(length, _I32, "length", dev, rows), _at(pad, _I32, "pad", dev, rows),
+          _at(path, _I32, "path", dev, (B, T)), _at(n_emit, _I32, "n_emit", dev, rows), _rows(idx, B, N, dev),
+          flags.data_ptr())
     return flags
