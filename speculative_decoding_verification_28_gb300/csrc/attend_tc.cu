@@ -120,6 +120,18 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *r)
                  : "memory");
 }
 
+// the loads so far have arrived; r are registers of theirs
+__device__ __forceinline__ void tc_loaded(uint32_t *r)
+{
+    tc_wait_ld();
+    tc_pin<32>(r);
+}
+__device__ __forceinline__ void tc_load(uint32_t addr, uint32_t *r)
+{
+    tc_ld32(addr, r);
+    tc_loaded(r);
+}
+
 // Shared-memory operand with 128-byte swizzle: rows of 128 bytes, groups of
 // eight rows 1024 bytes apart, panels of 64 elements `panel` bytes apart
 // (used by operands whose long axis is not the summed one).
@@ -127,6 +139,57 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t panel)
 {
     return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(panel >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
            (1ull << 46) | (2ull << 61);
+}
+
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+__device__ __forceinline__ float max32(const uint32_t *r)
+{
+    float m[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t *x = r + 16 * h;
+        m[h] = __uint_as_float(x[15]);
+#pragma unroll
+        for (int e = 0; e < 14; e += 2)
+            m[h] = max3(m[h], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+        m[h] = fmaxf(m[h], __uint_as_float(x[14]));
+    }
+    return fmaxf(m[0], m[1]);
 }
 
 template <typename T>
@@ -170,6 +233,8 @@ __device__ __forceinline__ uint32_t tc_idesc(int n, bool b_rows_summed)
 // ---------------------------------------------------------------------------
 // shapes
 // ---------------------------------------------------------------------------
+constexpr int kTmemP = 64;  // columns of a score buffer where its weights begin
+
 template <int D, int NT>
 struct TcShape {
     static constexpr int kPanels = D / 64;
@@ -413,7 +478,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
             if (lane == 0) {
                 const int steps = (valid + 15) / 16;
                 for (int c = 0; c < steps; ++c)
-                    mma_ts(d, p + c * 8, operand(v + c * 2048, Sh::kPanel), ideo, add || c > 0);
+                    mma_ts(d, p + kTmemP + c * 8, operand(v + c * 2048, Sh::kPanel), ideo, add || c > 0);
             }
         };
         auto commit = [&](uint64_t *bar) {
@@ -626,43 +691,57 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                 if (busy) {
                     const Tile tl = tile_of<PROMPT>(u, a.G, tile);
                     const uint32_t tm_s = tmem + lanes + x * 128;
+                    // The weights take the upper half of the scores' columns.
+                    // Chunks of 32 columns are weighed from the top down, each
+                    // after the scores that its weights replace, which are
+                    // read a second time where registers did not keep them.
+                    const int lim = PROMPT ? min(tl.valid, u.seq.prefix + tok + 1 - tile * kKeys) : tl.valid;
+                    const bool plain = !tl.nodes && !__any_sync(0xFFFFFFFFu, lim < kKeys);
+                    uint32_t s0[32], s1[32], s2[32];
+                    float mx;
+                    uint64_t bits = 0;
                     const int nch = (tl.valid + 31) / 32;
-                    uint32_t sr[128];
+                    auto masked = [&](uint32_t *v, int k) {
+                        if (tl.nodes) {
+                            const uint32_t w = (uint32_t)(bits >> (32 * k));
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < nch)
-                            tc_ld32(tm_s + 32 * k, sr + 32 * k);
-                    tc_wait_ld();
-                    tc_pin<128>(sr);
-                    float *sc = reinterpret_cast<float *>(sr);
-                    if (tl.nodes) {
-                        uint64_t bits = 0;
-                        if (real)
-                            bits = a.mask ? a.mask[(size_t)u.b * a.seq.T + tok] : (2ull << tok) - 1;
-                        bits &= tl.valid < 64 ? (1ull << tl.valid) - 1 : ~0ull;
+                            for (int e = 0; e < 32; ++e)
+                                if (!(w >> e & 1))
+                                    v[e] = 0xFF800000u;
+                        } else {
 #pragma unroll
-                        for (int k = 0; k < 64; ++k)
-                            if (!(bits >> k & 1))
-                                sc[k] = -INFINITY;
-#pragma unroll
-                        for (int k = 64; k < 128; ++k)
-                            sc[k] = -INFINITY;
+                            for (int e = 0; e < 32; ++e)
+                                if (32 * k + e >= lim)
+                                    v[e] = 0xFF800000u;
+                        }
+                    };
+                    if (plain) {
+                        tc_load(tm_s, s0);
+                        tc_ld32(tm_s + 32, s1);
+                        mx = max32(s0);
+                        tc_loaded(s1);
+                        tc_ld32(tm_s + 64, s2);
+                        mx = fmaxf(mx, max32(s1));
+                        tc_loaded(s2);
+                        tc_ld32(tm_s + 96, s1);
+                        mx = fmaxf(mx, max32(s2));
+                        tc_loaded(s1);
+                        mx = fmaxf(mx, max32(s1));
                     } else {
-                        int lim = tl.valid;
-                        if (PROMPT)
-                            lim = min(lim, u.seq.prefix + tok + 1 - tile * kKeys);
-                        if (__any_sync(0xFFFFFFFFu, lim < kKeys)) {
-#pragma unroll
-                            for (int k = 0; k < 128; ++k)
-                                if (k >= lim)
-                                    sc[k] = -INFINITY;
+                        if (tl.nodes) {
+                            if (real)
+                                bits = a.mask ? a.mask[(size_t)u.b * a.seq.T + tok] : (2ull << tok) - 1;
+                            bits &= tl.valid < 64 ? (1ull << tl.valid) - 1 : ~0ull;
+                        }
+                        mx = -INFINITY;
+#pragma unroll 1
+                        for (int k = 0; k < nch; ++k) {
+                            tc_load(tm_s + 32 * k, s0);
+                            masked(s0, k);
+                            mx = fmaxf(mx, max32(s0));
                         }
                     }
-                    float mx = sc[0];
-#pragma unroll
-                    for (int k = 1; k < 127; k += 2)
-                        mx = fmaxf(mx, fmaxf(sc[k], sc[k + 1]));
-                    mx = fmaxf(mx, sc[127]) * c;
+                    mx *= c;
                     float f = 1.0f;
                     if (tile == u.tile) {
                         m = mx;
@@ -679,35 +758,56 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                         if (!ok)
                             break;
                         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                         for (int k = 0; k < D / 32; ++k) {
-                            uint32_t o[32];
-                            tc_ld32(tm_o + 32 * k, o);
-                            tc_wait_ld();
-                            tc_pin<32>(o);
+                            tc_load(tm_o + 32 * k, s0);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tc_st32(tm_o + 32 * k, o);
+                            for (int e = 0; e < 32; e += 2) {
+                                float x0, x1;
+                                unpair(mul2(pair(__uint_as_float(s0[e]), __uint_as_float(s0[e + 1])), pair(f, f)), x0, x1);
+                                s0[e] = __float_as_uint(x0);
+                                s0[e + 1] = __float_as_uint(x1);
+                            }
+                            tc_st32(tm_o + 32 * k, s0);
                         }
                     }
                     const float m0 = m == -INFINITY ? 0.0f : m;
-                    float sum[4] = {0, 0, 0, 0};
+                    const uint64_t c2 = pair(c, c), m2 = pair(-m0, -m0);
+                    uint64_t sum[2] = {0, 0};
+                    auto weigh32 = [&](const uint32_t *v, int k) {
+                        uint32_t pk[16];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < nch) {
-                            uint32_t pk[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                const float p0 = exp2_sfu(fmaf(sc[32 * k + 2 * e], c, -m0));
-                                const float p1 = exp2_sfu(fmaf(sc[32 * k + 2 * e + 1], c, -m0));
-                                sum[(2 * e) & 3] += p0;
-                                sum[(2 * e + 1) & 3] += p1;
-                                pk[e] = TcType<T>::pack(p0, p1);
-                            }
-                            tc_st16(tm_s + 16 * k, pk);
+                        for (int e = 0; e < 16; ++e) {
+                            float x0, x1;
+                            unpair(fma2(pair(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), c2, m2), x0, x1);
+                            const float p0 = exp2_sfu(x0), p1 = exp2_sfu(x1);
+                            sum[e & 1] = add2(sum[e & 1], pair(p0, p1));
+                            pk[e] = TcType<T>::pack(p0, p1);
                         }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        tc_st16(tm_s + kTmemP + 16 * k, pk);
+                    };
+                    if (plain) {
+                        tc_ld32(tm_s, s0);
+                        weigh32(s1, 3);
+                        tc_loaded(s0);
+                        tc_ld32(tm_s + 32, s1);
+                        weigh32(s2, 2);
+                        tc_loaded(s1);
+                        weigh32(s1, 1);
+                        weigh32(s0, 0);
+                    } else {
+#pragma unroll 1
+                        for (int k = nch - 1; k >= 0; --k) {
+                            tc_load(tm_s + 32 * k, s0);
+                            masked(s0, k);
+                            weigh32(s0, k);
+                        }
+                    }
+                    {
+                        float x0, x1;
+                        unpair(add2(sum[0], sum[1]), x0, x1);
+                        l += x0 + x1;
+                    }
                     tc_wait_st();
                 }
                 if (!seen) {
@@ -741,9 +841,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
 #pragma unroll 1
                     for (int k = 0; k < D / 32; ++k) {
                         uint32_t o[32];
-                        tc_ld32(tm_o + 32 * k, o);
-                        tc_wait_ld();
-                        tc_pin<32>(o);
+                        tc_load(tm_o + 32 * k, o);
                         if (any_odd && real) {
                             // the values taken out of V go where they are seen
                             int g = 0;
