@@ -30,7 +30,8 @@
 namespace spec {
 
 constexpr int kKeys = 128;  // keys of a tile, rows of a query tile
-constexpr int kTcWaitLimit = 2000;  // probes of up to ~1 ms
+constexpr int kTcWaitLimit = 2000;  // probes of up to ~1 ms, after a wait that gave up
+constexpr long long kTcWaitClocks = 4000000000ll;  // about 2 s
 constexpr float kLazy = 8.0f;       // base-2 headroom of the running maximum
 constexpr int kGuardRing = 8;       // units whose guard words may be live at once
 
@@ -50,6 +51,18 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *m, 
                  "%5}], [%6];" ::"r"(dst),
                  "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
                  : "memory");
+}
+// one probe of a phase, without a time of its own to sleep: it wakes sooner
+__device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(smem_addr(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar)
 {
@@ -73,20 +86,39 @@ __device__ __forceinline__ void tc_pin(uint32_t *r)
 }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D = A B (+ D): A and B in shared memory
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+// Shared-memory operand with 128-byte swizzle: rows of 128 bytes, groups of
+// eight rows 1024 bytes apart, panels of 64 elements `panel` bytes apart
+// (used by operands whose long axis is not the summed one).
+// Operand descriptors: the upper word is the same for all, the lower holds
+// the address and the panel step.  Only the elected lane issues (`one`), but
+// the whole warp computes, so that the words stay in uniform registers: built
+// per lane they cost more than the 64 cycles of a 128 x 128 x 16 product.
+constexpr uint32_t kOperandHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t panel) { return (addr >> 4) | ((panel >> 4) << 16); }
+
+__device__ __forceinline__ uint32_t elect_one()
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-                 "l"(a), "l"(b), "r"(idesc), "r"(acc)
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one;
+}
+
+// D = A B (+ D): A and B in shared memory
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
+{
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "mov.b64 x, {%1, %6};\n\tmov.b64 y, {%2, %6};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(one), "n"(kOperandHi)
                  : "memory");
 }
 // A in TMEM
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc)
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
 {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "l"(b), "r"(idesc), "r"(acc)
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "mov.b64 y, {%2, %6};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+                 "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(one), "n"(kOperandHi)
                  : "memory");
 }
 
@@ -130,15 +162,6 @@ __device__ __forceinline__ void tc_load(uint32_t addr, uint32_t *r)
 {
     tc_ld32(addr, r);
     tc_loaded(r);
-}
-
-// Shared-memory operand with 128-byte swizzle: rows of 128 bytes, groups of
-// eight rows 1024 bytes apart, panels of 64 elements `panel` bytes apart
-// (used by operands whose long axis is not the summed one).
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t panel)
-{
-    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(panel >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
 }
 
 // two fp32 operations in one instruction
@@ -388,14 +411,18 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
     // a bounded wait; after one that gave up every role leaves its loop.
     // wait1 is one lane's, wait the whole warp's (its answer is the warp's)
     auto wait1 = [&](uint64_t *bar, uint32_t parity) -> bool {
-        for (int i = 0; i < kTcWaitLimit; ++i) {
-            if (mbar_try_wait(bar, parity))
-                return true;
+        if (mbar_poll(bar, parity))
+            return true;
+        const long long t0 = clock64();
+        while (!mbar_poll(bar, parity)) {
             if (*reinterpret_cast<volatile int *>(&s.abort))
                 return false;
+            if (clock64() - t0 > kTcWaitClocks) {
+                *reinterpret_cast<volatile int *>(&s.abort) = 1;
+                return false;
+            }
         }
-        *reinterpret_cast<volatile int *>(&s.abort) = 1;
-        return false;
+        return true;
     };
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
         return __all_sync(0xFFFFFFFFu, wait1(bar, parity));
@@ -465,24 +492,30 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
             ok_ph ^= 1u << sg;
             return wait(&s.v_ok[sg], (ok_ph >> sg & 1) ^ 1);
         };
+        const uint32_t one = elect_one();
         auto score = [&](uint32_t q, uint32_t k, uint32_t d, int valid) {
             const uint32_t ides = tc_idesc<T>(min(kKeys, (valid + 15) & ~15), false);
-            if (lane == 0)
+            const uint32_t qd = operand(q, 16), kd = operand(k, 16);
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
-                    const uint32_t o = (c / 4) * Sh::kPanel + (c % 4) * 32;
-                    mma_ss(d, operand(q + o, 16), operand(k + o, 16), ides, c > 0);
-                }
+            for (int c = 0; c < D / 16; ++c) {
+                const uint32_t o = ((c / 4) * Sh::kPanel + (c % 4) * 32) >> 4;
+                mma_ss(one, d, qd + o, kd + o, ides, c > 0);
+            }
         };
         auto weigh = [&](uint32_t p, uint32_t v, uint32_t d, int valid, bool add) {
-            if (lane == 0) {
-                const int steps = (valid + 15) / 16;
-                for (int c = 0; c < steps; ++c)
-                    mma_ts(d, p + kTmemP + c * 8, operand(v + c * 2048, Sh::kPanel), ideo, add || c > 0);
+            const uint32_t vd = operand(v, Sh::kPanel);
+            mma_ts(one, d, p + kTmemP, vd, ideo, add);
+            if (valid > kKeys - 16) {
+#pragma unroll
+                for (int c = 1; c < kKeys / 16; ++c)
+                    mma_ts(one, d, p + kTmemP + c * 8, vd + c * (2048 >> 4), ideo, 1);
+            } else {
+                for (int c = 1; c < (valid + 15) / 16; ++c)
+                    mma_ts(one, d, p + kTmemP + c * 8, vd + c * (2048 >> 4), ideo, 1);
             }
         };
         auto commit = [&](uint64_t *bar) {
-            if (lane == 0)
+            if (one)
                 tc_commit(bar);
         };
         if constexpr (NT == 1) {
