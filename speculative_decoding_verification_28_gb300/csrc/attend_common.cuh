@@ -28,6 +28,7 @@ struct AttendUnit {
     Seq seq;
     int tile, tile_end;    // this CTA's tiles of the unit
     int n_tiles;           // tiles of the unit
+    int seen_first, seen_last;  // prompt: keys that the first and the last query row see
     int part, n_parts;     // place among the unit's parts
     int first_cta;         // CTA that has part 0
 };
@@ -255,9 +256,10 @@ __device__ inline bool prompt_unit(const AttendArgs &a, const Shape &sh, AttendU
     u.seq = load_seq(a.seq, a.cache.N, a.cache.S, b);
     u.row0 = which * sh.unit_rows;
     u.n_rows = min(sh.unit_rows, u.seq.n * sh.G - u.row0);
-    const int keys = u.seq.prefix + (u.row0 + u.n_rows - 1) / sh.G + 1;  // seen by the last row
+    u.seen_first = u.seq.prefix + u.row0 / sh.G + 1;
+    u.seen_last = u.seq.prefix + (u.row0 + u.n_rows - 1) / sh.G + 1;
     u.tile = 0;
-    u.n_tiles = u.tile_end = (keys + sh.tile_keys - 1) / sh.tile_keys;
+    u.n_tiles = u.tile_end = (u.seen_last + sh.tile_keys - 1) / sh.tile_keys;
     u.part = u.first_cta = 0;
     u.n_parts = 1;
     return true;

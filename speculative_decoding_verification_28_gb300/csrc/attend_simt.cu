@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(AttendArgs a)
                 }
             } else {
                 const int k0 = tile * kSimtKeys;
-                const int end = PROMPT ? u.seq.prefix + (u.row0 + u.n_rows - 1) / a.G + 1 : u.seq.prefix;
+                const int end = PROMPT ? u.seen_last : u.seq.prefix;
                 keys = min(kSimtKeys, end - k0);
                 ks = kc + (long long)k0 * D;
                 vs = vc + (long long)k0 * D;

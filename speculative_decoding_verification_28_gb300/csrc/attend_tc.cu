@@ -299,14 +299,13 @@ struct Tile {
     bool nodes, masked;
 };
 template <bool PROMPT>
-__device__ __forceinline__ Tile tile_of(const AttendUnit &u, int G, int tile)
+__device__ __forceinline__ Tile tile_of(const AttendUnit &u, int tile)
 {
     Tile t;
     if (PROMPT) {
-        const int first = u.seq.prefix + u.row0 / G + 1, last = u.seq.prefix + (u.row0 + u.n_rows - 1) / G + 1;
         t.nodes = false;
-        t.valid = min(kKeys, last - tile * kKeys);
-        t.masked = (tile + 1) * kKeys > first;
+        t.valid = min(kKeys, u.seen_last - tile * kKeys);
+        t.masked = (tile + 1) * kKeys > u.seen_first;
     } else {
         t.nodes = tile == u.n_tiles - 1;
         t.valid = t.nodes ? u.seq.n : min(kKeys, u.seq.prefix - tile * kKeys);
@@ -535,7 +534,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                     return;
                 tc_fence_after();
                 score(q_smem + qb * Sh::kTile, ring + sg * Sh::kTile, tmem + (is & 1) * 128,
-                      tile_of<PROMPT>(w, a.G, wt).valid);
+                      tile_of<PROMPT>(w, wt).valid);
                 commit(&s.s_full[is & 1]);
                 commit(&s.kv_empty[sg]);
                 ++is;
@@ -553,7 +552,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                     if (have)
                         score_next();
                     const int sg = (2 * i + 1) % ST;
-                    const Tile tl = tile_of<PROMPT>(u, a.G, tile);
+                    const Tile tl = tile_of<PROMPT>(u, tile);
                     ok = ok && wait(&s.p_full[i & 1], (i >> 1) & 1) && wait(&s.kv_full[sg], ((2 * i + 1) / ST) & 1);
                     if (ok && guarded(tl))
                         ok = wait_guard(sg);
@@ -584,13 +583,13 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                 for (int t = 0; t < NT; ++t)
                     if (u.tile < te[t]) {
                         score(q_smem + t * Sh::kTile, ring + ((2 * i) % ST) * Sh::kTile, tmem + t * 128,
-                              tile_of<PROMPT>(u, a.G, u.tile).valid);
+                              tile_of<PROMPT>(u, u.tile).valid);
                         commit(&s.s_full[t]);
                     }
                 commit(&s.kv_empty[(2 * i) % ST]);
                 for (int tile = u.tile; ok && tile < end; ++tile, ++i) {
                     const int sv = (2 * i + 1) % ST, sk = (2 * i + 2) % ST;
-                    const Tile tl = tile_of<PROMPT>(u, a.G, tile);
+                    const Tile tl = tile_of<PROMPT>(u, tile);
                     ok = wait(&s.kv_full[sv], ((2 * i + 1) / ST) & 1);
                     if (ok && guarded(tl))
                         ok = wait_guard(sv);
@@ -612,7 +611,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                         }
                         if (tile + 1 < te[t]) {
                             score(q_smem + t * Sh::kTile, ring + sk * Sh::kTile, tmem + t * 128,
-                                  tile_of<PROMPT>(u, a.G, tile + 1).valid);
+                                  tile_of<PROMPT>(u, tile + 1).valid);
                             commit(&s.s_full[t]);
                         }
                     }
@@ -635,7 +634,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
             __syncwarp();
             int g = 0;  // masked tiles of the unit so far
             for (int tile = u.tile; ok && tile < u.tile_end; ++tile, ++i) {
-                const Tile tl = tile_of<PROMPT>(u, a.G, tile);
+                const Tile tl = tile_of<PROMPT>(u, tile);
                 // The guard sees every load of the ring and releases it too, so
                 // that no barrier is ever two phases ahead of it
                 const int sk = (2 * i) % ST, sg = (2 * i + 1) % ST;
@@ -722,7 +721,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                 // the tile is handed over: a parity says nothing of older ones
                 bool seen = NT != 1 || tile == u.tile;
                 if (busy) {
-                    const Tile tl = tile_of<PROMPT>(u, a.G, tile);
+                    const Tile tl = tile_of<PROMPT>(u, tile);
                     const uint32_t tm_s = tmem + lanes + x * 128;
                     // The weights take the upper half of the scores' columns.
                     // Chunks of 32 columns are weighed from the top down, each
@@ -879,7 +878,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                             // the values taken out of V go where they are seen
                             int g = 0;
                             for (int tile = u.tile; tile < u.tile_end; ++tile) {
-                                const Tile tl = tile_of<PROMPT>(u, a.G, tile);
+                                const Tile tl = tile_of<PROMPT>(u, tile);
                                 if (!tl.masked)
                                     continue;
                                 for (int key = 0; key < tl.valid; ++key) {
