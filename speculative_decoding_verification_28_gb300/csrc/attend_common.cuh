@@ -178,13 +178,15 @@ struct UnitWalk {
 // ---------------------------------------------------------------------------
 // [counters: one per CTA, zero between calls] [slots: two per CTA, one for the
 // unit that it finishes for others or passes on, one for the unit that starts
-// in it and is cut]; a slot is ROWS x D sums, ROWS maxima (base 2), ROWS sums.
+// in it and is cut]; a slot is ROWS rows of sums (D rounded up to 4), ROWS
+// maxima (base 2), ROWS sums of weights.
 constexpr size_t kPartHead = SPEC_ATTEND_ZERO;
 static_assert(kAttendCtas * sizeof(int) <= kPartHead, "one counter per CTA");
+__host__ __device__ inline int part_cols(int D) { return (D + 3) & ~3; }
 template <int ROWS>
 __host__ __device__ inline size_t part_floats(int D)
 {
-    return (size_t)ROWS * D + 2 * ROWS;
+    return (size_t)ROWS * part_cols(D) + 2 * ROWS;
 }
 template <int ROWS>
 __device__ __forceinline__ float *part_slot(const AttendArgs &a, int cta, int part)
@@ -266,37 +268,96 @@ __device__ inline bool prompt_unit(const AttendArgs &a, const Shape &sh, AttendU
 }
 
 // Joins a unit's parts: O = sum 2^(m_p - m) O_p / sum 2^(m_p - m) l_p.  Called
-// by NT threads of which this is thread t, after every part was seen.  A row
-// that no part saw anything for (every l zero) gives zeros.
-template <typename T, int ROWS, int NT>
-__device__ void join_parts(const AttendArgs &a, const AttendUnit &u, int t)
+// by whole warps, of which this is warp w of `warps`, after every part was
+// seen.  A warp takes JOIN_ROWS rows at a time: lane p has the maximum and the
+// sum of part p, lane l four columns of the output; the loads of all rows are
+// in flight together, since the time of a join is their latency (a thread that
+// took one row's parts after another needed 8 to 35 us where a unit of 36 to
+// 252 rows is cut; this form 1 to 4).  A row that no part saw anything for
+// (every l zero) gives zeros.
+constexpr int kJoinRows = 4;
+template <typename T, int ROWS>
+__device__ void join_parts(const AttendArgs &a, const AttendUnit &u, int w, int warps)
 {
-    const int D = a.cache.D, rows = u.n_rows;
+    const int D = a.cache.D, dp = part_cols(D), lane = threadIdx.x & 31;
     T *out = reinterpret_cast<T *>(a.out);
-    const int cols = (D + 3) / 4;
-    for (int w = t; w < rows * cols; w += NT) {
-        const int r = w / cols, c = (w - r * cols) * 4;
-        float m = -INFINITY;
-        for (int p = 0; p < u.n_parts; ++p)
-            m = fmaxf(m, __ldcg(part_slot<ROWS>(a, u.first_cta + p, p) + (size_t)ROWS * D + r));
-        const float m0 = m == -INFINITY ? 0.0f : m;
-        float o[4] = {0, 0, 0, 0}, l = 0.0f;
-        for (int p = 0; p < u.n_parts; ++p) {
-            const float *slot = part_slot<ROWS>(a, u.first_cta + p, p);
-            const float f = exp2f(__ldcg(slot + (size_t)ROWS * D + r) - m0);
-            l = fmaf(f, __ldcg(slot + (size_t)ROWS * D + ROWS + r), l);
+    for (int r0 = w * kJoinRows; r0 < u.n_rows; r0 += warps * kJoinRows)
+        for (int c0 = 0; c0 < dp; c0 += 128) {
+            const int c = c0 + lane * 4;
+            const bool mine = c < dp;
+            float o[kJoinRows][4] = {}, m[kJoinRows], l[kJoinRows];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + e < D)
-                    o[e] = fmaf(f, __ldcg(slot + (size_t)r * D + c + e), o[e]);
+            for (int i = 0; i < kJoinRows; ++i) {
+                m[i] = -INFINITY;
+                l[i] = 0.0f;
+            }
+            for (int p0 = 0; p0 < u.n_parts; p0 += 32) {
+                const int p = p0 + lane, np = min(32, u.n_parts - p0);
+                float wt[kJoinRows], mp[kJoinRows], lp[kJoinRows];
+                const float *slot = p < u.n_parts ? part_slot<ROWS>(a, u.first_cta + p, p) + (size_t)ROWS * dp : nullptr;
+#pragma unroll
+                for (int i = 0; i < kJoinRows; ++i) {
+                    const bool in = slot && r0 + i < u.n_rows;
+                    mp[i] = in ? __ldcg(slot + r0 + i) : -INFINITY;
+                    lp[i] = in ? __ldcg(slot + ROWS + r0 + i) : 0.0f;
+                }
+                for (int j0 = 0; j0 < np; j0 += 2) {
+                    float4 x[2][kJoinRows];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int pj = p0 + min(j0 + j, np - 1);
+                        const float *from = part_slot<ROWS>(a, u.first_cta + pj, pj) + (size_t)r0 * dp + c;
+#pragma unroll
+                        for (int i = 0; i < kJoinRows; ++i)
+                            x[j][i] = mine && r0 + i < u.n_rows ? __ldcg(reinterpret_cast<const float4 *>(from + i * dp))
+                                                                : make_float4(0, 0, 0, 0);
+                    }
+                    if (j0 == 0) {  // the weights, with the first sums in flight
+#pragma unroll
+                        for (int i = 0; i < kJoinRows; ++i) {
+                            float mx = mp[i];
+                            for (int k = 1; k < np; k <<= 1)
+                                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
+                            mx = fmaxf(__shfl_sync(0xFFFFFFFFu, mx, 0), m[i]);
+                            const float m0 = mx == -INFINITY ? 0.0f : mx, f = exp2f(m[i] - m0);
+                            m[i] = mx;
+                            wt[i] = exp2f(mp[i] - m0);
+                            float ls = wt[i] * lp[i];
+                            for (int k = 1; k < np; k <<= 1)
+                                ls += __shfl_xor_sync(0xFFFFFFFFu, ls, k);
+                            l[i] = fmaf(l[i], f, __shfl_sync(0xFFFFFFFFu, ls, 0));
+                            if (p0 > 0)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    o[i][e] *= f;
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int i = 0; i < kJoinRows; ++i) {
+                            const float f = __shfl_sync(0xFFFFFFFFu, wt[i], j0 + j);
+                            if (j0 + j < np) {
+                                o[i][0] = fmaf(f, x[j][i].x, o[i][0]);
+                                o[i][1] = fmaf(f, x[j][i].y, o[i][1]);
+                                o[i][2] = fmaf(f, x[j][i].z, o[i][2]);
+                                o[i][3] = fmaf(f, x[j][i].w, o[i][3]);
+                            }
+                        }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kJoinRows; ++i) {
+                if (r0 + i >= u.n_rows || !mine)
+                    continue;
+                const float inv = l[i] > 0.0f || l[i] != l[i] ? 1.0f / l[i] : 0.0f;
+                T *dst = out + row_place(a, u, r0 + i) + c;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < D)
+                        dst[e] = round_to<T>(o[i][e] * inv);
+            }
         }
-        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-        T *dst = out + row_place(a, u, r) + c;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (c + e < D)
-                dst[e] = round_to<T>(o[e] * inv);
-    }
 }
 
 }  // namespace spec

@@ -246,12 +246,12 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(AttendArgs a)
                         if (whole)
                             reinterpret_cast<T *>(a.out)[row_place(a, u, r) + c] = round_to<T>(acc[cb][i][e] * inv);
                         else
-                            __stcg(slot + (size_t)r * D + c, acc[cb][i][e]);
+                            __stcg(slot + (size_t)r * dp + c, acc[cb][i][e]);
                     }
                 }
             if (!whole && lane == 0) {
-                __stcg(slot + (size_t)kSimtRows * D + r, s_m[r]);
-                __stcg(slot + (size_t)kSimtRows * D + kSimtRows + r, l);
+                __stcg(slot + (size_t)kSimtRows * dp + r, s_m[r]);
+                __stcg(slot + (size_t)kSimtRows * dp + kSimtRows + r, l);
             }
         }
         if (!whole) {
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(AttendArgs a)
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                join_parts<T, kSimtRows, kSimtThreads>(a, u, t);
+                join_parts<T, kSimtRows>(a, u, warp, kSimtThreads / 32);
             }
         }
         __syncthreads();  // q, s_l and s_last are rewritten next

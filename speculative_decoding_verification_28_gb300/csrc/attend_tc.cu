@@ -957,7 +957,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                     break;
                 if (s.last) {
                     __threadfence();
-                    join_parts<T, Sh::kRows, Sh::kSoftmax>(a, u, tid);
+                    join_parts<T, Sh::kRows>(a, u, warp, Sh::kSoftmax / 32);
                 }
             }
             ++n;
