@@ -464,7 +464,7 @@ SPEC_API int spec_append_prompt(const void *qkv, spec_dtype dt, int M, int Hq, v
 /* Workspace of spec_attend_round (does not depend on B or S; 256-byte
  * aligned; its first SPEC_ATTEND_ZERO bytes zero before its first use, and
  * again after each call). */
-#define SPEC_ATTEND_ZERO 1024
+#define SPEC_ATTEND_ZERO 2048
 SPEC_API size_t spec_attend_workspace_bytes(int T, int Hq, int H, int D);
 
 /*

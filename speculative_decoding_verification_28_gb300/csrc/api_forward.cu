@@ -203,6 +203,10 @@ int spec_attend_round(const void *q, spec_dtype dt, int B, int T, int Hq, const 
     const long long nq = (long long)B * T * Hq * D * dtype_bytes(dt);
     if (!len || (!idx && B > N) || overlap(q, nq, out, nq))
         return SPEC_EINVAL;
+    // tiles of 64 keys for 16 query rows each: the kernels count them in 31 bits
+    const long long groups = ((long long)T * (Hq / H) + 15) / 16, tiles = (S + 63LL) / 64 + 1;
+    if ((double)B * H * groups * tiles > (double)INT_MAX)
+        return SPEC_EINVAL;
     if (!int_arrays_ok(len, pad, idx, n_nodes, flags) || !aligned(tree_mask, 8) ||
         !aligned(staged, dtype_bytes(dt)))
         return SPEC_EALIGN;

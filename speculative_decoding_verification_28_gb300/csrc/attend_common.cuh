@@ -45,37 +45,39 @@ __device__ __forceinline__ int round_tiles(const Seq &s, const Shape &sh)
 }
 __device__ __forceinline__ int unit_groups(const Seq &s, const Shape &sh)
 {
-    return (int)(((long long)s.n * sh.G + sh.unit_rows - 1) / sh.unit_rows);
+    return (int)(((uint32_t)s.n * sh.G + sh.unit_rows - 1) / (uint32_t)sh.unit_rows);
 }
-__device__ __forceinline__ long long round_weight(const Seq &s, const Shape &sh, int H)
+// tiles of a sequence; over all sequences they are fewer than 2^31 (checked on
+// the host), so that the walk needs no 64-bit division
+__device__ __forceinline__ uint32_t round_weight(const Seq &s, const Shape &sh, int H)
 {
-    return (long long)H * unit_groups(s, sh) * round_tiles(s, sh);
+    return (uint32_t)H * unit_groups(s, sh) * round_tiles(s, sh);
 }
 
 // The run of this CTA: filled by the whole CTA, read by every role.
 struct Run {
-    long long begin, end;  // tiles, over all sequences
-    long long per;         // tiles of a full run
-    long long seq_begin;   // first tile of sequence b
+    uint32_t begin, end;   // tiles, over all sequences
+    uint32_t per;          // tiles of a full run
+    uint32_t seq_begin;    // first tile of sequence b
     int b;                 // sequence that holds `begin`
 };
 
 // Exclusive prefix of v over the block; total in *total.  s: one value per warp.
 template <int THREADS>
-__device__ long long block_exclusive(long long v, long long *s, long long *total)
+__device__ uint32_t block_exclusive(uint32_t v, uint32_t *s, uint32_t *total)
 {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    long long x = v;
+    uint32_t x = v;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
-        const long long o = __shfl_up_sync(0xFFFFFFFFu, x, m);
+        const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, x, m);
         if (lane >= m)
             x += o;
     }
     if (lane == 31)
         s[w] = x;
     __syncthreads();
-    long long before = 0, sum = 0;
+    uint32_t before = 0, sum = 0;
 #pragma unroll
     for (int i = 0; i < THREADS / 32; ++i) {
         if (i < w)
@@ -89,37 +91,40 @@ __device__ long long block_exclusive(long long v, long long *s, long long *total
 // Every thread takes a contiguous range of sequences; s_run is complete after
 // the caller's next __syncthreads.  CTA 0 writes the flags.
 template <int THREADS>
-__device__ void find_run(const AttendArgs &a, const Shape &sh, long long *s_scan, Run *s_run)
+__device__ void find_run(const AttendArgs &a, const Shape &sh, uint32_t *s_scan, Run *s_run)
 {
     const int per_thread = (a.seq.B + THREADS - 1) / THREADS;
     const int b0 = threadIdx.x * per_thread, b1 = min(a.seq.B, b0 + per_thread);
-    long long w = 0;
+    uint32_t w = 0;
     for (int b = b0; b < b1; ++b) {
         const Seq s = load_seq(a.seq, a.cache.N, a.cache.S, b);
         w += round_weight(s, sh, a.cache.H);
         if (blockIdx.x == 0 && a.flags)
             a.flags[b] = s.ok ? 0u : SPEC_FLAG_BAD_STATE;
     }
-    long long total;
-    long long at = block_exclusive<THREADS>(w, s_scan, &total);
-    const long long even = (total + gridDim.x - 1) / gridDim.x;
-    const long long per = even < kMinTiles ? kMinTiles : even;
-    const long long begin = per * blockIdx.x;
+    uint32_t total;
+    uint32_t at = block_exclusive<THREADS>(w, s_scan, &total);
+    const uint32_t even = (total + gridDim.x - 1) / gridDim.x;
+    const uint32_t per = even < kMinTiles ? kMinTiles : even;
+    const uint32_t begin = min(per * blockIdx.x, total);
     if (threadIdx.x == 0) {
         s_run->per = per;
-        s_run->begin = begin < total ? begin : total;
-        s_run->end = begin + per < total ? begin + per : total;
+        s_run->begin = begin;
+        s_run->end = min(begin + per, total);
     }
-    if (begin < total && at <= begin && begin < at + w) {  // one thread holds it
-        for (int b = b0; b < b1; ++b) {
-            const long long wb = round_weight(load_seq(a.seq, a.cache.N, a.cache.S, b), sh, a.cache.H);
-            if (begin < at + wb) {
-                s_run->b = b;
-                s_run->seq_begin = at;
-                break;
+    if (at <= begin && begin < at + w) {  // one thread holds it
+        if (b1 - b0 > 1)
+            for (int b = b0; b < b1; ++b) {
+                const uint32_t wb = round_weight(load_seq(a.seq, a.cache.N, a.cache.S, b), sh, a.cache.H);
+                if (begin < at + wb) {
+                    s_run->b = b;
+                    break;
+                }
+                at += wb;
             }
-            at += wb;
-        }
+        else
+            s_run->b = b0;
+        s_run->seq_begin = at;
     }
 }
 
@@ -128,8 +133,7 @@ struct UnitWalk {
     const AttendArgs *a;
     Shape sh;
     Run run;
-    long long pos;
-    long long weight;
+    uint32_t pos, weight;
     int loaded;  // sequence held in `cur`, or -1
     Seq cur;
     __device__ UnitWalk(const AttendArgs &args, const Shape &shape, const Run &r)
@@ -151,23 +155,29 @@ struct UnitWalk {
             run.seq_begin += weight;
             ++run.b;  // ends: run.end is at most the tiles of all sequences
         }
-        const int tiles = round_tiles(cur, sh), groups = unit_groups(cur, sh);
-        const long long off = pos - run.seq_begin;
-        const int which = (int)(off / tiles), t0 = (int)(off - (long long)which * tiles);
-        const long long left = run.end - pos;
+        const uint32_t tiles = round_tiles(cur, sh), groups = unit_groups(cur, sh);
+        const uint32_t off = pos - run.seq_begin;
+        const uint32_t which = off / tiles, t0 = off - which * tiles;
+        const uint32_t left = run.end - pos;
         u.b = run.b;
-        u.h = which / groups;
+        u.h = groups == 1 ? which : which / groups;
         u.row0 = (which - u.h * groups) * sh.unit_rows;
         u.n_rows = min(sh.unit_rows, cur.n * sh.G - u.row0);
         u.seq = cur;
         u.tile = t0;
-        u.tile_end = tiles - t0 < left ? tiles : t0 + (int)left;
+        u.tile_end = t0 + min(tiles - t0, left);
         u.n_tiles = tiles;
-        const long long g0 = pos - t0;  // the unit's first tile
-        const long long first = g0 / run.per, last = (g0 + tiles - 1) / run.per;
-        u.first_cta = (int)first;
-        u.n_parts = (int)(last - first) + 1;
-        u.part = (int)((long long)blockIdx.x - first);
+        const uint32_t g0 = pos - t0;  // the unit's first tile
+        if (t0 == 0 && u.tile_end == (int)tiles) {
+            u.first_cta = blockIdx.x;
+            u.n_parts = 1;
+            u.part = 0;
+        } else {
+            const uint32_t first = g0 / run.per, last = (g0 + tiles - 1) / run.per;
+            u.first_cta = first;
+            u.n_parts = last - first + 1;
+            u.part = blockIdx.x - first;
+        }
         pos += u.tile_end - t0;
         return true;
     }
@@ -181,7 +191,7 @@ struct UnitWalk {
 // in it and is cut]; a slot is ROWS rows of sums (D rounded up to 4), ROWS
 // maxima (base 2), ROWS sums of weights.
 constexpr size_t kPartHead = SPEC_ATTEND_ZERO;
-static_assert(kAttendCtas * sizeof(int) <= kPartHead, "one counter per CTA");
+static_assert(2 * kAttendCtas * sizeof(int) <= kPartHead, "one counter per CTA");
 __host__ __device__ inline int part_cols(int D) { return (D + 3) & ~3; }
 template <int ROWS>
 __host__ __device__ inline size_t part_floats(int D)

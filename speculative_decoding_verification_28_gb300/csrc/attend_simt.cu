@@ -65,7 +65,7 @@ template <typename T, int CB, bool PROMPT>
 __global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(AttendArgs a)
 {
     extern __shared__ __align__(16) float smem[];
-    __shared__ long long s_scan[kSimtThreads / 32];
+    __shared__ uint32_t s_scan[kSimtThreads / 32];
     __shared__ Run s_run;
     __shared__ float s_f[kSimtRows], s_m[kSimtRows], s_l[kSimtRows];
     __shared__ int s_last;

@@ -21,237 +21,9 @@
 // NT = 1 (up to 128 query rows): S has two buffers, so the next tile's scores
 // form while this tile's weights do.  NT = 2: the two tiles take turns on the
 // tensor pipe.
-#include <cuda.h>
-
-#include "attend_common.cuh"
-#include "bulk_copy.cuh"
-#include "verify_common.cuh"
+#include "tcgen.cuh"
 
 namespace spec {
-
-constexpr int kKeys = 128;  // keys of a tile, rows of a query tile
-constexpr int kTcWaitLimit = 2000;  // probes of up to ~1 ms, after a wait that gave up
-constexpr long long kTcWaitClocks = 4000000000ll;  // about 2 s
-constexpr float kLazy = 8.0f;       // base-2 headroom of the running maximum
-constexpr int kGuardRing = 8;       // units whose guard words may be live at once
-
-// ---------------------------------------------------------------------------
-// inline PTX
-// ---------------------------------------------------------------------------
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *m, int x, int y, int z, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-                 "[%5];" ::"r"(dst),
-                 "l"(m), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *m, int x, int y, int z, int w, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-                 "%5}], [%6];" ::"r"(dst),
-                 "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
-                 : "memory");
-}
-// one probe of a phase, without a time of its own to sleep: it wakes sooner
-__device__ __forceinline__ bool mbar_poll(uint64_t *bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok)
-                 : "r"(smem_addr(bar)), "r"(parity)
-                 : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t *bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-__device__ __forceinline__ void tc_commit(uint64_t *bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// keeps what is done with loaded registers behind the wait for them
-template <int N>
-__device__ __forceinline__ void tc_pin(uint32_t *r)
-{
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        asm volatile("" : "+r"(r[i]));
-}
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Shared-memory operand with 128-byte swizzle: rows of 128 bytes, groups of
-// eight rows 1024 bytes apart, panels of 64 elements `panel` bytes apart
-// (used by operands whose long axis is not the summed one).
-// Operand descriptors: the upper word is the same for all, the lower holds
-// the address and the panel step.  Only the elected lane issues (`one`), but
-// the whole warp computes, so that the words stay in uniform registers: built
-// per lane they cost more than the 64 cycles of a 128 x 128 x 16 product.
-constexpr uint32_t kOperandHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t operand(uint32_t addr, uint32_t panel) { return (addr >> 4) | ((panel >> 4) << 16); }
-
-__device__ __forceinline__ uint32_t elect_one()
-{
-    uint32_t one;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-    return one;
-}
-
-// D = A B (+ D): A and B in shared memory
-__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
-{
-    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-                 "mov.b64 x, {%1, %6};\n\tmov.b64 y, {%2, %6};\n\t"
-                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(one), "n"(kOperandHi)
-                 : "memory");
-}
-// A in TMEM
-__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
-{
-    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-                 "mov.b64 y, {%2, %6};\n\t"
-                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(one), "n"(kOperandHi)
-                 : "memory");
-}
-
-#define SPEC_R4(x, i) x[i], x[i + 1], x[i + 2], x[i + 3]
-#define SPEC_OUT4(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3])
-#define SPEC_IN4(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3])
-
-// 32 columns of this warp's 32 lanes
-__device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t *r)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-                 "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-                 : SPEC_OUT4(r, 0), SPEC_OUT4(r, 4), SPEC_OUT4(r, 8), SPEC_OUT4(r, 12), SPEC_OUT4(r, 16),
-                   SPEC_OUT4(r, 20), SPEC_OUT4(r, 24), SPEC_OUT4(r, 28)
-                 : "r"(addr));
-}
-__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t *r)
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-                 "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::
-                     SPEC_IN4(r, 0),
-                 SPEC_IN4(r, 4), SPEC_IN4(r, 8), SPEC_IN4(r, 12), SPEC_IN4(r, 16), SPEC_IN4(r, 20), SPEC_IN4(r, 24),
-                 SPEC_IN4(r, 28), "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t *r)
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
-                 "%13, %14, %15};" ::SPEC_IN4(r, 0),
-                 SPEC_IN4(r, 4), SPEC_IN4(r, 8), SPEC_IN4(r, 12), "r"(addr)
-                 : "memory");
-}
-
-// the loads so far have arrived; r are registers of theirs
-__device__ __forceinline__ void tc_loaded(uint32_t *r)
-{
-    tc_wait_ld();
-    tc_pin<32>(r);
-}
-__device__ __forceinline__ void tc_load(uint32_t addr, uint32_t *r)
-{
-    tc_ld32(addr, r);
-    tc_loaded(r);
-}
-
-// two fp32 operations in one instruction
-__device__ __forceinline__ uint64_t pair(float lo, float hi)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-__device__ __forceinline__ float max32(const uint32_t *r)
-{
-    float m[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const uint32_t *x = r + 16 * h;
-        m[h] = __uint_as_float(x[15]);
-#pragma unroll
-        for (int e = 0; e < 14; e += 2)
-            m[h] = max3(m[h], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-        m[h] = fmaxf(m[h], __uint_as_float(x[14]));
-    }
-    return fmaxf(m[0], m[1]);
-}
-
-template <typename T>
-struct TcType;
-template <>
-struct TcType<__nv_bfloat16> {
-    static constexpr uint32_t kFmt = 1;
-    __device__ static uint32_t pack(float lo, float hi)
-    {
-        uint32_t r;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-        return r;
-    }
-    // exponent of all ones in either half
-    __device__ static bool odd(uint32_t w) { return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u; }
-    __device__ static uint32_t max_abs(uint32_t m, uint32_t w) { return max_nan_bf16x2(m, w & 0x7FFF7FFFu); }
-    static constexpr uint32_t kExp = 0x7F80u;
-};
-template <>
-struct TcType<__half> {
-    static constexpr uint32_t kFmt = 0;
-    __device__ static uint32_t pack(float lo, float hi)
-    {
-        uint32_t r;
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-        return r;
-    }
-    __device__ static bool odd(uint32_t w) { return (w & 0x7C00u) == 0x7C00u || (w & 0x7C000000u) == 0x7C000000u; }
-    __device__ static uint32_t max_abs(uint32_t m, uint32_t w) { return max_nan_f16x2(m, w & 0x7FFF7FFFu); }
-    static constexpr uint32_t kExp = 0x7C00u;
-};
-
-// instruction descriptor: fp32 accumulators, both operands T, M = 128
-template <typename T>
-__device__ __forceinline__ uint32_t tc_idesc(int n, bool b_rows_summed)
-{
-    return (1u << 4) | (TcType<T>::kFmt << 7) | (TcType<T>::kFmt << 10) | ((b_rows_summed ? 1u : 0u) << 16) |
-           ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
-}
 
 // ---------------------------------------------------------------------------
 // shapes
@@ -272,48 +44,17 @@ struct TcShape {
     static constexpr uint32_t kTmemO = 256;
 };
 
-struct TcMaps {
-    CUtensorMap q, kv, node;
-};
-// rows the maps' boxes bring
-struct TcBoxes {
-    int q_tok, tok_tile, kv_rows, node_rows;
-};
-
 template <int STAGES>
 struct TcShared {
     uint64_t kv_full[STAGES], kv_empty[STAGES], q_full[2], q_empty[2];
     uint64_t v_ok[STAGES];  // guarded tiles: a stage's next one waits for its own consumption
     uint64_t s_full[2], p_full[2], pv_done[2], joined;
-    long long scan[16];
+    uint32_t scan[16];
     Run run;
     uint32_t tmem;
     int abort, last;
-    uint32_t odd[kGuardRing][12];  // keys of the guarded tiles with a value that is not finite
+    uint32_t odd[kGuardRing][13];  // keys of the guarded tiles with a value that is not finite; [12]: any
 };
-
-// A tile of a unit: how many of its keys are real, and whether some row does
-// not see all of those.
-struct Tile {
-    int valid;
-    bool nodes, masked;
-};
-template <bool PROMPT>
-__device__ __forceinline__ Tile tile_of(const AttendUnit &u, int tile)
-{
-    Tile t;
-    if (PROMPT) {
-        t.nodes = false;
-        t.valid = min(kKeys, u.seen_last - tile * kKeys);
-        t.masked = (tile + 1) * kKeys > u.seen_first;
-    } else {
-        t.nodes = tile == u.n_tiles - 1;
-        t.valid = t.nodes ? u.seq.n : min(kKeys, u.seq.prefix - tile * kKeys);
-        t.masked = t.nodes;
-    }
-    return t;
-}
-__device__ __forceinline__ bool guarded(const Tile &t) { return t.masked || (t.valid & 15); }
 
 // end of the tiles that query tile `t` of the unit needs
 template <bool PROMPT, int NT>
@@ -409,20 +150,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
 
     // a bounded wait; after one that gave up every role leaves its loop.
     // wait1 is one lane's, wait the whole warp's (its answer is the warp's)
-    auto wait1 = [&](uint64_t *bar, uint32_t parity) -> bool {
-        if (mbar_poll(bar, parity))
-            return true;
-        const long long t0 = clock64();
-        while (!mbar_poll(bar, parity)) {
-            if (*reinterpret_cast<volatile int *>(&s.abort))
-                return false;
-            if (clock64() - t0 > kTcWaitClocks) {
-                *reinterpret_cast<volatile int *>(&s.abort) = 1;
-                return false;
-            }
-        }
-        return true;
-    };
+    auto wait1 = [&](uint64_t *bar, uint32_t parity) -> bool { return wait_phase(bar, parity, &s.abort); };
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
         return __all_sync(0xFFFFFFFFu, wait1(bar, parity));
     };
@@ -432,7 +160,6 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
         if (lane == 0) {
-            const int heads = a.cache.N * a.cache.H;  // V slabs follow the K slabs
             uint32_t it = 0, n = 0;
             bool ok = true;
             while (ok && units.next(u)) {
@@ -449,23 +176,18 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                         tma_load_4d(q_smem + (qb * NT + t) * Sh::kTile + p * Sh::kPanel, &maps.q, p * 64, 0, u.h,
                                     tok + t * box.tok_tile, &s.q_full[qb]);
                 for (int tile = u.tile; ok && tile < u.tile_end; ++tile) {
-                    const bool nodes = !PROMPT && tile == u.n_tiles - 1;
-                    const CUtensorMap *m = nodes ? &maps.node : &maps.kv;
-                    const bool st = nodes && a.seq.staged;
-                    const int y = st ? 0 : u.seq.slot0 + (nodes ? u.seq.prefix : tile * kKeys);
-                    const int z = st ? u.b * a.cache.H + u.h : u.seq.row * a.cache.H + u.h;
-                    const int zv = st ? a.seq.B * a.cache.H : heads;
-                    const uint32_t bytes = Sh::kPanels * 128 * (nodes ? box.node_rows : box.kv_rows);
+                    const KvBox k = kv_box<Sh::kPanels>(a, maps, box, u, tile, !PROMPT && tile == u.n_tiles - 1);
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
                         const int sg = it % ST;
                         ok = ok && wait1(&s.kv_empty[sg], ((it / ST) & 1) ^ 1);
                         if (!ok)
                             break;
-                        mbar_arrive_expect_tx(&s.kv_full[sg], bytes);
+                        mbar_arrive_expect_tx(&s.kv_full[sg], k.bytes);
 #pragma unroll
                         for (int p = 0; p < Sh::kPanels; ++p)
-                            tma_load_3d(ring + sg * Sh::kTile + p * Sh::kPanel, m, p * 64, y, z + kv * zv, &s.kv_full[sg]);
+                            tma_load_3d(ring + sg * Sh::kTile + p * Sh::kPanel, k.m, p * 64, k.y, k.z + kv * k.zv,
+                                        &s.kv_full[sg]);
                         ++it;
                     }
                 }
@@ -629,7 +351,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
         bool ok = true;
         while (ok && units.next(u)) {
             uint32_t *odd = s.odd[n % kGuardRing];
-            if (lane < 12)
+            if (lane < 13)
                 odd[lane] = 0;
             __syncwarp();
             int g = 0;  // masked tiles of the unit so far
@@ -649,41 +371,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                         mbar_arrive(&s.kv_empty[sg]);
                     continue;
                 }
-                unsigned char *v = ring_p + sg * Sh::kTile;
-                for (int r = tl.valid + (lane >> 3); r < ((tl.valid + 15) & ~15); r += 4)
-#pragma unroll
-                    for (int p = 0; p < Sh::kPanels; ++p)
-                        *reinterpret_cast<uint4 *>(v + p * Sh::kPanel + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-                if (tl.masked) {
-                    uint32_t m = 0;
-                    for (int r = lane >> 3; r < tl.valid; r += 4)
-#pragma unroll
-                        for (int p = 0; p < Sh::kPanels; ++p) {
-                            const uint4 x = *reinterpret_cast<const uint4 *>(v + p * Sh::kPanel + r * 128 + (lane & 7) * 16);
-                            m = TcType<T>::max_abs(TcType<T>::max_abs(m, x.x), x.y);
-                            m = TcType<T>::max_abs(TcType<T>::max_abs(m, x.z), x.w);
-                        }
-                    if (__any_sync(0xFFFFFFFFu, TcType<T>::odd(m))) {
-                        // rare: take the values out, remember their keys
-                        for (int r = lane >> 3; r < tl.valid; r += 4) {
-                            for (int p = 0; p < Sh::kPanels; ++p) {
-                                uint32_t *w = reinterpret_cast<uint32_t *>(v + p * Sh::kPanel + r * 128 + (lane & 7) * 16);
-                                for (int e = 0; e < 4; ++e) {
-                                    uint32_t x = w[e];
-                                    if (!TcType<T>::odd(x))
-                                        continue;
-                                    if ((x & TcType<T>::kExp) == TcType<T>::kExp)
-                                        x &= 0xFFFF0000u;
-                                    if ((x >> 16 & TcType<T>::kExp) == TcType<T>::kExp)
-                                        x &= 0x0000FFFFu;
-                                    w[e] = x;
-                                    atomicOr(&odd[g * 4 + (r >> 5)], 1u << (r & 31));
-                                }
-                            }
-                        }
-                    }
-                    ++g;
-                }
+                guard_tile<T, Sh::kPanels>(ring_p + sg * Sh::kTile, tl, odd, g);
                 __threadfence_block();
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -864,10 +552,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                 tc_fence_after();
                 const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
                 const uint32_t *odd = s.odd[n % kGuardRing];
-                uint32_t any_odd = 0;
-#pragma unroll
-                for (int k = 0; k < 12; ++k)
-                    any_odd |= *reinterpret_cast<const volatile uint32_t *>(odd + k);
+                const uint32_t any_odd = *reinterpret_cast<const volatile uint32_t *>(odd + 12);
                 T *dst = real ? reinterpret_cast<T *>(a.out) + row_place(a, u, ur) : nullptr;
                 if (busy) {
 #pragma unroll 1
@@ -885,22 +570,11 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                                     if (!(odd[g * 4 + (key >> 5)] >> (key & 31) & 1))
                                         continue;
                                     bool sees;
-                                    const T *v;
-                                    if (tl.nodes) {
-                                        const uint64_t bits =
-                                            a.mask ? a.mask[(size_t)u.b * a.seq.T + tok] : (2ull << tok) - 1;
-                                        sees = bits >> key & 1;
-                                    } else {
-                                        sees = tile * kKeys + key <= u.seq.prefix + tok;
-                                    }
-                                    if (tl.nodes && a.seq.staged)
-                                        v = reinterpret_cast<const T *>(a.staged) +
-                                            ((a.st_v + (long long)u.b * a.cache.H + u.h) * a.seq.T + key) * D;
+                                    if (tl.nodes)
+                                        sees = (a.mask ? a.mask[(size_t)u.b * a.seq.T + tok] : (2ull << tok) - 1) >> key & 1;
                                     else
-                                        v = reinterpret_cast<const T *>(a.cache.kv) +
-                                            ((a.cache.v_slab + (long long)u.seq.row * a.cache.H + u.h) * a.cache.S +
-                                             u.seq.slot0 + (tl.nodes ? u.seq.prefix : tile * kKeys) + key) *
-                                                D;
+                                        sees = tile * kKeys + key <= u.seq.prefix + tok;
+                                    const T *v = value_row<T>(a, u, tl, tile, key);
                                     if (sees)
 #pragma unroll
                                         for (int e = 0; e < 32; ++e) {
@@ -976,76 +650,15 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
 // ---------------------------------------------------------------------------
 namespace {
 
-typedef CUresult (*EncodeTiled)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled()
-{
-    static EncodeTiled fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
-}
-
-// 16-bit elements, innermost extent D in panels of 64, the further extents,
-// strides (bytes) and box as given
-bool make_map(CUtensorMap *m, bool bf16, const void *p, int rank, const cuuint64_t *dim, const cuuint64_t *stride,
-              const cuuint32_t *box)
-{
-    const cuuint32_t one[4] = {1, 1, 1, 1};
-    return encode_tiled()(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
-                          const_cast<void *>(p), dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <typename T, int D, int NT, bool PROMPT>
 cudaError_t launch_tc(const AttendArgs &a, cudaStream_t st)
 {
     using Sh = TcShape<D, NT>;
-    const bool bf16 = TcType<T>::kFmt == 1;
-    const cuuint64_t e = 2, row = (cuuint64_t)D * e;
-    const long long tokens = PROMPT ? a.seq.M : (long long)a.seq.B * a.seq.T;
-    TcBoxes box;
-    box.tok_tile = kKeys / a.G;
-    box.q_tok = (int)(box.tok_tile < tokens ? box.tok_tile : tokens);
-    box.kv_rows = a.cache.S < kKeys ? a.cache.S : kKeys;
     TcMaps maps;
-    {
-        const cuuint64_t dim[4] = {(cuuint64_t)D, (cuuint64_t)a.G, (cuuint64_t)a.cache.H, (cuuint64_t)tokens};
-        const cuuint64_t stride[3] = {row, row * a.G, row * a.Hq};
-        const cuuint32_t bx[4] = {64, (cuuint32_t)a.G, 1, (cuuint32_t)box.q_tok};
-        if (!make_map(&maps.q, bf16, a.q, 4, dim, stride, bx))
-            return cudaErrorInvalidValue;
-    }
-    const cuuint64_t slab = row * a.cache.S;
-    const char *layer = static_cast<const char *>(a.cache.kv) + a.cache.k_slab * slab;
-    {
-        const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)a.cache.S, 2ull * a.cache.N * a.cache.H};
-        const cuuint64_t stride[2] = {row, slab};
-        const cuuint32_t bx[3] = {64, (cuuint32_t)box.kv_rows, 1};
-        if (!make_map(&maps.kv, bf16, layer, 3, dim, stride, bx))
-            return cudaErrorInvalidValue;
-    }
-    maps.node = maps.kv;
-    box.node_rows = 0;
-    if (!PROMPT) {
-        const int rows = a.seq.staged ? a.seq.T : a.cache.S;
-        box.node_rows = a.seq.T < rows ? a.seq.T : rows;
-        const cuuint64_t sl = row * rows, n = a.seq.staged ? 2ull * a.seq.B * a.cache.H : 2ull * a.cache.N * a.cache.H;
-        const cuuint64_t dim[3] = {(cuuint64_t)D, (cuuint64_t)rows, n};
-        const cuuint64_t stride[2] = {row, sl};
-        const cuuint32_t bx[3] = {64, (cuuint32_t)box.node_rows, 1};
-        const char *p = a.seq.staged ? static_cast<const char *>(a.staged) + a.st_k * sl : layer;
-        if (!make_map(&maps.node, bf16, p, 3, dim, stride, bx))
-            return cudaErrorInvalidValue;
-    }
+    TcBoxes box;
+    if (!tc_make_maps(a, TcType<T>::kFmt == 1, kKeys, &maps, &box))
+        return cudaErrorInvalidValue;
+    const long long tokens = PROMPT ? a.seq.M : (long long)a.seq.B * a.seq.T;
     const cudaError_t err = cudaFuncSetAttribute(attend_tc_kernel<T, D, NT, PROMPT>,
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
     if (err != cudaSuccess)
@@ -1077,11 +690,13 @@ bool attend_tc_takes(const AttendArgs &a, spec_dtype dt)
         return false;
     const uintptr_t at = reinterpret_cast<uintptr_t>(a.q) | reinterpret_cast<uintptr_t>(a.out) |
                          reinterpret_cast<uintptr_t>(a.cache.kv) | reinterpret_cast<uintptr_t>(a.staged);
-    return at % 16 == 0 && encode_tiled() != nullptr;
+    return at % 16 == 0 && tc_available();
 }
 
 cudaError_t launch_attend_tc(const AttendArgs &a, spec_dtype dt, cudaStream_t st)
 {
+    if (!a.seq.cu && a.seq.T * a.G <= 64)
+        return launch_attend_few(a, dt, st);
     if (a.cache.D == 64)
         return dt == SPEC_BF16 ? launch_tc_d<__nv_bfloat16, 64>(a, st) : launch_tc_d<__half, 64>(a, st);
     return dt == SPEC_BF16 ? launch_tc_d<__nv_bfloat16, 128>(a, st) : launch_tc_d<__half, 128>(a, st);
@@ -1091,7 +706,8 @@ size_t attend_tc_workspace(int T, int Hq, int H, int D)
 {
     const long long rows = (long long)T * (Hq / (H > 0 ? H : 1));
     const size_t part = rows <= kKeys ? part_floats<128>(D) : part_floats<256>(D);
-    return align256(kPartHead + 2 * kAttendCtas * part * sizeof(float));
+    const size_t tc = align256(kPartHead + 2 * kAttendCtas * part * sizeof(float)), few = attend_few_workspace(D);
+    return tc > few ? tc : few;
 }
 
 }  // namespace spec

@@ -118,6 +118,8 @@ cudaError_t launch_attend(const AttendArgs &a, spec_dtype dt, cudaStream_t st);
 size_t attend_workspace(int T, int Hq, int H, int D);
 bool attend_tc_takes(const AttendArgs &a, spec_dtype dt);
 cudaError_t launch_attend_tc(const AttendArgs &a, spec_dtype dt, cudaStream_t st);
+cudaError_t launch_attend_few(const AttendArgs &a, spec_dtype dt, cudaStream_t st);
+size_t attend_few_workspace(int D);
 size_t attend_tc_workspace(int T, int Hq, int H, int D);
 
 struct TreeArgs {

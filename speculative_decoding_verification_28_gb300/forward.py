@@ -23,7 +23,7 @@ from .api import _DT, _check, _need
 FLAG_BAD_STATE, FLAG_BAD_TREE = 16, 32
 MAX_NODES = 64
 MAX_HEAD_DIM = 256
-ATTEND_ZERO = 1024
+ATTEND_ZERO = 2048
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent from builds without CUDA
