@@ -17,8 +17,9 @@
 
 namespace spec {
 
-constexpr int kAppendThreads = 256;
-constexpr int kAppendAhead = 4;  // 16-byte loads of a thread in flight before the angles are ready
+constexpr int kAppendThreads = 128;
+constexpr int kAppendAhead = 4;     // heads of a thread whose loads are in flight together
+constexpr int kAppendWarps = 9728;  // fewer warps than this leave the GPU idle: tokens are shared out
 
 // round-to-nearest stores of fp32 values
 template <typename T>
@@ -30,20 +31,7 @@ __device__ __forceinline__ __nv_bfloat16 to_storage<__nv_bfloat16>(float x) { re
 template <>
 __device__ __forceinline__ __half to_storage<__half>(float x) { return __float2half_rn(x); }
 
-template <typename T>
-__device__ __forceinline__ uint4 pack16(const float *f)
-{
-    constexpr int VEC = Storage<T>::kVec;
-    T t[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i)
-        t[i] = to_storage<T>(f[i]);
-    uint4 u;
-    memcpy(&u, t, 16);
-    return u;
-}
-
-// The token of this CTA: its sequence, place and position.
+// A token: its sequence, place and position.
 struct Token {
     bool live;
     long long q_row;  // row of qkv and q_out
@@ -57,6 +45,7 @@ struct Token {
 // to the calls that write the cache
 __device__ __forceinline__ bool writes_cache(const SeqArgs &s) { return !s.staged; }
 
+// by a whole warp
 __device__ Token find_token(const AppendArgs &a, long long m)
 {
     Token t;
@@ -79,7 +68,7 @@ __device__ Token find_token(const AppendArgs &a, long long m)
         if (b >= a.seq.B || broken)
             return t;
     } else {
-        b = (int)(m / a.seq.T);
+        b = (int)((uint32_t)m / (uint32_t)a.seq.T);
     }
     const Seq s = load_seq(a.seq, a.cache.N, a.cache.S, b);
     i = (int)(m - s.tok0);
@@ -123,14 +112,27 @@ __device__ void append_flags(const AppendArgs &a)
     }
 }
 
-// cos and sin of pos * f.  The turns left after reduction are exact to fp64;
-// the fp32 argument's rounding is put back to first order.
+// cos and sin of pos * f.  Only the fraction of pos * f / (2 pi) turns counts,
+// and it is formed exactly enough for any position: f / (2 pi) is a pair g + h
+// of fp32 numbers (48 bits), pos * g is split by an FMA into its rounded value,
+// whose fraction is exact, and its error.  Below 2^24, where an fp32 pos is
+// exact, what is left off is under 2e-8 turns; beyond, fp64 (two lanes a clock
+// on this part, 10 times the time) does the same.
 __device__ __forceinline__ float2 turn(int pos, float f)
 {
-    double t = (double)pos * (double)f * 0.15915494309189533577;  // 1 / (2 pi)
-    t = 2.0 * (t - rint(t));  // half turns in [-1, 1]
-    const float h = (float)t;
-    const float d = (float)(t - (double)h) * 3.14159265358979f;
+    float h, d = 0.0f;  // half turns in [-1, 1], and what its rounding left off
+    if (pos < (1 << 24)) {
+        constexpr float kHi = 0.15915493667125702f, kLo = 6.420638243e-09f;  // 1 / (2 pi)
+        const float p = (float)pos;
+        const float g = f * kHi, gl = fmaf(f, kHi, -g) + f * kLo;
+        const float t = p * g, e = fmaf(p, g, -t) + p * gl;
+        h = 2.0f * ((t - rintf(t)) + e);
+    } else {
+        double t = (double)pos * (double)f * 0.15915494309189533577;
+        t = 2.0 * (t - rint(t));
+        h = (float)t;
+        d = (float)(t - (double)h) * 3.14159265358979f;
+    }
     float s, c;
     sincospif(h, &s, &c);
     return make_float2(fmaf(-s, d, c), fmaf(c, d, s));
@@ -151,95 +153,222 @@ __device__ __forceinline__ T *head_dst(const AppendArgs &a, const Token &t, int 
     return base + slab * row_len + t.kv_off + h * t.head_step;
 }
 
-// One CTA per token; LPH lanes hold one head, 16 bytes each.  Rotation over
-// the whole head (R == D) or none.  A thread's first kAppendAhead heads are
-// loaded before the angles are computed.
-template <typename T, int LPH>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a)
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t two(float lo, float hi)
 {
-    constexpr int VEC = Storage<T>::kVec;
-    constexpr int D = LPH * VEC;
-    constexpr int GROUPS = kAppendThreads / LPH;
-    __shared__ float2 s_turn[D / 2];
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 parts(uint64_t v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ uint64_t two_mul(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t two_fma(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// 8 bytes of storage as fp32 pairs (one for fp32, two for 16-bit types)
+template <typename T>
+struct Half8;
+template <>
+struct Half8<float> {
+    static constexpr int kPairs = 1;
+    __device__ static void load(uint2 u, uint64_t *x) { x[0] = two(__uint_as_float(u.x), __uint_as_float(u.y)); }
+    __device__ static uint2 store(const uint64_t *x)
+    {
+        const float2 f = parts(x[0]);
+        return make_uint2(__float_as_uint(f.x), __float_as_uint(f.y));
+    }
+};
+template <>
+struct Half8<__nv_bfloat16> {
+    static constexpr int kPairs = 2;
+    __device__ static uint64_t word(uint32_t w) { return two(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+    __device__ static void load(uint2 u, uint64_t *x)
+    {
+        x[0] = word(u.x);
+        x[1] = word(u.y);
+    }
+    __device__ static uint32_t back(uint64_t x)
+    {
+        const float2 f = parts(x);
+        uint32_t r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
+        return r;
+    }
+    __device__ static uint2 store(const uint64_t *x) { return make_uint2(back(x[0]), back(x[1])); }
+};
+template <>
+struct Half8<__half> {
+    static constexpr int kPairs = 2;
+    __device__ static uint64_t word(uint32_t w)
+    {
+        __half2 h;
+        memcpy(&h, &w, 4);
+        const float2 f = __half22float2(h);
+        return two(f.x, f.y);
+    }
+    __device__ static void load(uint2 u, uint64_t *x)
+    {
+        x[0] = word(u.x);
+        x[1] = word(u.y);
+    }
+    __device__ static uint32_t back(uint64_t x)
+    {
+        const float2 f = parts(x);
+        uint32_t r;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
+        return r;
+    }
+    __device__ static uint2 store(const uint64_t *x) { return make_uint2(back(x[0]), back(x[1])); }
+};
+
+__device__ __forceinline__ uint2 ld_stream8(const uint2 *p)
+{
+    uint2 r;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    return r;
+}
+
+// `share` warps per token (1 where there are tokens enough to fill the GPU,
+// up to 8 where there are not).  LPH lanes hold one head: 8 bytes of its first
+// half and the same 8 of its second, so that a rotation's pairs are in one
+// lane, as are the angles and norm weights of all heads of a token.  Rotation
+// over the whole head (R == D) or none.  The first loads are asked for before
+// anything else: what decides the token's place and angles is a chain of
+// three loads itself.  A first form with a CTA a token and 16 contiguous bytes
+// a lane (8 shuffles a vector for the pairs, angles and weights from shared
+// memory) was bound by its instructions: 216 us for 26624 tokens of 48 heads
+// of 128 in bf16, where HBM needs 96.  This one takes 129 us (5.1 TB/s), bound by
+// the loads in flight: 64 registers for a fourth CTA of 256 or loads for the
+// next head behind each head measured 130 and 154 us, two warps a token 139.
+template <typename T, int LPH>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a, int tokens, int share)
+{
+    using H8 = Half8<T>;
+    constexpr int NP = H8::kPairs;                 // pairs of elements in 8 bytes
+    constexpr int D = LPH * 16 / (int)sizeof(T);
+    constexpr int HPW = 32 / LPH;                  // heads a warp holds at a time
     append_flags(a);
-    const Token tok = find_token(a, blockIdx.x);
-    if (!tok.live)
+    const int lane = threadIdx.x & 31, ln = lane % LPH;
+    const uint32_t gw = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t m = gw / (uint32_t)share;
+    if (m >= (uint32_t)tokens)
         return;
     const int heads = a.Hq + 2 * a.cache.H;
-    const int grp = threadIdx.x / LPH, ln = threadIdx.x % LPH;
-    const uint4 *src = reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(a.qkv) + tok.q_row * heads * D) + ln;
-    for (int base = 0; base < heads; base += GROUPS * kAppendAhead) {
-        uint4 r[kAppendAhead];
+    const int first = (int)(gw - m * (uint32_t)share) * HPW + lane / LPH, step = share * HPW;
+    const T *src = reinterpret_cast<const T *>(a.qkv) + (size_t)m * heads * D + ln * 2 * NP;
+    Token tok;
+    T *q0, *k0, *v0;                               // head 0 of each kind
+    uint64_t cs[NP], sn[NP], ns[NP];               // per pair of elements: cosines, sines, minus sines
+    uint64_t gq[NP * 2], gk[NP * 2];
+    for (int base = 0; base < heads; base += kAppendAhead * step) {
+        uint2 lo[kAppendAhead], hi[kAppendAhead];
 #pragma unroll
         for (int u = 0; u < kAppendAhead; ++u) {
-            const int head = base + u * GROUPS + grp;
-            if (head < heads)
-                r[u] = ld_stream16(src + (size_t)head * LPH);
-        }
-        if (base == 0 && a.R) {
-            for (int i = threadIdx.x; i < D / 2; i += kAppendThreads)
-                s_turn[i] = turn(tok.pos, a.inv_freq[i]);
-            __syncthreads();
-        }
-#pragma unroll
-        for (int u = 0; u < kAppendAhead; ++u) {
-            const int head = base + u * GROUPS + grp;
-            // warps stay whole up to here: the shuffles below need every lane
-            if (base + u * GROUPS >= heads)
-                break;
-            const bool mine = head < heads;
-            const bool is_v = head >= a.Hq + a.cache.H;
-            float x[VEC];
-            Storage<T>::unpack(r[u], x);
-            if (!mine) {
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    x[e] = 0.0f;
+            const int head = base + u * step + first;
+            if (head < heads) {
+                lo[u] = ld_stream8(reinterpret_cast<const uint2 *>(src + (long long)head * D));
+                hi[u] = ld_stream8(reinterpret_cast<const uint2 *>(src + (long long)head * D + D / 2));
             }
-            const T *w = reinterpret_cast<const T *>(head < a.Hq ? a.q_weight : a.k_weight);
-            if (a.q_weight || a.k_weight) {  // the same for every thread
-                float sq = 0.0f;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e)
-                    sq = fmaf(x[e], x[e], sq);
-#pragma unroll
-                for (int m = LPH / 2; m > 0; m >>= 1)
-                    sq += __shfl_xor_sync(0xFFFFFFFFu, sq, m);
-                if (w && !is_v) {
-                    const float inv = rsqrtf(sq * (1.0f / D) + a.eps);
-                    float g[VEC];
-                    Storage<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(w) + ln), g);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e)
-                        x[e] = x[e] * inv * g[e];
-                }
-            }
+        }
+        if (base == 0) {
+            auto weights = [&](const void *w, uint64_t *g) {
+                const T *p = reinterpret_cast<const T *>(w) + ln * 2 * NP;
+                H8::load(__ldg(reinterpret_cast<const uint2 *>(p)), g);
+                H8::load(__ldg(reinterpret_cast<const uint2 *>(p + D / 2)), g + NP);
+            };
+            if (a.q_weight)
+                weights(a.q_weight, gq);
+            if (a.k_weight)
+                weights(a.k_weight, gk);
+            tok = find_token(a, m);
+            if (!tok.live)
+                return;  // the whole warp
+            q0 = head_dst<T>(a, tok, 0) + ln * 2 * NP;
+            k0 = head_dst<T>(a, tok, a.Hq) + ln * 2 * NP;
+            v0 = head_dst<T>(a, tok, a.Hq + a.cache.H) + ln * 2 * NP;
             if (a.R) {
-                if (a.interleaved) {
-                    if (!is_v) {
+                // half split: pair i of the lane turns with frequency 2 NP ln + i;
+                // interleaved: elements (2 i, 2 i + 1) of each half with
+                // NP ln + i and D / 4 + NP ln + i
 #pragma unroll
-                        for (int e = 0; e < VEC; e += 2) {
-                            const float2 cs = s_turn[(ln * VEC + e) / 2];
-                            const float lo = x[e], hi = x[e + 1];
-                            x[e] = lo * cs.x - hi * cs.y;
-                            x[e + 1] = hi * cs.x + lo * cs.y;
-                        }
-                    }
-                } else {
-                    // the other half of each pair is LPH / 2 lanes away
-                    const bool low = ln < LPH / 2;
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float o = __shfl_xor_sync(0xFFFFFFFFu, x[e], LPH / 2);
-                        if (!is_v) {
-                            const float2 cs = s_turn[(ln % (LPH / 2)) * VEC + e];
-                            x[e] = low ? x[e] * cs.x - o * cs.y : x[e] * cs.x + o * cs.y;
-                        }
-                    }
+                for (int i = 0; i < NP; ++i) {
+                    const int f0 = a.interleaved ? NP * ln + i : 2 * NP * ln + 2 * i;
+                    const int f1 = a.interleaved ? D / 4 + NP * ln + i : f0 + 1;
+                    const float2 t0 = turn(tok.pos, a.inv_freq[f0]), t1 = turn(tok.pos, a.inv_freq[f1]);
+                    cs[i] = two(t0.x, t1.x);
+                    sn[i] = two(t0.y, t1.y);
+                    ns[i] = two(-t0.y, -t1.y);
                 }
             }
-            if (mine)
-                reinterpret_cast<uint4 *>(head_dst<T>(a, tok, head))[ln] = is_v ? r[u] : pack16<T>(x);
+        }
+#pragma unroll
+        for (int u = 0; u < kAppendAhead; ++u) {
+            if (base + u * step >= heads)
+                break;  // the warp stays whole for the shuffles
+            const int head = base + u * step + first;
+            const bool mine = head < heads, is_v = head >= a.Hq + a.cache.H;
+            uint2 ol = lo[u], oh = hi[u];
+            if (__any_sync(0xFFFFFFFFu, mine && !is_v)) {
+                uint64_t x[2 * NP];
+                H8::load(mine ? lo[u] : make_uint2(0, 0), x);
+                H8::load(mine ? hi[u] : make_uint2(0, 0), x + NP);
+                const bool is_q = head < a.Hq;
+                if (a.q_weight || a.k_weight) {  // the same for every thread
+                    uint64_t sq = two_mul(x[0], x[0]);
+#pragma unroll
+                    for (int i = 1; i < 2 * NP; ++i)
+                        sq = two_fma(x[i], x[i], sq);
+                    const float2 q2 = parts(sq);
+                    float sum = q2.x + q2.y;
+#pragma unroll
+                    for (int k = LPH / 2; k > 0; k >>= 1)
+                        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, k);
+                    if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
+                        const float inv = rsqrtf(sum * (1.0f / D) + a.eps);
+#pragma unroll
+                        for (int i = 0; i < 2 * NP; ++i)
+                            x[i] = two_mul(two_mul(x[i], two(inv, inv)), is_q ? gq[i] : gk[i]);
+                    }
+                }
+                if (a.R && !a.interleaved) {
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        const uint64_t l = x[i], h = x[NP + i];
+                        x[i] = two_fma(l, cs[i], two_mul(h, ns[i]));
+                        x[NP + i] = two_fma(h, cs[i], two_mul(l, sn[i]));
+                    }
+                } else if (a.R) {
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) {
+                        const float2 c = parts(cs[i]), s = parts(sn[i]), l = parts(x[i]), h = parts(x[NP + i]);
+                        x[i] = two(l.x * c.x - l.y * s.x, l.y * c.x + l.x * s.x);
+                        x[NP + i] = two(h.x * c.y - h.y * s.y, h.y * c.y + h.x * s.y);
+                    }
+                }
+                if (!is_v) {
+                    ol = H8::store(x);
+                    oh = H8::store(x + NP);
+                }
+            }
+            if (mine) {
+                T *dst = head < a.Hq ? q0 + head * D : (is_v ? v0 : k0) + (head - a.Hq - (is_v ? a.cache.H : 0)) * tok.head_step;
+                *reinterpret_cast<uint2 *>(dst) = ol;
+                *reinterpret_cast<uint2 *>(dst + D / 2) = oh;
+            }
         }
     }
 }
@@ -301,20 +430,27 @@ __global__ void __launch_bounds__(kAppendThreads) append_any_kernel(AppendArgs a
 template <typename T>
 cudaError_t launch_append_t(const AppendArgs &a, cudaStream_t st)
 {
-    const unsigned grid = (unsigned)(a.seq.cu ? (a.seq.M > 0 ? a.seq.M : 1) : a.seq.B * a.seq.T);
+    const int tokens = a.seq.cu ? a.seq.M : a.seq.B * a.seq.T;
     const int D = a.cache.D;
     const long long bytes = (long long)D * sizeof(T);
     auto ok16 = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
     const bool vec = (a.R == D || a.R == 0) && ok16(a.qkv) && ok16(a.q_out) && ok16(a.kv_out) && ok16(a.staged) &&
                      ok16(a.q_weight) && ok16(a.k_weight);
-    if (vec && bytes == 512)
-        append_kernel<T, 32><<<grid, kAppendThreads, 0, st>>>(a);
-    else if (vec && bytes == 256)
-        append_kernel<T, 16><<<grid, kAppendThreads, 0, st>>>(a);
-    else if (vec && bytes == 128)
-        append_kernel<T, 8><<<grid, kAppendThreads, 0, st>>>(a);
-    else
-        append_any_kernel<T><<<grid, kAppendThreads, 0, st>>>(a);
+    if (vec && (bytes == 512 || bytes == 256 || bytes == 128)) {
+        int share = 1;
+        while (share < 8 && (long long)tokens * share * 2 <= kAppendWarps)
+            share *= 2;
+        const long long warps = (long long)tokens * share, per = kAppendThreads / 32;
+        const unsigned grid = (unsigned)(warps > 0 ? (warps + per - 1) / per : 1);
+        if (bytes == 512)
+            append_kernel<T, 32><<<grid, kAppendThreads, 0, st>>>(a, tokens, share);
+        else if (bytes == 256)
+            append_kernel<T, 16><<<grid, kAppendThreads, 0, st>>>(a, tokens, share);
+        else
+            append_kernel<T, 8><<<grid, kAppendThreads, 0, st>>>(a, tokens, share);
+    } else {
+        append_any_kernel<T><<<(unsigned)(tokens > 0 ? tokens : 1), kAppendThreads, 0, st>>>(a);
+    }
     return cudaGetLastError();
 }
 

@@ -26,7 +26,10 @@ MAX_HEAD_DIM = 256
 ATTEND_ZERO = 2048
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # absent from builds without CUDA
+# absent from builds without CUDA
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device_now = getattr(torch._C, "_cuda_getDevice", None)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", None)
 
 
 def _streamed(fn):
@@ -45,11 +48,12 @@ def _streamed(fn):
 
 def _call(fn, dev, *args):
     """fn(*args, the current stream of dev), with dev the current device."""
-    if torch.cuda.current_device() == dev.index:
-        rc = fn(*args, _raw_stream(dev.index))
+    i = dev.index
+    if _device_now() == i:
+        rc = fn(*args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _raw_stream(dev.index))
+            rc = fn(*args, _raw_stream(i))
     if rc:
         _check(rc)
 
@@ -80,7 +84,7 @@ def _ws(given, kind, nbytes, device, head):
         buf = getattr(given, "buf", given)
         _need(buf, torch.uint8, "workspace", device)
         return buf
-    capturing = torch.cuda.is_current_stream_capturing()
+    capturing = _capturing()
     if not capturing:
         key = kind, device.index, _raw_stream(device.index)
         buf = _scratch.get(key)
@@ -185,6 +189,9 @@ def spec_append_prompt(qkv, kv, layer, cu, pad, inv_freq, q_weight=None, k_weigh
     return q_out, flags
 
 
+_attend_bytes = {}  # spec_attend_workspace_bytes by its arguments
+
+
 def spec_attend_workspace_bytes(T, Hq, H, D):
     return int(_lib.load().spec_attend_workspace_bytes(int(T), int(Hq), int(H), int(D)))
 
@@ -205,7 +212,10 @@ def spec_attend_round(q, kv, layer, length, pad, tree_mask=None, n_nodes=None, i
     out = _out(out, shape, dt, dev, "out")
     flags = _out(flags, rows, _I32, dev, "flags")
     lib = _lib.load()
-    ws = _ws(workspace, "attend", lib.spec_attend_workspace_bytes(T, Hq, H, D), dev, ATTEND_ZERO)
+    need = _attend_bytes.get((T, Hq, H, D))
+    if need is None:
+        need = _attend_bytes[T, Hq, H, D] = lib.spec_attend_workspace_bytes(T, Hq, H, D)
+    ws = _ws(workspace, "attend", need, dev, ATTEND_ZERO)
     _call(lib.spec_attend_round, dev, _at(q, dt, "q", dev, shape), _DT[dt], B, T, Hq, kv.data_ptr(), L, N, H, S, D,
           layer, _at(length, _I32, "length", dev, rows), _at(pad, _I32, "pad", dev, rows), _rows(idx, B, N, dev),
           _at(n_nodes, _I32, "n_nodes", dev, rows), _at(tree_mask, torch.int64, "tree_mask", dev, (B, T)),
@@ -250,19 +260,13 @@ def spec_verify_tree(target_logits, tokens, parent, n_nodes=None, eos_id=-1, rem
     if dt not in _DT:
         raise ValueError(f"unsupported logits dtype {dt}")
     rows, nodes = (B,), (B, T)
-    if out_tokens is None and path is None and n_accept is None and n_emit is None and flags is None:
-        # one block for the five outputs
-        block = torch.empty(B * (2 * T + 3), dtype=_I32, device=dev)
-        out_tokens, path, n_accept, n_emit, flags = block.split((B * T, B * T, B, B, B))
-        out_tokens, path = out_tokens.view(nodes), path.view(nodes)
-    else:
-        out_tokens = _out(out_tokens, nodes, _I32, dev, "out_tokens")
-        path = _out(path, nodes, _I32, dev, "path")
-        n_accept = _out(n_accept, rows, _I32, dev, "n_accept")
-        n_emit = _out(n_emit, rows, _I32, dev, "n_emit")
-        flags = _out(flags, rows, _I32, dev, "flags")
+    out_tokens = _out(out_tokens, nodes, _I32, dev, "out_tokens")
+    path = _out(path, nodes, _I32, dev, "path")
+    n_accept = _out(n_accept, rows, _I32, dev, "n_accept")
+    n_emit = _out(n_emit, rows, _I32, dev, "n_emit")
+    flags = _out(flags, rows, _I32, dev, "flags")
     lib = _lib.load()
-    ws = _ws(workspace, "tree", max(256, lib.spec_tree_workspace_bytes(B)), dev, 0)
+    ws = _ws(workspace, "tree", 256 * B, dev, 0)  # at least what the call needs
     _call(lib.spec_verify_tree, dev, target_logits.data_ptr(), _DT[dt], B, T, V, _at(tokens, _I32, "tokens", dev, nodes),
           _at(parent, _I32, "parent", dev, nodes), _at(n_nodes, _I32, "n_nodes", dev, rows), int(eos_id),
           _at(remaining, _I32, "remaining", dev, rows), out_tokens.data_ptr(), path.data_ptr(), n_accept.data_ptr(),
