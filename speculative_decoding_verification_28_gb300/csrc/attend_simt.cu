@@ -1,78 +1,93 @@
 // attend_simt.cu -- attention on the CUDA cores: every storage type, any head
 // size up to SPEC_MAX_HEAD_DIM and any alignment, in fp32 throughout.  It is
 // the form for fp32 caches (the tensor cores have no fp32 product) and for
-// head sizes the tensor-core kernel (attend_tc.cu) has no tile for.
+// head sizes the tensor-core kernels have no tile for.
 //
 //   o_r = sum_j e^(s_rj - m_r) v_j / sum_j e^(s_rj - m_r),  s_rj = scale q_r.k_j
 //
 // over the keys row r sees, in one pass with a running maximum m and sum.
-// A unit has 16 query rows, a tile 64 keys: K and V tiles are brought to
-// shared memory as fp32 once for the 16 rows; a thread forms 2 x 4 scores and
-// 4 rows x 4 columns of the output.  Bound by the FMA pipe from about 20 rows
-// a key head on, by HBM below.
+// A unit has 16 IR query rows, a tile 64 keys.  256 threads stand in 16 x 16:
+// thread (ty, tx) forms the scores of rows IR ty .. and keys tx + 16 j, and
+// the output of the same rows and columns 4 tx + 64 j, so that a row's maximum,
+// sum and rescaling stay with the 16 lanes of its ty.  K and then V take the
+// same shared buffer as fp32, the next of them on its way in registers; the
+// weights pass through shared memory.  IR = 4 is bound by the FMA pipe (64
+// FMAs to 8 shared loads in the scores, 32 to 3 in the output); IR = 1, for up
+// to 16 rows, by shared memory and latency.
 #include "attend_common.cuh"
+#include "verify_common.cuh"
 
 namespace spec {
 
-constexpr int kSimtThreads = 128;
-constexpr int kSimtRows = 16;
+constexpr int kSimtThreads = 256;
 constexpr int kSimtKeys = 64;
+constexpr int kSimtCtas = 2 * kAttendCtas;
 
-// shared memory, in floats: q[16][DP], k[64][DP + 4], v[64][DP], p[64][16];
-// DP = D rounded up to 4 (the +4 spreads a column of keys over the banks)
 __host__ __device__ inline int simt_dp(int D) { return (D + 3) & ~3; }
-inline size_t simt_smem(int D)
+// q[rows][dp], k or v[64][dp + 4], p[64][rows + 4], in floats (the + 4 spread
+// columns over the banks)
+inline size_t simt_smem(int D, int rows)
 {
-    const int dp = simt_dp(D);
-    return sizeof(float) * ((size_t)kSimtRows * dp + (size_t)kSimtKeys * (dp + 4) + (size_t)kSimtKeys * dp +
-                            kSimtKeys * kSimtRows);
+    const size_t dp = simt_dp(D);
+    return sizeof(float) * (rows * dp + kSimtKeys * (dp + 4) + kSimtKeys * (size_t)(rows + 4));
 }
 
-// rows x D elements at src (row step `step`) to fp32 rows of `ld` floats;
-// rows from `have` on and columns from D on are zero
+// four elements from p on as fp32; those from `left` on are zero
 template <typename T>
-__device__ __forceinline__ void load_rows(const T *src, long long step, int have, int rows, int D, float *dst, int ld)
+__device__ __forceinline__ float4 load4(const T *p, int left, bool vec)
 {
-    const int dp = simt_dp(D), quads = dp / 4;
-    const bool vec = D % 4 == 0 && (reinterpret_cast<uintptr_t>(src) % (4 * sizeof(T))) == 0;
-    for (int w = threadIdx.x; w < rows * quads; w += kSimtThreads) {
-        const int r = w / quads, c = (w - r * quads) * 4;
-        float4 f = make_float4(0, 0, 0, 0);
-        if (r < have) {
-            const T *s = src + r * step + c;
-            if (vec) {
-                if constexpr (sizeof(T) == 4) {
-                    f = __ldg(reinterpret_cast<const float4 *>(s));
-                } else {
-                    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(s));
-                    float x[8];
-                    Storage<T>::unpack(make_uint4(u.x, u.y, 0, 0), x);
-                    f = make_float4(x[0], x[1], x[2], x[3]);
-                }
-            } else {
-                f.x = Storage<T>::at(s, 0);
-                f.y = c + 1 < D ? Storage<T>::at(s, 1) : 0.0f;
-                f.z = c + 2 < D ? Storage<T>::at(s, 2) : 0.0f;
-                f.w = c + 3 < D ? Storage<T>::at(s, 3) : 0.0f;
-            }
+    if (vec) {
+        if constexpr (sizeof(T) == 4) {
+            return __ldg(reinterpret_cast<const float4 *>(p));
+        } else {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+            float x[8];
+            Storage<T>::unpack(make_uint4(u.x, u.y, 0, 0), x);
+            return make_float4(x[0], x[1], x[2], x[3]);
         }
-        *reinterpret_cast<float4 *>(dst + (size_t)r * ld + c) = f;
     }
+    float4 f;
+    f.x = Storage<T>::at(p, 0);
+    f.y = left > 1 ? Storage<T>::at(p, 1) : 0.0f;
+    f.z = left > 2 ? Storage<T>::at(p, 2) : 0.0f;
+    f.w = left > 3 ? Storage<T>::at(p, 3) : 0.0f;
+    return f;
 }
 
-// CB: column blocks of 128 of the output (1: D <= 128, 2: D <= 256)
-template <typename T, int CB, bool PROMPT>
-__global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(AttendArgs a)
+template <bool B>
+struct Flag {
+    static constexpr bool value = B;
+};
+
+// maximum / sum over the 16 lanes of a ty
+__device__ __forceinline__ float max16(float x)
 {
+#pragma unroll
+    for (int m = 8; m > 0; m >>= 1)
+        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, m));
+    return x;
+}
+__device__ __forceinline__ float sum16(float x)
+{
+#pragma unroll
+    for (int m = 8; m > 0; m >>= 1)
+        x += __shfl_xor_sync(0xFFFFFFFFu, x, m);
+    return x;
+}
+
+// CB: blocks of 64 columns (D <= 64 CB)
+template <typename T, int IR, int CB, bool PROMPT>
+__global__ void __launch_bounds__(kSimtThreads, CB <= 2 ? 2 : 1) attend_simt_kernel(AttendArgs a)
+{
+    constexpr int ROWS = 16 * IR;
     extern __shared__ __align__(16) float smem[];
     __shared__ uint32_t s_scan[kSimtThreads / 32];
     __shared__ Run s_run;
-    __shared__ float s_f[kSimtRows], s_m[kSimtRows], s_l[kSimtRows];
     __shared__ int s_last;
-    const int D = a.cache.D, dp = simt_dp(D);
-    float *q = smem, *k = q + kSimtRows * dp, *v = k + kSimtKeys * (dp + 4), *p = v + kSimtKeys * dp;
-    const Shape sh{kSimtKeys, kSimtRows, a.G};
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int D = a.cache.D, dp = simt_dp(D), ld = dp + 4;
+    float *q = smem, *kv = q + ROWS * dp, *p = kv + kSimtKeys * ld;
+    const Shape sh{kSimtKeys, ROWS, a.G};
+    const int t = threadIdx.x, tx = t & 15, ty = t >> 4, warp = t >> 5;
 
     AttendUnit u;
     bool have;
@@ -81,6 +96,7 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(AttendArgs a)
     } else {
         if (t == 0)
             s_run.begin = s_run.end = 0;
+        __syncthreads();
         find_run<kSimtThreads>(a, sh, s_scan, &s_run);
         __syncthreads();
     }
@@ -92,166 +108,216 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(AttendArgs a)
         const T *kc = reinterpret_cast<const T *>(a.cache.kv) +
                       (a.cache.k_slab + (long long)u.seq.row * a.cache.H + u.h) * slab + (long long)u.seq.slot0 * D;
         const T *vc = kc + (a.cache.v_slab - a.cache.k_slab) * slab;
-        // query rows: row r at row_place
-        for (int w = t; w < kSimtRows * dp; w += kSimtThreads) {
-            const int r = w / dp, c = w - r * dp;
-            q[w] = r < u.n_rows && c < D
-                       ? Storage<T>::at(reinterpret_cast<const T *>(a.q) + row_place(a, u, r), c) * a.scale_log2
-                       : 0.0f;
+        // K or V of a tile: where its keys are, how many are real
+        struct Src {
+            const T *at;
+            int keys;
+            bool nodes;
+        };
+        auto tile_src = [&](int tile, bool v) -> Src {
+            Src s;
+            s.nodes = !PROMPT && tile == u.n_tiles - 1;
+            s.at = v ? vc : kc;
+            if (s.nodes) {
+                s.keys = u.seq.n;
+                if (a.seq.staged)
+                    s.at = reinterpret_cast<const T *>(a.staged) +
+                           ((v ? a.st_v : a.st_k) + (long long)u.b * a.cache.H + u.h) * a.seq.T * D;
+                else
+                    s.at += (long long)u.seq.prefix * D;
+            } else {
+                s.keys = min(kSimtKeys, (PROMPT ? u.seen_last : u.seq.prefix) - tile * kSimtKeys);
+                s.at += (long long)tile * kSimtKeys * D;
+            }
+            return s;
+        };
+        // this thread's part of a tile: rows ty + 16 j, quads tx + 16 b
+        float4 pre[4 * CB];
+        auto fetch = [&](const Src &s) {
+            const bool vec = D % 4 == 0 && reinterpret_cast<uintptr_t>(s.at) % (4 * sizeof(T)) == 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int b = 0; b < CB; ++b) {
+                    const int r = ty + 16 * j, c = 4 * (tx + 16 * b);
+                    pre[j * CB + b] = r < s.keys && c < D ? load4<T>(s.at + (long long)r * D + c, D - c, vec)
+                                                          : make_float4(0, 0, 0, 0);
+                }
+        };
+        auto put = [&]() {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int b = 0; b < CB; ++b) {
+                    const int c = 4 * (tx + 16 * b);
+                    if (c < dp)
+                        *reinterpret_cast<float4 *>(kv + (ty + 16 * j) * ld + c) = pre[j * CB + b];
+                }
+        };
+        fetch(tile_src(u.tile, false));
+        // query rows, scaled
+        for (int r = ty; r < ROWS; r += 16) {
+            const T *src = reinterpret_cast<const T *>(a.q) + (r < u.n_rows ? row_place(a, u, r) : 0);
+            for (int c = tx; c < dp; c += 16)
+                q[r * dp + c] = r < u.n_rows && c < D ? Storage<T>::at(src, c) * a.scale_log2 : 0.0f;
         }
-        if (t < kSimtRows) {
-            s_m[t] = -INFINITY;
-            s_l[t] = 0.0f;
+        float m[IR], l[IR], acc[IR][4 * CB];
+        uint64_t bits[IR];  // nodes that the row sees
+        int tok[IR];
+#pragma unroll
+        for (int i = 0; i < IR; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4 * CB; ++e)
+                acc[i][e] = 0.0f;
+            const int r = IR * ty + i;
+            tok[i] = (u.row0 + r) / a.G;
+            bits[i] = 0;
+            if (!PROMPT && r < u.n_rows && u.tile_end == u.n_tiles)
+                bits[i] = a.mask ? a.mask[(size_t)u.b * a.seq.T + tok[i]] : (2ull << tok[i]) - 1;
         }
-        float acc[CB][4][4] = {};
-        const int rg = warp * 4;  // rows rg .. rg + 3 of the output and of the softmax
+        put();
         __syncthreads();
         for (int tile = u.tile; tile < u.tile_end; ++tile) {
-            const bool nodes = !PROMPT && tile == u.n_tiles - 1;
-            int keys;  // real keys of the tile; the rest of it is zero
-            const T *ks, *vs;
-            if (nodes) {
-                keys = u.seq.n;
-                if (a.seq.staged) {
-                    const long long at = ((long long)u.b * a.cache.H + u.h) * a.seq.T * D, sl = (long long)a.seq.T * D;
-                    ks = reinterpret_cast<const T *>(a.staged) + a.st_k * sl + at;
-                    vs = reinterpret_cast<const T *>(a.staged) + a.st_v * sl + at;
-                } else {
-                    ks = kc + (long long)u.seq.prefix * D;
-                    vs = vc + (long long)u.seq.prefix * D;
-                }
-            } else {
-                const int k0 = tile * kSimtKeys;
-                const int end = PROMPT ? u.seen_last : u.seq.prefix;
-                keys = min(kSimtKeys, end - k0);
-                ks = kc + (long long)k0 * D;
-                vs = vc + (long long)k0 * D;
+            const Src vs = tile_src(tile, true);
+            fetch(vs);  // V, while the scores form
+            float s[IR][4];
+#pragma unroll
+            for (int i = 0; i < IR; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    s[i][j] = 0.0f;
+#pragma unroll 4
+            for (int c = 0; c < dp; c += 4) {
+                float4 x[IR], y[4];
+#pragma unroll
+                for (int i = 0; i < IR; ++i)
+                    x[i] = *reinterpret_cast<const float4 *>(q + (IR * ty + i) * dp + c);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    y[j] = *reinterpret_cast<const float4 *>(kv + (tx + 16 * j) * ld + c);
+#pragma unroll
+                for (int i = 0; i < IR; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        s[i][j] = fmaf(x[i].x, y[j].x,
+                                       fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, s[i][j]))));
             }
-            load_rows<T>(ks, D, keys, kSimtKeys, D, k, dp + 4);
-            load_rows<T>(vs, D, keys, kSimtKeys, D, v, dp);
-            __syncthreads();
-            // scores: rows 2 (t / 16) + {0, 1}, keys t % 16 + {0, 16, 32, 48}
-            {
-                float s[2][4] = {};
-                const int r0 = (t >> 4) * 2, kk = t & 15;
-                for (int c = 0; c < dp; c += 4) {
-                    const float4 q0 = *reinterpret_cast<const float4 *>(q + r0 * dp + c);
-                    const float4 q1 = *reinterpret_cast<const float4 *>(q + (r0 + 1) * dp + c);
+            // places the row does not see
+            bool hidden = vs.nodes || vs.keys < kSimtKeys;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float4 x = *reinterpret_cast<const float4 *>(k + (kk + 16 * j) * (dp + 4) + c);
-                        s[0][j] = fmaf(q0.x, x.x, fmaf(q0.y, x.y, fmaf(q0.z, x.z, fmaf(q0.w, x.w, s[0][j]))));
-                        s[1][j] = fmaf(q1.x, x.x, fmaf(q1.y, x.y, fmaf(q1.z, x.z, fmaf(q1.w, x.w, s[1][j]))));
-                    }
-                }
+            for (int i = 0; i < IR; ++i) {
+                int lim = vs.keys;
+                if (PROMPT)
+                    lim = min(lim, u.seq.prefix + tok[i] + 1 - tile * kSimtKeys);
+                hidden |= lim < kSimtKeys;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int tok = (u.row0 + r0 + i) / a.G;
-                    int lim = keys;  // keys of this tile the row sees, as a count ...
-                    uint64_t bits = ~0ull;  // ... or as a mask
-                    if (PROMPT)
-                        lim = min(keys, u.seq.prefix + tok + 1 - tile * kSimtKeys);
-                    else if (nodes) {
-                        if (r0 + i < u.n_rows)
-                            bits = a.mask ? a.mask[(size_t)u.b * a.seq.T + tok] : (2ull << tok) - 1;
-                        else
-                            bits = 0;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int key = kk + 16 * j;
-                        p[key * kSimtRows + r0 + i] = key < lim && (bits >> key & 1) ? s[i][j] : -INFINITY;
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const int key = tx + 16 * j;
+                    if (key >= lim || (vs.nodes && !(bits[i] >> key & 1)))
+                        s[i][j] = -INFINITY;
                 }
             }
-            __syncthreads();
-            // softmax: warp w has rows 4 w .. 4 w + 3, lane l keys l and l + 32
+            float w[4][IR];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = rg + i;
-                const float x0 = p[lane * kSimtRows + r], x1 = p[(lane + 32) * kSimtRows + r];
-                float mx = fmaxf(x0, x1);
+            for (int i = 0; i < IR; ++i) {
+                const float mx = fmaxf(m[i], max16(fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]))));
+                const float m0 = mx == -INFINITY ? 0.0f : mx;  // nothing seen yet: every weight is 0
+                const float f = exp2f(m[i] - m0);
+                m[i] = mx;
+                float sum = 0.0f;
 #pragma unroll
-                for (int m = 16; m > 0; m >>= 1)
-                    mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, m));
-                const float m_old = s_m[r], m_new = fmaxf(m_old, mx);
-                const float m0 = m_new == -INFINITY ? 0.0f : m_new;  // nothing seen yet: every weight is 0
-                // a place that is not seen has weight 0, whatever its score
-                const float e0 = exp2f(x0 - m0), e1 = exp2f(x1 - m0);
-                p[lane * kSimtRows + r] = e0;
-                p[(lane + 32) * kSimtRows + r] = e1;
-                float sum = e0 + e1;
-#pragma unroll
-                for (int m = 16; m > 0; m >>= 1)
-                    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
-                __syncwarp();
-                if (lane == 0) {
-                    const float f = exp2f(m_old - m0);
-                    s_f[r] = f;
-                    s_l[r] = fmaf(s_l[r], f, sum);
-                    s_m[r] = m_new;
+                for (int j = 0; j < 4; ++j) {
+                    w[j][i] = exp2f(s[i][j] - m0);
+                    sum += w[j][i];
                 }
+                l[i] = fmaf(l[i], f, sum16(sum));
+#pragma unroll
+                for (int e = 0; e < 4 * CB; ++e)
+                    acc[i][e] *= f;
             }
-            __syncwarp();
-            // output: the same rows, columns 4 lane + 128 cb ..; a weight of 0
-            // takes nothing, so a value that is not finite stays with the rows
-            // that see it
-            float f[4];
+            __syncthreads();  // K has been read
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                f[i] = s_f[rg + i];
+            for (int j = 0; j < 4; ++j) {
+                float *dst = p + (tx + 16 * j) * (ROWS + 4) + IR * ty;
+                if constexpr (IR == 4)
+                    *reinterpret_cast<float4 *>(dst) = make_float4(w[j][0], w[j][1], w[j][2], w[j][3]);
+                else
+                    dst[0] = w[j][0];
+            }
+            put();
+            if (tile + 1 < u.tile_end)
+                fetch(tile_src(tile + 1, false));  // the next K, while the output forms
+            const bool any_hidden = __syncthreads_or(hidden);
+            auto product = [&](auto guarded) {
+#pragma unroll 4
+                for (int key = 0; key < vs.keys; ++key) {
+                    float ww[IR];
+                    if constexpr (IR == 4) {
+                        const float4 x = *reinterpret_cast<const float4 *>(p + key * (ROWS + 4) + 4 * ty);
+                        ww[0] = x.x;
+                        ww[1] = x.y;
+                        ww[2] = x.z;
+                        ww[3] = x.w;
+                    } else {
+                        ww[0] = p[key * (ROWS + 4) + ty];
+                    }
 #pragma unroll
-            for (int cb = 0; cb < CB; ++cb)
+                    for (int b = 0; b < CB; ++b) {
+                        const int c = 4 * (tx + 16 * b);
+                        if (CB * 64 > dp && c >= dp)
+                            continue;
+                        const float4 x = *reinterpret_cast<const float4 *>(kv + key * ld + c);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        acc[cb][i][e] *= f[i];
-            for (int key = 0; key < keys; ++key) {
-                const float4 w = *reinterpret_cast<const float4 *>(p + key * kSimtRows + rg);
-#pragma unroll
-                for (int cb = 0; cb < CB; ++cb) {
-                    const int c = 4 * lane + 128 * cb;
-                    if (c < dp) {
-                        const float4 x = *reinterpret_cast<const float4 *>(v + (size_t)key * dp + c);
-                        const float ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (ww[i] != 0.0f) {
-                                acc[cb][i][0] = fmaf(ww[i], x.x, acc[cb][i][0]);
-                                acc[cb][i][1] = fmaf(ww[i], x.y, acc[cb][i][1]);
-                                acc[cb][i][2] = fmaf(ww[i], x.z, acc[cb][i][2]);
-                                acc[cb][i][3] = fmaf(ww[i], x.w, acc[cb][i][3]);
+                        for (int i = 0; i < IR; ++i) {
+                            // a weight of 0 takes nothing where some rows do not
+                            // see the key: its value may be anything
+                            if (!decltype(guarded)::value || ww[i] != 0.0f) {
+                                acc[i][4 * b] = fmaf(ww[i], x.x, acc[i][4 * b]);
+                                acc[i][4 * b + 1] = fmaf(ww[i], x.y, acc[i][4 * b + 1]);
+                                acc[i][4 * b + 2] = fmaf(ww[i], x.z, acc[i][4 * b + 2]);
+                                acc[i][4 * b + 3] = fmaf(ww[i], x.w, acc[i][4 * b + 3]);
                             }
                         }
                     }
                 }
+            };
+            if (any_hidden)
+                product(Flag<true>{});
+            else
+                product(Flag<false>{});
+            __syncthreads();  // V and the weights have been read
+            if (tile + 1 < u.tile_end) {
+                put();
+                __syncthreads();
             }
-            __syncthreads();
         }
         const bool whole = u.n_parts == 1;
-        float *slot = whole ? nullptr : part_slot<kSimtRows>(a, blockIdx.x, u.part);
+        float *slot = whole ? nullptr : part_slot<ROWS>(a, blockIdx.x, u.part);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = rg + i;
+        for (int i = 0; i < IR; ++i) {
+            const int r = IR * ty + i;
             if (r >= u.n_rows)
                 continue;
-            const float l = s_l[r], inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+            const float f = !whole ? 1.0f : l[i] > 0.0f || l[i] != l[i] ? 1.0f / l[i] : 0.0f;
+            T *dst = reinterpret_cast<T *>(a.out) + row_place(a, u, r);
 #pragma unroll
-            for (int cb = 0; cb < CB; ++cb)
+            for (int b = 0; b < CB; ++b) {
+                const int c = 4 * (tx + 16 * b);
+                if (whole) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int c = 4 * lane + 128 * cb + e;
-                    if (c < D) {
-                        if (whole)
-                            reinterpret_cast<T *>(a.out)[row_place(a, u, r) + c] = round_to<T>(acc[cb][i][e] * inv);
-                        else
-                            __stcg(slot + (size_t)r * dp + c, acc[cb][i][e]);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (c + e < D)
+                            dst[c + e] = round_to<T>(acc[i][4 * b + e] * f);
+                } else if (c < dp) {
+                    __stcg(reinterpret_cast<float4 *>(slot + (size_t)r * dp + c),
+                           make_float4(acc[i][4 * b], acc[i][4 * b + 1], acc[i][4 * b + 2], acc[i][4 * b + 3]));
                 }
-            if (!whole && lane == 0) {
-                __stcg(slot + (size_t)kSimtRows * dp + r, s_m[r]);
-                __stcg(slot + (size_t)kSimtRows * dp + kSimtRows + r, l);
+            }
+            if (!whole && tx == 0) {
+                __stcg(slot + (size_t)ROWS * dp + r, m[i]);
+                __stcg(slot + (size_t)ROWS * dp + ROWS + r, l[i]);
             }
         }
         if (!whole) {
@@ -266,10 +332,10 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(AttendArgs a)
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                join_parts<T, kSimtRows>(a, u, warp, kSimtThreads / 32);
+                join_parts<T, ROWS>(a, u, warp, kSimtThreads / 32);
             }
         }
-        __syncthreads();  // q, s_l and s_last are rewritten next
+        __syncthreads();  // q, kv and s_last are rewritten next
         if constexpr (PROMPT)
             have = false;
         else
@@ -277,34 +343,43 @@ __global__ void __launch_bounds__(kSimtThreads) attend_simt_kernel(AttendArgs a)
     }
 }
 
-template <typename T, int CB, bool PROMPT>
+template <typename T, int IR, int CB, bool PROMPT>
 cudaError_t launch_simt(const AttendArgs &a, cudaStream_t st)
 {
-    const size_t smem = simt_smem(a.cache.D);
-    cudaError_t e = cudaFuncSetAttribute(attend_simt_kernel<T, CB, PROMPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    constexpr int ROWS = 16 * IR;
+    const size_t smem = simt_smem(a.cache.D, ROWS);
+    cudaError_t e = cudaFuncSetAttribute(attend_simt_kernel<T, IR, CB, PROMPT>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
-    dim3 grid(kAttendCtas);
+    dim3 grid(kSimtCtas);
     if (PROMPT) {
-        const long long units = ((long long)a.seq.M * a.G + kSimtRows - 1) / kSimtRows + a.seq.B;
+        const long long units = (long long)a.seq.M * a.G / ROWS + a.seq.B;
         grid = dim3((unsigned)units, (unsigned)a.cache.H);
     }
-    attend_simt_kernel<T, CB, PROMPT><<<grid, kSimtThreads, smem, st>>>(a);
+    attend_simt_kernel<T, IR, CB, PROMPT><<<grid, kSimtThreads, smem, st>>>(a);
     return cudaGetLastError();
+}
+
+template <typename T, int CB>
+cudaError_t launch_simt_cb(const AttendArgs &a, cudaStream_t st)
+{
+    if (a.seq.cu)
+        return launch_simt<T, 4, CB, true>(a, st);
+    return a.seq.T * a.G <= 16 ? launch_simt<T, 1, CB, false>(a, st) : launch_simt<T, 4, CB, false>(a, st);
 }
 
 template <typename T>
 cudaError_t launch_simt_t(const AttendArgs &a, cudaStream_t st)
 {
-    if (a.cache.D <= 128)
-        return a.seq.cu ? launch_simt<T, 1, true>(a, st) : launch_simt<T, 1, false>(a, st);
-    return a.seq.cu ? launch_simt<T, 2, true>(a, st) : launch_simt<T, 2, false>(a, st);
+    if (a.cache.D <= 64)
+        return launch_simt_cb<T, 1>(a, st);
+    return a.cache.D <= 128 ? launch_simt_cb<T, 2>(a, st) : launch_simt_cb<T, 4>(a, st);
 }
 
 size_t attend_workspace(int T, int Hq, int H, int D)
 {
-    const size_t simt = align256(kPartHead + 2 * kAttendCtas * part_floats<kSimtRows>(D) * sizeof(float));
+    const size_t simt = align256(kPartHead + 2 * kSimtCtas * part_floats<64>(D) * sizeof(float));
     const size_t tc = D == 64 || D == 128 ? attend_tc_workspace(T, Hq, H, D) : 0;
     return simt > tc ? simt : tc;
 }
