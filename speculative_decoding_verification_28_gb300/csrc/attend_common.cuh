@@ -188,8 +188,9 @@ struct UnitWalk {
 // ---------------------------------------------------------------------------
 // [counters: one per CTA, zero between calls] [slots: two per CTA, one for the
 // unit that it finishes for others or passes on, one for the unit that starts
-// in it and is cut]; a slot is ROWS rows of sums (D rounded up to 4), ROWS
-// maxima (base 2), ROWS sums of weights.
+// in it and is cut]; a slot is the sums, four columns of all ROWS rows after
+// another (threads that hold a row each then write and read side by side), ROWS
+// maxima (base 2) and ROWS sums of weights.
 constexpr size_t kPartHead = SPEC_ATTEND_ZERO;
 static_assert(2 * kAttendCtas * sizeof(int) <= kPartHead, "one counter per CTA");
 __host__ __device__ inline int part_cols(int D) { return (D + 3) & ~3; }
@@ -203,6 +204,12 @@ __device__ __forceinline__ float *part_slot(const AttendArgs &a, int cta, int pa
 {
     float *slots = reinterpret_cast<float *>(static_cast<char *>(a.ws) + kPartHead);
     return slots + (size_t)(2 * cta + (part == 0 ? 1 : 0)) * part_floats<ROWS>(a.cache.D);
+}
+// place of columns 4 q .. 4 q + 3 of a row in a slot, in floats
+template <int ROWS>
+__device__ __forceinline__ size_t part_quad(int q, int row)
+{
+    return ((size_t)q * ROWS + row) * 4;
 }
 __device__ __forceinline__ int *part_counter(const AttendArgs &a, int cta)
 {
@@ -278,96 +285,79 @@ __device__ inline bool prompt_unit(const AttendArgs &a, const Shape &sh, AttendU
 }
 
 // Joins a unit's parts: O = sum 2^(m_p - m) O_p / sum 2^(m_p - m) l_p.  Called
-// by whole warps, of which this is warp w of `warps`, after every part was
-// seen.  A warp takes JOIN_ROWS rows at a time: lane p has the maximum and the
-// sum of part p, lane l four columns of the output; the loads of all rows are
-// in flight together, since the time of a join is their latency (a thread that
-// took one row's parts after another needed 8 to 35 us where a unit of 36 to
-// 252 rows is cut; this form 1 to 4).  A row that no part saw anything for
-// (every l zero) gives zeros.
-constexpr int kJoinRows = 4;
+// by all `threads` threads of which this is t, after every part was seen.  A
+// thread takes 16 columns of a row; what a join costs is its loads' latency,
+// so those of a part are in flight together, and the first part's before the
+// maxima are known.  A row that no part saw anything for (every l zero) gives
+// zeros.
 template <typename T, int ROWS>
-__device__ void join_parts(const AttendArgs &a, const AttendUnit &u, int w, int warps)
+__device__ void join_parts(const AttendArgs &a, const AttendUnit &u, int t, int threads)
 {
-    const int D = a.cache.D, dp = part_cols(D), lane = threadIdx.x & 31;
+    const int D = a.cache.D, dp = part_cols(D), quads = dp / 4, groups = (quads + 3) / 4;
     T *out = reinterpret_cast<T *>(a.out);
-    for (int r0 = w * kJoinRows; r0 < u.n_rows; r0 += warps * kJoinRows)
-        for (int c0 = 0; c0 < dp; c0 += 128) {
-            const int c = c0 + lane * 4;
-            const bool mine = c < dp;
-            float o[kJoinRows][4] = {}, m[kJoinRows], l[kJoinRows];
+    for (int w = t; w < u.n_rows * groups; w += threads) {
+        const int g = w / u.n_rows, r = w - g * u.n_rows, q0 = 4 * g;
+        auto sums = [&](int p, float4 *x) {
+            const float4 *slot = reinterpret_cast<const float4 *>(part_slot<ROWS>(a, u.first_cta + p, p)) + r;
 #pragma unroll
-            for (int i = 0; i < kJoinRows; ++i) {
-                m[i] = -INFINITY;
-                l[i] = 0.0f;
-            }
-            for (int p0 = 0; p0 < u.n_parts; p0 += 32) {
-                const int p = p0 + lane, np = min(32, u.n_parts - p0);
-                float wt[kJoinRows], mp[kJoinRows], lp[kJoinRows];
-                const float *slot = p < u.n_parts ? part_slot<ROWS>(a, u.first_cta + p, p) + (size_t)ROWS * dp : nullptr;
+            for (int k = 0; k < 4; ++k)
+                x[k] = q0 + k < quads ? __ldcg(slot + (size_t)(q0 + k) * ROWS) : make_float4(0, 0, 0, 0);
+        };
+        float4 x[2][4];
+        sums(0, x[0]);
+        sums(1, x[1]);
+        float m = -INFINITY;
+#pragma unroll 4
+        for (int p = 0; p < u.n_parts; ++p)
+            m = fmaxf(m, __ldcg(part_slot<ROWS>(a, u.first_cta + p, p) + (size_t)ROWS * dp + r));
+        const float m0 = m == -INFINITY ? 0.0f : m;
+        float o[16] = {}, l = 0.0f;
+        for (int p0 = 0; p0 < u.n_parts; p0 += 2) {
+            float f[2], lp[2];
 #pragma unroll
-                for (int i = 0; i < kJoinRows; ++i) {
-                    const bool in = slot && r0 + i < u.n_rows;
-                    mp[i] = in ? __ldcg(slot + r0 + i) : -INFINITY;
-                    lp[i] = in ? __ldcg(slot + ROWS + r0 + i) : 0.0f;
-                }
-                for (int j0 = 0; j0 < np; j0 += 2) {
-                    float4 x[2][kJoinRows];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int pj = p0 + min(j0 + j, np - 1);
-                        const float *from = part_slot<ROWS>(a, u.first_cta + pj, pj) + (size_t)r0 * dp + c;
-#pragma unroll
-                        for (int i = 0; i < kJoinRows; ++i)
-                            x[j][i] = mine && r0 + i < u.n_rows ? __ldcg(reinterpret_cast<const float4 *>(from + i * dp))
-                                                                : make_float4(0, 0, 0, 0);
-                    }
-                    if (j0 == 0) {  // the weights, with the first sums in flight
-#pragma unroll
-                        for (int i = 0; i < kJoinRows; ++i) {
-                            float mx = mp[i];
-                            for (int k = 1; k < np; k <<= 1)
-                                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, k));
-                            mx = fmaxf(__shfl_sync(0xFFFFFFFFu, mx, 0), m[i]);
-                            const float m0 = mx == -INFINITY ? 0.0f : mx, f = exp2f(m[i] - m0);
-                            m[i] = mx;
-                            wt[i] = exp2f(mp[i] - m0);
-                            float ls = wt[i] * lp[i];
-                            for (int k = 1; k < np; k <<= 1)
-                                ls += __shfl_xor_sync(0xFFFFFFFFu, ls, k);
-                            l[i] = fmaf(l[i], f, __shfl_sync(0xFFFFFFFFu, ls, 0));
-                            if (p0 > 0)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    o[i][e] *= f;
-                        }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int i = 0; i < kJoinRows; ++i) {
-                            const float f = __shfl_sync(0xFFFFFFFFu, wt[i], j0 + j);
-                            if (j0 + j < np) {
-                                o[i][0] = fmaf(f, x[j][i].x, o[i][0]);
-                                o[i][1] = fmaf(f, x[j][i].y, o[i][1]);
-                                o[i][2] = fmaf(f, x[j][i].z, o[i][2]);
-                                o[i][3] = fmaf(f, x[j][i].w, o[i][3]);
-                            }
-                        }
-                }
+            for (int j = 0; j < 2; ++j) {
+                const int p = min(p0 + j, u.n_parts - 1);
+                const float *slot = part_slot<ROWS>(a, u.first_cta + p, p) + (size_t)ROWS * dp + r;
+                f[j] = p0 + j < u.n_parts ? exp2f(__ldcg(slot) - m0) : 0.0f;
+                lp[j] = __ldcg(slot + ROWS);
+                if (p0 > 0)
+                    sums(p, x[j]);
             }
 #pragma unroll
-            for (int i = 0; i < kJoinRows; ++i) {
-                if (r0 + i >= u.n_rows || !mine)
+            for (int j = 0; j < 2; ++j) {
+                if (p0 + j >= u.n_parts)
                     continue;
-                const float inv = l[i] > 0.0f || l[i] != l[i] ? 1.0f / l[i] : 0.0f;
-                T *dst = out + row_place(a, u, r0 + i) + c;
+                l = fmaf(f[j], lp[j], l);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (c + e < D)
-                        dst[e] = round_to<T>(o[i][e] * inv);
+                for (int k = 0; k < 4; ++k) {
+                    o[4 * k] = fmaf(f[j], x[j][k].x, o[4 * k]);
+                    o[4 * k + 1] = fmaf(f[j], x[j][k].y, o[4 * k + 1]);
+                    o[4 * k + 2] = fmaf(f[j], x[j][k].z, o[4 * k + 2]);
+                    o[4 * k + 3] = fmaf(f[j], x[j][k].w, o[4 * k + 3]);
+                }
             }
         }
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        T *dst = out + row_place(a, u, r) + 16 * g;
+        if (D % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0) {
+            T v[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                v[e] = round_to<T>(o[e] * inv);
+            constexpr int N = sizeof(T);
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                uint4 y;
+                memcpy(&y, v + 16 / N * k, 16);
+                reinterpret_cast<uint4 *>(dst)[k] = y;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (16 * g + e < D)
+                    dst[e] = round_to<T>(o[e] * inv);
+        }
+    }
 }
 
 }  // namespace spec

@@ -363,19 +363,11 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     if (!real)
                         continue;
                     if (whole) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint4 w;
-                            w.x = TcType<T>::pack(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f);
-                            w.y = TcType<T>::pack(__uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
-                            w.z = TcType<T>::pack(__uint_as_float(o[e + 4]) * f, __uint_as_float(o[e + 5]) * f);
-                            w.w = TcType<T>::pack(__uint_as_float(o[e + 6]) * f, __uint_as_float(o[e + 7]) * f);
-                            *reinterpret_cast<uint4 *>(dst + k + e) = w;
-                        }
+                        store_row32<T>(dst + k, o, f);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            __stcg(reinterpret_cast<uint4 *>(slot + (size_t)r * D + k + e),
+                            __stcg(reinterpret_cast<uint4 *>(slot + part_quad<kFewRows>((k + e) / 4, r)),
                                    make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
                     }
                 }
@@ -407,7 +399,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     break;
                 if (s.last) {
                     __threadfence();
-                    join_parts<T, kFewRows>(a, u, warp, 4);
+                    join_parts<T, kFewRows>(a, u, tid, 128);
                 }
             }
             ++n;

@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kSimtThreads, CB <= 2 ? 2 : 1) attend_simt_ker
     const int D = a.cache.D, dp = simt_dp(D), ld = dp + 4;
     float *q = smem, *kv = q + ROWS * dp, *p = kv + kSimtKeys * ld;
     const Shape sh{kSimtKeys, ROWS, a.G};
-    const int t = threadIdx.x, tx = t & 15, ty = t >> 4, warp = t >> 5;
+    const int t = threadIdx.x, tx = t & 15, ty = t >> 4;
 
     AttendUnit u;
     bool have;
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(kSimtThreads, CB <= 2 ? 2 : 1) attend_simt_ker
                         if (c + e < D)
                             dst[c + e] = round_to<T>(acc[i][4 * b + e] * f);
                 } else if (c < dp) {
-                    __stcg(reinterpret_cast<float4 *>(slot + (size_t)r * dp + c),
+                    __stcg(reinterpret_cast<float4 *>(slot + part_quad<ROWS>(c / 4, r)),
                            make_float4(acc[i][4 * b], acc[i][4 * b + 1], acc[i][4 * b + 2], acc[i][4 * b + 3]));
                 }
             }
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kSimtThreads, CB <= 2 ? 2 : 1) attend_simt_ker
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                join_parts<T, ROWS>(a, u, warp, kSimtThreads / 32);
+                join_parts<T, ROWS>(a, u, t, kSimtThreads);
             }
         }
         __syncthreads();  // q, kv and s_last are rewritten next

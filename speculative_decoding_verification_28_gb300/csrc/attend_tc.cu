@@ -39,7 +39,7 @@ struct TcShape {
     static constexpr int kStages = D == 128 ? 5 : 8;
     static constexpr int kSmem = (kQBuf * NT + kStages) * kTile + 1024;
     static constexpr int kSoftmax = 128 * NT;
-    static constexpr int kThreads = kSoftmax + 96;
+    static constexpr int kThreads = kSoftmax + (NT == 2 ? 128 : 96);  // NT = 2: whole warpgroups, see below
     static constexpr int kRows = 128 * NT;
     static constexpr uint32_t kTmemO = 256;
 };
@@ -159,6 +159,12 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
+        // A round's walk over units costs the softmax warps registers: 384
+        // threads launch with 168 each (64512), those keep 208 and the others
+        // 80 (256 * 208 + 128 * 80 = 63488); 149 -> 135 us for trees of 64
+        // nodes and 7 heads.  A prompt's one unit fits 168.
+        if constexpr (NT == 2 && !PROMPT)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (lane == 0) {
             uint32_t it = 0, n = 0;
             bool ok = true;
@@ -207,6 +213,8 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
         __syncwarp();
     } else if (warp == kMmaWarp) {
         // -------------------------------------------------------------- mma
+        if constexpr (NT == 2 && !PROMPT)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         const uint32_t ideo = tc_idesc<T>(D, true);
         uint32_t ok_ph = 0;  // per stage: parity of its guarded uses
         auto wait_guard = [&](int sg) -> bool {
@@ -345,8 +353,13 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                 ++nq;
             }
         }
+    } else if (warp == kLoadWarp + 2) {  // completes the warpgroup
+        if constexpr (NT == 2 && !PROMPT)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     } else if (warp == kLoadWarp + 1) {
         // ------------------------------------------------------------ guard
+        if constexpr (NT == 2 && !PROMPT)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         uint32_t i = 0, n = 0;
         bool ok = true;
         while (ok && units.next(u)) {
@@ -384,6 +397,8 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
         }
     } else {
         // ---------------------------------------------------------- softmax
+        if constexpr (NT == 2 && !PROMPT)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int t = NT == 1 ? 0 : warp >> 2;
         const int r = (warp & 3) * 32 + lane;        // row of the tile = TMEM lane
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
@@ -588,19 +603,11 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                         }
                         if (real) {
                             if (whole) {
-#pragma unroll
-                                for (int e = 0; e < 32; e += 8) {
-                                    uint4 w;
-                                    w.x = TcType<T>::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv);
-                                    w.y = TcType<T>::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-                                    w.z = TcType<T>::pack(__uint_as_float(o[e + 4]) * inv, __uint_as_float(o[e + 5]) * inv);
-                                    w.w = TcType<T>::pack(__uint_as_float(o[e + 6]) * inv, __uint_as_float(o[e + 7]) * inv);
-                                    *reinterpret_cast<uint4 *>(dst + 32 * k + e) = w;
-                                }
+                                store_row32<T>(dst + 32 * k, o, inv);
                             } else {
 #pragma unroll
                                 for (int e = 0; e < 32; e += 4)
-                                    __stcg(reinterpret_cast<uint4 *>(slot + (size_t)ur * D + 32 * k + e),
+                                    __stcg(reinterpret_cast<uint4 *>(slot + part_quad<Sh::kRows>(8 * k + e / 4, ur)),
                                            make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
                             }
                         }
@@ -631,7 +638,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                     break;
                 if (s.last) {
                     __threadfence();
-                    join_parts<T, Sh::kRows>(a, u, warp, Sh::kSoftmax / 32);
+                    join_parts<T, Sh::kRows>(a, u, tid, Sh::kSoftmax);
                 }
             }
             ++n;

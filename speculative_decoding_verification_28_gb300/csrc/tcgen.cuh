@@ -236,6 +236,28 @@ struct TcType<__half> {
     static constexpr uint32_t kExp = 0x7C00u;
 };
 
+// 32 columns of a row times f, rounded, to 16-byte aligned dst.  A thread
+// writes a row of its own, so whole 32-byte sectors at a time where it may.
+template <typename T>
+__device__ __forceinline__ void store_row32(T *dst, const uint32_t *o, float f)
+{
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+        w[e] = TcType<T>::pack(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
+    if (reinterpret_cast<uintptr_t>(dst) % 32 == 0) {
+#pragma unroll
+        for (int e = 0; e < 16; e += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 2 * e), SPEC_IN4(w, e),
+                         SPEC_IN4(w, e + 4)
+                         : "memory");
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<uint4 *>(dst + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+    }
+}
+
 // instruction descriptor: fp32 accumulators, both operands T, M = 128
 template <typename T>
 __device__ __forceinline__ uint32_t tc_idesc(int n, bool b_rows_summed, bool a_rows_summed = false)
