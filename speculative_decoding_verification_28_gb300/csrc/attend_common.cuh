@@ -285,65 +285,75 @@ __device__ inline bool prompt_unit(const AttendArgs &a, const Shape &sh, AttendU
 }
 
 // Joins a unit's parts: O = sum 2^(m_p - m) O_p / sum 2^(m_p - m) l_p.  Called
-// by all `threads` threads of which this is t, after every part was seen.  A
-// thread takes 16 columns of a row; what a join costs is its loads' latency,
-// so those of a part are in flight together, and the first part's before the
-// maxima are known.  A row that no part saw anything for (every l zero) gives
-// zeros.
-template <typename T, int ROWS>
-__device__ void join_parts(const AttendArgs &a, const AttendUnit &u, int t, int threads)
+// by all `threads` threads of which this is t, after every part was seen;
+// `sync` is a barrier among them that orders their writes to the workspace
+// (false: it gave up).  A thread joins 16 columns of a row at a time; what that
+// costs is its loads' latency.  Where a thread has many to join, every row's
+// factors are formed first, in place of the parts' maxima, which leaves one
+// round of loads each (252 rows: 18000 -> 8000 cycles); where it has few, the
+// factors come with the sums (4 rows: two rounds and no barrier).  A row that
+// no part saw anything for (every l zero) gives zeros.
+template <typename T, int ROWS, typename Sync>
+__device__ bool join_parts(const AttendArgs &a, const AttendUnit &u, int t, int threads, Sync sync)
 {
     const int D = a.cache.D, dp = part_cols(D), quads = dp / 4, groups = (quads + 3) / 4;
     T *out = reinterpret_cast<T *>(a.out);
-    for (int w = t; w < u.n_rows * groups; w += threads) {
-        const int g = w / u.n_rows, r = w - g * u.n_rows, q0 = 4 * g;
-        auto sums = [&](int p, float4 *x) {
-            const float4 *slot = reinterpret_cast<const float4 *>(part_slot<ROWS>(a, u.first_cta + p, p)) + r;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                x[k] = q0 + k < quads ? __ldcg(slot + (size_t)(q0 + k) * ROWS) : make_float4(0, 0, 0, 0);
-        };
-        float4 x[2][4];
-        sums(0, x[0]);
-        sums(1, x[1]);
+    auto stats = [&](int p) { return part_slot<ROWS>(a, u.first_cta + p, p) + (size_t)ROWS * dp; };
+    // a row's maximum and the inverse of its sum
+    auto whole_row = [&](int r, float &m0, float &inv) {
         float m = -INFINITY;
 #pragma unroll 4
         for (int p = 0; p < u.n_parts; ++p)
-            m = fmaxf(m, __ldcg(part_slot<ROWS>(a, u.first_cta + p, p) + (size_t)ROWS * dp + r));
-        const float m0 = m == -INFINITY ? 0.0f : m;
-        float o[16] = {}, l = 0.0f;
-        for (int p0 = 0; p0 < u.n_parts; p0 += 2) {
-            float f[2], lp[2];
+            m = fmaxf(m, __ldcg(stats(p) + r));
+        m0 = m == -INFINITY ? 0.0f : m;
+        float l = 0.0f;
+#pragma unroll 4
+        for (int p = 0; p < u.n_parts; ++p)
+            l = fmaf(exp2f(__ldcg(stats(p) + r) - m0), __ldcg(stats(p) + ROWS + r), l);
+        inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    };
+    const bool many = u.n_rows * groups > 4 * threads;
+    if (many) {
+        for (int r = t; r < u.n_rows; r += threads) {
+            float m0, inv;
+            whole_row(r, m0, inv);
+#pragma unroll 4
+            for (int p = 0; p < u.n_parts; ++p)
+                __stcg(stats(p) + r, exp2f(__ldcg(stats(p) + r) - m0) * inv);
+        }
+        if (!sync())
+            return false;
+    }
+    for (int w = t; w < u.n_rows * groups; w += threads) {
+        const int g = w / u.n_rows, r = w - g * u.n_rows, q0 = 4 * g;
+        float o[16] = {}, m0 = 0.0f, inv = 1.0f;
+        if (!many)
+            whole_row(r, m0, inv);
+#pragma unroll 2
+        for (int p = 0; p < u.n_parts; ++p) {
+            const float *slot = part_slot<ROWS>(a, u.first_cta + p, p);
+            float f = __ldcg(slot + (size_t)ROWS * dp + r);
+            if (!many)
+                f = exp2f(f - m0) * inv;
+            float4 x[4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int p = min(p0 + j, u.n_parts - 1);
-                const float *slot = part_slot<ROWS>(a, u.first_cta + p, p) + (size_t)ROWS * dp + r;
-                f[j] = p0 + j < u.n_parts ? exp2f(__ldcg(slot) - m0) : 0.0f;
-                lp[j] = __ldcg(slot + ROWS);
-                if (p0 > 0)
-                    sums(p, x[j]);
-            }
+            for (int k = 0; k < 4; ++k)
+                x[k] = q0 + k < quads ? __ldcg(reinterpret_cast<const float4 *>(slot + part_quad<ROWS>(q0 + k, r)))
+                                      : make_float4(0, 0, 0, 0);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if (p0 + j >= u.n_parts)
-                    continue;
-                l = fmaf(f[j], lp[j], l);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    o[4 * k] = fmaf(f[j], x[j][k].x, o[4 * k]);
-                    o[4 * k + 1] = fmaf(f[j], x[j][k].y, o[4 * k + 1]);
-                    o[4 * k + 2] = fmaf(f[j], x[j][k].z, o[4 * k + 2]);
-                    o[4 * k + 3] = fmaf(f[j], x[j][k].w, o[4 * k + 3]);
-                }
+            for (int k = 0; k < 4; ++k) {
+                o[4 * k] = fmaf(f, x[k].x, o[4 * k]);
+                o[4 * k + 1] = fmaf(f, x[k].y, o[4 * k + 1]);
+                o[4 * k + 2] = fmaf(f, x[k].z, o[4 * k + 2]);
+                o[4 * k + 3] = fmaf(f, x[k].w, o[4 * k + 3]);
             }
         }
-        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
         T *dst = out + row_place(a, u, r) + 16 * g;
         if (D % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0) {
             T v[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-                v[e] = round_to<T>(o[e] * inv);
+                v[e] = round_to<T>(o[e]);
             constexpr int N = sizeof(T);
 #pragma unroll
             for (int k = 0; k < N; ++k) {
@@ -355,9 +365,10 @@ __device__ void join_parts(const AttendArgs &a, const AttendUnit &u, int t, int 
 #pragma unroll
             for (int e = 0; e < 16; ++e)
                 if (16 * g + e < D)
-                    dst[e] = round_to<T>(o[e] * inv);
+                    dst[e] = round_to<T>(o[e]);
         }
     }
+    return true;
 }
 
 }  // namespace spec

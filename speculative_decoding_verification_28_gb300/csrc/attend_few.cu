@@ -399,7 +399,15 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     break;
                 if (s.last) {
                     __threadfence();
-                    join_parts<T, kFewRows>(a, u, tid, 128);
+                    ok = join_parts<T, kFewRows>(a, u, tid, 128, [&] {
+                        __threadfence();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&s.joined);
+                        return wait(&s.joined, joins++ & 1);
+                    });
+                    if (!ok)
+                        break;
                 }
             }
             ++n;

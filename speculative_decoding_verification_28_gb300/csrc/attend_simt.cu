@@ -332,7 +332,11 @@ __global__ void __launch_bounds__(kSimtThreads, CB <= 2 ? 2 : 1) attend_simt_ker
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                join_parts<T, ROWS>(a, u, t, kSimtThreads);
+                join_parts<T, ROWS>(a, u, t, kSimtThreads, [] {
+                    __threadfence();
+                    __syncthreads();
+                    return true;
+                });
             }
         }
         __syncthreads();  // q, kv and s_last are rewritten next

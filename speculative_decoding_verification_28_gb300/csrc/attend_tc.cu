@@ -160,11 +160,11 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
         // A round's walk over units costs the softmax warps registers: 384
-        // threads launch with 168 each (64512), those keep 208 and the others
-        // 80 (256 * 208 + 128 * 80 = 63488); 149 -> 135 us for trees of 64
-        // nodes and 7 heads.  A prompt's one unit fits 168.
+        // threads launch with 168 each (64512), those keep 200 and the others
+        // 104 (256 * 200 + 128 * 104 = 64512); 149 -> 135 us for trees of 64
+        // nodes and 7 heads (208 and 80: 5% slower than this).  A prompt's one unit fits 168.
         if constexpr (NT == 2 && !PROMPT)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (lane == 0) {
             uint32_t it = 0, n = 0;
             bool ok = true;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
     } else if (warp == kMmaWarp) {
         // -------------------------------------------------------------- mma
         if constexpr (NT == 2 && !PROMPT)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         const uint32_t ideo = tc_idesc<T>(D, true);
         uint32_t ok_ph = 0;  // per stage: parity of its guarded uses
         auto wait_guard = [&](int sg) -> bool {
@@ -355,11 +355,11 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
         }
     } else if (warp == kLoadWarp + 2) {  // completes the warpgroup
         if constexpr (NT == 2 && !PROMPT)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     } else if (warp == kLoadWarp + 1) {
         // ------------------------------------------------------------ guard
         if constexpr (NT == 2 && !PROMPT)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         uint32_t i = 0, n = 0;
         bool ok = true;
         while (ok && units.next(u)) {
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
     } else {
         // ---------------------------------------------------------- softmax
         if constexpr (NT == 2 && !PROMPT)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int t = NT == 1 ? 0 : warp >> 2;
         const int r = (warp & 3) * 32 + lane;        // row of the tile = TMEM lane
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
@@ -638,7 +638,13 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                     break;
                 if (s.last) {
                     __threadfence();
-                    join_parts<T, Sh::kRows>(a, u, tid, Sh::kSoftmax);
+                    ok = join_parts<T, Sh::kRows>(a, u, tid, Sh::kSoftmax, [&] {
+                        __threadfence();
+                        mbar_arrive(&s.joined);
+                        return wait(&s.joined, n_join++ & 1);
+                    });
+                    if (!ok)
+                        break;
                 }
             }
             ++n;
