@@ -408,6 +408,9 @@ SPEC_API int spec_round_sample(const void *target_logits, spec_dtype dt, float t
  * path is known, and spec_commit_tree then copies that path to those slots.
  *
  * flags [B] uint32 (or NULL): SPEC_FLAG_BAD_STATE / _BAD_TREE / _TIMEOUT or 0.
+ * B is at most SPEC_MAX_POOL (tree and commit calls: 65535).  Buffers a call
+ * writes must not overlap any other of its buffers; where the overlap of two
+ * large ones can be seen on the host it is SPEC_EINVAL.
  * ---------------------------------------------------------------------------
  */
 
@@ -463,7 +466,8 @@ SPEC_API int spec_append_prompt(const void *qkv, spec_dtype dt, int M, int Hq, v
 
 /* Workspace of spec_attend_round (does not depend on B or S; 256-byte
  * aligned; its first SPEC_ATTEND_ZERO bytes zero before its first use, and
- * again after each call). */
+ * again after each call, unless one ended in SPEC_FLAG_TIMEOUT: clear them
+ * then). */
 #define SPEC_ATTEND_ZERO 2048
 SPEC_API size_t spec_attend_workspace_bytes(int T, int Hq, int H, int D);
 
@@ -475,7 +479,8 @@ SPEC_API size_t spec_attend_workspace_bytes(int T, int Hq, int H, int D);
  * NULL: a chain, a <= i).  The nodes' keys and values are read from `staged`,
  * or with staged NULL from slots pad + len - 1 ..  A query that sees nothing
  * (len 1, mask 0) gives zeros.  Slots no query of the sequence sees may hold
- * anything.  T = 1 is plain decoding.  scale > 0.  Statistics and sums are
+ * anything, and a value that is not finite reaches only the queries that see
+ * it.  T = 1 is plain decoding.  An index may be repeated.  scale > 0.  Statistics and sums are
  * fp32; the same inputs give the same bits.  q and out must not
  * overlap.
  */

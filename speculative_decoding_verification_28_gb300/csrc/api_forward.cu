@@ -28,7 +28,8 @@ int check_layer(int dt, int L, int N, int H, int S, int D, int layer, int heads)
 {
     if (L < 1 || N < 1 || H < 1 || S < 1 || D < 1 || D > SPEC_MAX_HEAD_DIM || layer < 0 || layer >= L)
         return SPEC_EINVAL;
-    if (heads < 1 || heads % H != 0 || H > 65535)
+    // a layer's slabs and a sequence's slots, rounded up to a tile, are counted in 31 bits
+    if (heads < 1 || heads % H != 0 || H > 65535 || 2LL * N * H > INT_MAX || S > INT_MAX - 256)
         return SPEC_EINVAL;
     return dtype_ok(dt) ? SPEC_OK : SPEC_EDTYPE;
 }
@@ -101,7 +102,7 @@ AppendArgs append_args(const Append &p, void *kv, int N, int H, int S, int D, in
 
 int check_attend(const void *q, int dt, long long tokens, int Hq, const void *kv, float scale, const void *out)
 {
-    if (!q || !kv || !out || !(scale > 0.0f) || !isfinite(scale))
+    if (!q || !kv || !out || !(scale > 0.0f) || !isfinite(scale * 1.44269504088896340736f))
         return SPEC_EINVAL;
     if (tokens * Hq > INT_MAX)
         return SPEC_EINVAL;
@@ -133,7 +134,7 @@ int spec_append_round(const void *qkv, spec_dtype dt, int B, int T, int Hq, void
                       const void *k_weight, float eps, const float *inv_freq, int R, int interleaved, void *q_out,
                       uint32_t *flags, void *cuda_stream)
 {
-    if (B < 0 || T < 1 || T > SPEC_MAX_NODES)
+    if (B < 0 || B > SPEC_MAX_POOL || T < 1 || T > SPEC_MAX_NODES)
         return SPEC_EINVAL;
     int rc = check_layer(dt, L, N, H, S, D, layer, Hq);
     if (rc != SPEC_OK || B == 0)
@@ -160,7 +161,7 @@ int spec_append_prompt(const void *qkv, spec_dtype dt, int M, int Hq, void *kv, 
                        const int32_t *idx, const void *q_weight, const void *k_weight, float eps,
                        const float *inv_freq, int R, int interleaved, void *q_out, uint32_t *flags, void *cuda_stream)
 {
-    if (B < 0 || M < 0)
+    if (B < 0 || B > SPEC_MAX_POOL || M < 0)
         return SPEC_EINVAL;
     int rc = check_layer(dt, L, N, H, S, D, layer, Hq);
     if (rc != SPEC_OK || B == 0)
@@ -192,7 +193,7 @@ int spec_attend_round(const void *q, spec_dtype dt, int B, int T, int Hq, const 
                       const int32_t *n_nodes, const uint64_t *tree_mask, const void *staged, float scale, void *out,
                       uint32_t *flags, void *workspace, size_t workspace_bytes, void *cuda_stream)
 {
-    if (B < 0 || T < 1 || T > SPEC_MAX_NODES)
+    if (B < 0 || B > SPEC_MAX_POOL || T < 1 || T > SPEC_MAX_NODES)
         return SPEC_EINVAL;
     int rc = check_layer(dt, L, N, H, S, D, layer, Hq);
     if (rc != SPEC_OK || B == 0)
@@ -233,7 +234,7 @@ int spec_attend_prompt(const void *q, spec_dtype dt, int M, int Hq, const void *
                        int layer, int B, const int32_t *cu, const int32_t *start, const int32_t *pad,
                        const int32_t *idx, float scale, void *out, uint32_t *flags, void *cuda_stream)
 {
-    if (B < 0 || M < 0)
+    if (B < 0 || B > SPEC_MAX_POOL || M < 0)
         return SPEC_EINVAL;
     int rc = check_layer(dt, L, N, H, S, D, layer, Hq);
     if (rc != SPEC_OK || B == 0)
@@ -267,7 +268,7 @@ int spec_verify_tree(const void *target_logits, spec_dtype dt, int B, int T, int
                      int32_t *out_tokens, int32_t *path, int32_t *n_accept, int32_t *n_emit, uint32_t *flags,
                      void *workspace, size_t workspace_bytes, void *cuda_stream)
 {
-    if (B < 0 || T < 1 || T > SPEC_MAX_NODES || V < 1)
+    if (B < 0 || T < 1 || T > SPEC_MAX_NODES || V < 1 || V > INT_MAX - 1024)
         return SPEC_EINVAL;
     if (!dtype_ok(dt))
         return SPEC_EDTYPE;

@@ -69,7 +69,8 @@ def attend_round(lib, q=Q, dt=1, B=2, T=4, Hq=8, kv=KV, L=2, N=2, H=2, S=64, D=6
 def test_attend_round_refusals(lib):
     for kw in (dict(B=-1), dict(T=0), dict(T=65), dict(Hq=9), dict(layer=2), dict(D=257), dict(q=None), dict(kv=None),
                dict(out=None), dict(length=None), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
-               dict(scale=float("inf")), dict(N=1), dict(out=Q), dict(B=1 << 27, N=1 << 27)):
+               dict(scale=float("inf")), dict(scale=3e38), dict(N=1), dict(out=Q), dict(B=1 << 27, N=1 << 27),
+               dict(B=65537, N=65537), dict(S=(1 << 31) - 1), dict(N=1 << 30)):
         assert attend_round(lib, **kw) == -1, kw
     assert attend_round(lib, dt=9) == -2
     for kw in (dict(ws=None), dict(ws=at(0x30000010)), dict(wsb=16)):
@@ -89,7 +90,7 @@ def attend_prompt(lib, q=Q, dt=1, M=9, Hq=8, kv=KV, L=2, N=2, H=2, S=64, D=64, l
 
 def test_attend_prompt_refusals(lib):
     for kw in (dict(B=-1), dict(M=-2), dict(Hq=9), dict(layer=-1), dict(D=257), dict(q=None), dict(kv=None), dict(out=None),
-               dict(cu=None), dict(scale=0.0), dict(N=1), dict(out=Q), dict(M=1 << 30)):
+               dict(cu=None), dict(scale=0.0), dict(N=1), dict(out=Q), dict(M=1 << 30), dict(B=65537, N=65537)):
         assert attend_prompt(lib, **kw) == -1, kw
     assert attend_prompt(lib, dt=4) == -2
     for kw in (dict(q=ODD), dict(cu=ODD), dict(start=ODD), dict(pad=ODD), dict(idx=ODD), dict(flags=ODD)):
@@ -111,7 +112,7 @@ def test_tree_refusals(lib):
                wsb=1 << 20):
         return lib.spec_verify_tree(x, dt, B, T, V, tok, parent, n, -1, rem, out, path, na, ne, None, ws, wsb, None)
 
-    for kw in (dict(B=-1), dict(T=0), dict(T=65), dict(V=0), dict(x=None), dict(tok=None), dict(parent=None),
+    for kw in (dict(B=-1), dict(T=0), dict(T=65), dict(V=0), dict(V=(1 << 31) - 1), dict(B=65536), dict(x=None), dict(tok=None), dict(parent=None),
                dict(out=None), dict(path=None), dict(na=None), dict(ne=None)):
         assert verify(**kw) == -1, kw
     assert verify(dt=5) == -2

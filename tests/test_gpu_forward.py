@@ -220,6 +220,54 @@ def test_attend_round_on_a_side_stream():
     assert torch.equal(o, a)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,G", [(2, 3), (5, 20)])
+def test_attend_round_many_sequences(dt, T, G):
+    # more sequences than a CTA has threads; some idle, some not valid
+    g, rng = gen(17), np.random.default_rng(17)
+    B, H, S, D = 777, 1, 24, 64
+    lens, n = rng.integers(1, 18, B), rng.integers(0, T + 1, B)
+    lens[::50] = 0
+    kv = randn(g, (1, 2, B, H, S, D), DT[dt])
+    q = randn(g, (B, T, G * H, D), DT[dt])
+    out = torch.full_like(q, 7.0).cuda()
+    o, flags = sv.spec_attend_round(q.cuda(), kv.cuda(), 0, i32(lens).cuda(), None, n_nodes=i32(n).cuda(), out=out)
+    assert ((flags.cpu() == 16) == (i32(lens) == 0)).all()
+    n[lens == 0] = 0
+    want, tol = ref.attend_round(q, kv, 0, np.maximum(lens, 1), np.zeros(B, int), n=n)
+    close(o, want, tol)
+    assert (o.cpu()[torch.isnan(want)] == 7.0).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_attend_round_of_one_row_twice(dt):
+    c = round_case(18, DT[dt], 4, 3, 4, 2, 128, 300, [200, 100, 30, 7], pool=4, tree=True, staged=True)
+    c["idx"] = i32([2, 2, 0, 2])
+    c["kv"] = randn(gen(19), c["kv"].shape, DT[dt])
+    check_round(c)
+
+
+def shifted(x):
+    """The same values one element further into a buffer."""
+    y = torch.zeros(x.numel() + 1, dtype=x.dtype, device=x.device)[1:].view(x.shape)
+    return y.copy_(x)
+
+
+@pytest.mark.parametrize("which", ["q", "kv", "staged", "out"])
+def test_attend_round_buffers_of_element_alignment(which):
+    c = round_case(20, torch.bfloat16, 3, 5, 2, 2, 64, 200, [150, 64, 3], tree=True, staged=True)
+    d = {k: cu_(v) for k, v in c.items()}
+    out = torch.zeros_like(d["q"])
+    if which == "out":
+        out = shifted(out)
+    else:
+        d[which] = shifted(d[which])
+    o, flags = sv.spec_attend_round(d["q"], d["kv"], 1, d["length"], d["pad"], tree_mask=d["mask"], n_nodes=d["n"],
+                                    staged=d["staged"], out=out)
+    want, tol = ref.attend_round(c["q"], c["kv"], 1, c["length"], c["pad"], c["mask"], c["n"], None, c["staged"])
+    close(o, want, tol)
+
+
 def test_attend_round_offsets_past_32_bits():
     # the layer's slabs start more than 2^32 elements into the cache
     free, _ = torch.cuda.mem_get_info()
@@ -324,6 +372,20 @@ def test_attend_prompt_later_values_that_are_not_finite_reach_no_earlier_row(dt)
     keep = [d for d in range(64) if d != 3]
     close(o[70:140][..., keep], want[70:140][..., keep], tol[70:140][..., keep])
     assert torch.isinf(o[70:140, :, 3]).all() and torch.isnan(o[140:]).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_attend_prompt_many_sequences(dt):
+    rng = np.random.default_rng(30)
+    check_prompt(prompt_case(30, DT[dt], 2, 2, 64, 40, rng.integers(0, 20, 100), past=rng.integers(0, 20, 100), pool=120))
+
+
+def test_attend_prompt_element_alignment():
+    c = prompt_case(31, torch.bfloat16, 2, 1, 128, 100, [40, 60])
+    d = {k: cu_(v) for k, v in c.items()}
+    o, _ = sv.spec_attend_prompt(shifted(d["q"]), d["kv"], 0, d["cu"], d["pad"])
+    want, tol = ref.attend_prompt(c["q"], c["kv"], 0, c["cu"], c["pad"])
+    close(o, want, tol)
 
 
 def test_attend_prompt_flags():
@@ -457,6 +519,33 @@ def test_append_far_positions(pos):
     assert torch.equal(st[0, 1, 0].transpose(0, 1).cpu(), v)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_append_many_sequences(dt):
+    """More prompts than a warp has lanes, into a pool, from an odd offset."""
+    g, rng = gen(35), np.random.default_rng(35)
+    B, N, S, D, H, Hq = 100, 130, 30, 64, 2, 4
+    lens = rng.integers(0, 12, B)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    start, pad, idx = rng.integers(0, 9, B), rng.integers(0, 9, B), rng.permutation(N)[:B]
+    qkv, kv = randn(g, (int(cu[-1]), Hq + 2 * H, D), DT[dt]), randn(g, (1, 2, N, H, S, D), DT[dt])
+    w = (1 + 0.1 * torch.randn(D, generator=g)).to(DT[dt])
+    want_kv, tol_kv = kv.double(), torch.zeros(kv.shape, dtype=torch.float64)
+    want_q, tol_q = torch.zeros(int(cu[-1]), Hq, D).double(), torch.zeros(int(cu[-1]), Hq, D).double()
+    for b in range(B):
+        s, at = slice(int(cu[b]), int(cu[b + 1])), int(pad[b] + start[b])
+        q, k, v = append_ref(qkv[s], H, torch.arange(lens[b]) + int(start[b]), w, w, 1e-6, freqs(D), False)
+        want_q[s], tol_q[s] = q, ref.append_tol(q, DT[dt])
+        want_kv[0, :, idx[b], :, at:at + lens[b]] = torch.stack([k, v.double()]).transpose(1, 2)
+        tol_kv[0, 0, idx[b], :, at:at + lens[b]] = ref.append_tol(k, DT[dt]).transpose(0, 1)
+    for move in (lambda x: x, shifted):
+        kvd = move(kv.cuda())
+        q, flags = sv.spec_append_prompt(move(qkv.cuda()), kvd, 0, i32(cu).cuda(), i32(pad).cuda(), freqs(D).cuda(),
+                                         q_weight=w.cuda(), k_weight=w.cuda(), start=i32(start).cuda(), idx=i32(idx).cuda())
+        assert (flags == 0).all()
+        close(q, want_q, tol_q)
+        close(kvd, want_kv, tol_kv)
+
+
 def test_append_extreme_heads():
     """All-zero heads, large and tiny ones, one that is not finite."""
     g = gen(33)
@@ -518,6 +607,14 @@ def test_tree_plan(T):
     mask, depth, flags = sv.spec_tree_plan(i32(parent).cuda(), i32(n).cuda())
     assert (flags == 0).all()
     assert np.array_equal(mask.cpu().numpy(), want_m) and np.array_equal(depth.cpu().numpy(), want_d)
+
+
+def test_verify_tree_from_an_odd_offset():
+    x, tokens, parent, n = verify_case(45, "bf16", 5, 9, 1001, 0.9)
+    d = shifted(x.cuda())
+    got = sv.spec_verify_tree(d, i32(tokens).cuda(), i32(parent).cuda(), n_nodes=i32(n).cuda())
+    want = sv.spec_verify_tree(x.cuda(), i32(tokens).cuda(), i32(parent).cuda(), n_nodes=i32(n).cuda())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 def test_tree_plan_flags():
