@@ -227,17 +227,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     const Tile tl = tile_of<false>(u, tile);
                     const int nch = (tl.valid + 31) / 32;
                     uint32_t s0[32], s1[32];
-                    auto hide = [&](uint32_t *v, int k) {
-                        uint32_t w;
-                        if (tl.nodes)
-                            w = (uint32_t)(bits >> (32 * k));
-                        else
-                            w = tl.valid >= 32 * k + 32 ? ~0u : (1u << (tl.valid - 32 * k)) - 1;
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(w >> e & 1))
-                                v[e] = 0xFF800000u;
-                    };
                     const bool plain = !tl.nodes && tl.valid == kKeys;
                     float mx;
                     if (plain) {
@@ -256,8 +245,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         mx = -INFINITY;
 #pragma unroll 1
                         for (int k = 0; k < nch; ++k) {
+                            const uint32_t w = seen32(tl.nodes, bits, tl.valid, k);
                             tc_load(tm_s + 32 * k, s0);
-                            hide(s0, k);
+                            if (__any_sync(0xFFFFFFFFu, real && w != ~0u))
+                                hide32(s0, w);
                             mx = fmaxf(mx, max32(s0));
                         }
                     }
@@ -314,8 +305,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     } else {
 #pragma unroll 1
                         for (int k = nch - 1; k >= 0; --k) {
+                            const uint32_t w = seen32(tl.nodes, bits, tl.valid, k);
                             tc_load(tm_s + 32 * k, s0);
-                            hide(s0, k);
+                            if (__any_sync(0xFFFFFFFFu, real && w != ~0u))
+                                hide32(s0, w);
                             weigh32(s0, k);
                         }
                     }

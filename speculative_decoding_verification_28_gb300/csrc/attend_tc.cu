@@ -434,22 +434,8 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                     const bool plain = !tl.nodes && !__any_sync(0xFFFFFFFFu, lim < kKeys);
                     uint32_t s0[32], s1[32], s2[32];
                     float mx;
-                    uint64_t bits = 0;
+                    uint64_t bits = 0;  // nodes that the row sees
                     const int nch = (tl.valid + 31) / 32;
-                    auto masked = [&](uint32_t *v, int k) {
-                        if (tl.nodes) {
-                            const uint32_t w = (uint32_t)(bits >> (32 * k));
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(w >> e & 1))
-                                    v[e] = 0xFF800000u;
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (32 * k + e >= lim)
-                                    v[e] = 0xFF800000u;
-                        }
-                    };
                     if (plain) {
                         tc_load(tm_s, s0);
                         tc_ld32(tm_s + 32, s1);
@@ -469,10 +455,16 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                             bits &= tl.valid < 64 ? (1ull << tl.valid) - 1 : ~0ull;
                         }
                         mx = -INFINITY;
+                        // a vote spares chunks that every row of the warp
+                        // sees whole, or not at all
 #pragma unroll 1
                         for (int k = 0; k < nch; ++k) {
+                            const uint32_t w = seen32(tl.nodes, bits, lim, k);
+                            if (!__any_sync(0xFFFFFFFFu, real && w != 0))
+                                continue;
                             tc_load(tm_s + 32 * k, s0);
-                            masked(s0, k);
+                            if (__any_sync(0xFFFFFFFFu, real && w != ~0u))
+                                hide32(s0, w);
                             mx = fmaxf(mx, max32(s0));
                         }
                     }
@@ -533,8 +525,15 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                     } else {
 #pragma unroll 1
                         for (int k = nch - 1; k >= 0; --k) {
+                            const uint32_t w = seen32(tl.nodes, bits, lim, k);
+                            if (!__any_sync(0xFFFFFFFFu, real && w != 0)) {
+                                uint32_t none[16] = {};
+                                tc_st16(tm_s + kTmemP + 16 * k, none);
+                                continue;
+                            }
                             tc_load(tm_s + 32 * k, s0);
-                            masked(s0, k);
+                            if (__any_sync(0xFFFFFFFFu, real && w != ~0u))
+                                hide32(s0, w);
                             weigh32(s0, k);
                         }
                     }

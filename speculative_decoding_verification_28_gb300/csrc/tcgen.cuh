@@ -258,6 +258,23 @@ __device__ __forceinline__ void store_row32(T *dst, const uint32_t *o, float f)
     }
 }
 
+// Columns 32 k .. of a tile that a row sees, as a word: the first `lim`, or
+// for nodes those with their bit set.
+__device__ __forceinline__ uint32_t seen32(bool nodes, uint64_t bits, int lim, int k)
+{
+    if (nodes)
+        return (uint32_t)(bits >> (32 * k));
+    return lim >= 32 * k + 32 ? ~0u : lim <= 32 * k ? 0u : (1u << (lim - 32 * k)) - 1;
+}
+// scores that are not seen: -inf
+__device__ __forceinline__ void hide32(uint32_t *v, uint32_t seen)
+{
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if (!(seen >> e & 1))
+            v[e] = 0xFF800000u;
+}
+
 // instruction descriptor: fp32 accumulators, both operands T, M = 128
 template <typename T>
 __device__ __forceinline__ uint32_t tc_idesc(int n, bool b_rows_summed, bool a_rows_summed = false)
