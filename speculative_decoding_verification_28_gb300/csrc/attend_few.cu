@@ -1,30 +1,33 @@
-// attend_few.cu -- attention of a round on the tensor cores where a key head
-// has few query rows (up to 64): decoding and short chains.
+// attend_few.cu -- attention on the tensor cores in small units: rounds where a
+// key head has few query rows (up to 64: decoding and short chains), and
+// short prompts (128 rows a unit, where attend_tc.cu's have 256).
 //
 // The mathematics and the softmax are attend_tc.cu's; the split is made for a
 // bandwidth-bound stream.  A tile of 128 keys arrives every 3000 cycles an SM
 // (512 bytes a key of 128 columns, HBM), its chain of score, softmax and
 // product takes about as long, and a unit's start and end as long again.  So
 // two CTAs share an SM, each with one buffer of everything (TMEM: 128 columns
-// of scores and weights, 128 of O; a ring of three tiles), and one's chain
-// runs while the other's keys arrive.
+// of scores and weights, 128 of O; a ring of two or three tiles), and one's
+// chain runs while the other's keys arrive.
 #include "tcgen.cuh"
 
 namespace spec {
 
-constexpr int kFewRows = 64;  // most query rows of a unit
+constexpr int kFewRows = 64;        // most query rows of a round's unit
+constexpr int kFewPromptRows = 128; // and of a prompt's
 constexpr int kFewCtas = 2 * kAttendCtas;
 constexpr int kFewThreads = 192;
 constexpr int kFewTmemP = 64;  // columns of the scores where the weights begin
 
-template <int D>
+template <int D, bool PROMPT>
 struct FewShape {
+    static constexpr int kRows = PROMPT ? kFewPromptRows : kFewRows;
     static constexpr int kPanels = D / 64;
     static constexpr int kPanel = kKeys * 128;
     static constexpr int kTile = kPanels * kPanel;       // bytes of a K or V tile
-    static constexpr int kQPanel = kFewRows * 128;       // the product reads 128 rows: what follows
+    static constexpr int kQPanel = kRows * 128;          // the product reads 128 rows: what follows
     static constexpr int kQ = kPanels * kQPanel;
-    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kStages = D == 128 ? (PROMPT ? 2 : 3) : 5;
 };
 template <int STAGES>
 struct FewShared {
@@ -36,19 +39,20 @@ struct FewShared {
     int abort, last;
     uint32_t odd[kGuardRing][13];
 };
-template <int D>
+template <int D, bool PROMPT>
 constexpr int few_smem()
 {
-    using Sh = FewShape<D>;
+    using Sh = FewShape<D, PROMPT>;
     return Sh::kStages * Sh::kTile + Sh::kQ + (int)sizeof(FewShared<Sh::kStages>);
 }
-static_assert(few_smem<128>() <= 115712 && few_smem<64>() <= 115712, "two CTAs an SM");
+static_assert(few_smem<128, false>() <= 115712 && few_smem<64, false>() <= 115712, "two CTAs an SM");
+static_assert(few_smem<128, true>() <= 115712 && few_smem<64, true>() <= 115712, "two CTAs an SM");
 
-template <typename T, int D>
+template <typename T, int D, bool PROMPT>
 __global__ void __launch_bounds__(kFewThreads, 2)
     attend_few_kernel(const AttendArgs a, const __grid_constant__ TcMaps maps, const TcBoxes box)
 {
-    using Sh = FewShape<D>;
+    using Sh = FewShape<D, PROMPT>;
     constexpr int ST = Sh::kStages;
     extern __shared__ __align__(1024) unsigned char base[];
     unsigned char *ring_p = base + Sh::kQ;  // queries first: rows past theirs are read from the ring
@@ -82,8 +86,14 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         const CUtensorMap *m = lane == 0 ? &maps.q : lane == 1 ? &maps.kv : &maps.node;
         asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
     }
-    __syncthreads();  // run.begin / end above come before find_run's
-    find_run<kFewThreads>(a, sh, s.scan, &s.run);
+    AttendUnit first{};
+    bool some = true;
+    if (PROMPT) {
+        some = prompt_unit(a, sh, first);
+    } else {
+        __syncthreads();  // run.begin / end above come before find_run's
+        find_run<kFewThreads>(a, sh, s.scan, &s.run);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -92,7 +102,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
         return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, &s.abort));
     };
-    UnitWalk units(a, sh, s.run);
+    Units<PROMPT> units(a, sh, s.run, first, some);
     AttendUnit u{};
 
     if (warp == kLoadWarp) {
@@ -104,7 +114,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 // the first keys before the queries: those wait for the unit
                 // before to be scored
                 for (int tile = u.tile; ok && tile < u.tile_end; ++tile) {
-                    const KvBox k = kv_box<Sh::kPanels>(a, maps, box, u, tile, tile == u.n_tiles - 1);
+                    const KvBox k = kv_box<Sh::kPanels>(a, maps, box, u, tile, !PROMPT && tile == u.n_tiles - 1);
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
                         const int sg = it % ST;
@@ -159,7 +169,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             int g = 0;
             for (int tile = u.tile; ok && tile < u.tile_end; ++tile, ++i) {
                 const uint32_t sk = (2 * i) % ST, sv = (2 * i + 1) % ST;
-                const Tile tl = tile_of<false>(u, tile);
+                const Tile tl = tile_of<PROMPT>(u, tile);
                 if (tile == u.tile)
                     ok = wait(&s.q_full, n & 1);
                 ok = ok && wait(&s.kv_full[sk], ((2 * i) / ST) & 1);
@@ -212,7 +222,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             const bool busy = __any_sync(0xFFFFFFFFu, real);
             const int tok = (u.row0 + r) / a.G;
             uint64_t bits = 0;  // nodes that the row sees
-            if (real && u.tile_end == u.n_tiles) {
+            if (!PROMPT && real && u.tile_end == u.n_tiles) {
                 bits = a.mask ? a.mask[(size_t)u.b * a.seq.T + tok] : (2ull << tok) - 1;
                 if (u.seq.n < 64)
                     bits &= (1ull << u.seq.n) - 1;
@@ -224,10 +234,11 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     break;
                 tc_fence_after();
                 if (busy) {
-                    const Tile tl = tile_of<false>(u, tile);
+                    const Tile tl = tile_of<PROMPT>(u, tile);
                     const int nch = (tl.valid + 31) / 32;
                     uint32_t s0[32], s1[32];
-                    const bool plain = !tl.nodes && tl.valid == kKeys;
+                    const int lim = PROMPT ? min(tl.valid, u.seq.prefix + tok + 1 - tile * kKeys) : tl.valid;
+                    const bool plain = !tl.nodes && !__any_sync(0xFFFFFFFFu, lim < kKeys);
                     float mx;
                     if (plain) {
                         tc_load(tm_s, s0);
@@ -245,7 +256,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         mx = -INFINITY;
 #pragma unroll 1
                         for (int k = 0; k < nch; ++k) {
-                            const uint32_t w = seen32(tl.nodes, bits, tl.valid, k);
+                            const uint32_t w = seen32(tl.nodes, bits, lim, k);
+                            if (!__any_sync(0xFFFFFFFFu, real && w != 0))
+                                continue;
                             tc_load(tm_s + 32 * k, s0);
                             if (__any_sync(0xFFFFFFFFu, real && w != ~0u))
                                 hide32(s0, w);
@@ -305,7 +318,12 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     } else {
 #pragma unroll 1
                         for (int k = nch - 1; k >= 0; --k) {
-                            const uint32_t w = seen32(tl.nodes, bits, tl.valid, k);
+                            const uint32_t w = seen32(tl.nodes, bits, lim, k);
+                            if (!__any_sync(0xFFFFFFFFu, real && w != 0)) {
+                                uint32_t none[16] = {};
+                                tc_st16(tm_s + kFewTmemP + 16 * k, none);
+                                continue;
+                            }
                             tc_load(tm_s + 32 * k, s0);
                             if (__any_sync(0xFFFFFFFFu, real && w != ~0u))
                                 hide32(s0, w);
@@ -329,7 +347,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 break;
             tc_fence_after();
             const bool whole = u.n_parts == 1;
-            float *slot = whole ? nullptr : part_slot<kFewRows>(a, blockIdx.x, u.part);
+            float *slot = whole ? nullptr : part_slot<Sh::kRows>(a, blockIdx.x, u.part);
             if (busy) {
                 const float f = !whole ? 1.0f : l > 0.0f || l != l ? 1.0f / l : 0.0f;
                 const uint32_t *odd = s.odd[n % kGuardRing];
@@ -340,18 +358,14 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     uint32_t o[32];
                     tc_load(tm_o + lanes + k, o);
                     if (any_odd && real) {
-                        // values the guard took out of the nodes' V go where they are seen
-                        const Tile tl = tile_of<false>(u, u.n_tiles - 1);
-                        for (int q = 0; q < u.seq.n; ++q)
-                            if ((odd[q >> 5] >> (q & 31) & 1) && (bits >> q & 1)) {
-                                const T *v = value_row<T>(a, u, tl, u.n_tiles - 1, q) + k;
+                        uint32_t x[32];  // rare; the call keeps only this copy in memory
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) {
-                                    const float x = Storage<T>::at(v, e);
-                                    if (!(fabsf(x) <= 3.0e38f))
-                                        o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
-                                }
-                            }
+                        for (int e = 0; e < 32; ++e)
+                            x[e] = o[e];
+                        put_back32<T, PROMPT>(a, u, odd, tok, k, x);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = x[e];
                     }
                     if (!real)
                         continue;
@@ -360,13 +374,13 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            __stcg(reinterpret_cast<uint4 *>(slot + part_quad<kFewRows>((k + e) / 4, r)),
+                            __stcg(reinterpret_cast<uint4 *>(slot + part_quad<Sh::kRows>((k + e) / 4, r)),
                                    make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
                     }
                 }
                 if (real && !whole) {
-                    __stcg(slot + (size_t)kFewRows * D + r, m);
-                    __stcg(slot + (size_t)kFewRows * D + kFewRows + r, l);
+                    __stcg(slot + (size_t)Sh::kRows * D + r, m);
+                    __stcg(slot + (size_t)Sh::kRows * D + Sh::kRows + r, l);
                 }
             }
             tc_fence_before();
@@ -392,7 +406,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     break;
                 if (s.last) {
                     __threadfence();
-                    ok = join_parts<T, kFewRows>(a, u, tid, 128, [&] {
+                    ok = join_parts<T, Sh::kRows>(a, u, tid, 128, [&] {
                         __threadfence();
                         __syncwarp();
                         if (lane == 0)
@@ -416,28 +430,38 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 
 namespace {
 
-template <typename T, int D>
+template <typename T, int D, bool PROMPT>
 cudaError_t launch_few(const AttendArgs &a, cudaStream_t st)
 {
+    using Sh = FewShape<D, PROMPT>;
     TcMaps maps;
     TcBoxes box;
-    if (!tc_make_maps(a, TcType<T>::kFmt == 1, kFewRows, &maps, &box))
+    if (!tc_make_maps(a, TcType<T>::kFmt == 1, Sh::kRows, &maps, &box))
         return cudaErrorInvalidValue;
-    const cudaError_t e =
-        cudaFuncSetAttribute(attend_few_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem<D>());
+    const cudaError_t e = cudaFuncSetAttribute(attend_few_kernel<T, D, PROMPT>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem<D, PROMPT>());
     if (e != cudaSuccess)
         return e;
-    attend_few_kernel<T, D><<<kFewCtas, kFewThreads, few_smem<D>(), st>>>(a, maps, box);
+    dim3 grid(kFewCtas);
+    if (PROMPT)
+        grid = dim3((unsigned)(a.seq.M / box.tok_tile + a.seq.B), (unsigned)a.cache.H);
+    attend_few_kernel<T, D, PROMPT><<<grid, kFewThreads, few_smem<D, PROMPT>(), st>>>(a, maps, box);
     return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_few_t(const AttendArgs &a, cudaStream_t st)
+{
+    if (a.cache.D == 64)
+        return a.seq.cu ? launch_few<T, 64, true>(a, st) : launch_few<T, 64, false>(a, st);
+    return a.seq.cu ? launch_few<T, 128, true>(a, st) : launch_few<T, 128, false>(a, st);
 }
 
 }  // namespace
 
 cudaError_t launch_attend_few(const AttendArgs &a, spec_dtype dt, cudaStream_t st)
 {
-    if (a.cache.D == 64)
-        return dt == SPEC_BF16 ? launch_few<__nv_bfloat16, 64>(a, st) : launch_few<__half, 64>(a, st);
-    return dt == SPEC_BF16 ? launch_few<__nv_bfloat16, 128>(a, st) : launch_few<__half, 128>(a, st);
+    return dt == SPEC_BF16 ? launch_few_t<__nv_bfloat16>(a, st) : launch_few_t<__half>(a, st);
 }
 
 size_t attend_few_workspace(int D)

@@ -28,6 +28,7 @@ namespace spec {
 // ---------------------------------------------------------------------------
 // shapes
 // ---------------------------------------------------------------------------
+constexpr int kShortPrompt = 512;
 constexpr int kTmemP = 64;  // columns of a score buffer where its weights begin
 
 template <int D, int NT>
@@ -69,26 +70,6 @@ __device__ __forceinline__ int tiles_end(const AttendUnit &u, int G, int tile_ro
     const int last = min(u.n_rows, (t + 1) * tile_rows) - 1;
     return (u.seq.prefix + (u.row0 + last) / G + kKeys) / kKeys;
 }
-
-// Walks the units of a CTA: a prompt's one, or a round's run.
-template <bool PROMPT>
-struct Units {
-    UnitWalk walk;
-    AttendUnit one;
-    bool fresh;
-    __device__ Units(const AttendArgs &a, const Shape &sh, const Run &r, const AttendUnit &u) : walk(a, sh, r), one(u), fresh(true)
-    {
-    }
-    __device__ bool next(AttendUnit &u)
-    {
-        if (!PROMPT)
-            return walk.next(u);
-        u = one;
-        const bool was = fresh;
-        fresh = false;
-        return was;
-    }
-};
 
 // ---------------------------------------------------------------------------
 // the kernel
@@ -154,7 +135,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
         return __all_sync(0xFFFFFFFFu, wait1(bar, parity));
     };
-    Units<PROMPT> units(a, sh, s.run, first);
+    Units<PROMPT> units(a, sh, s.run, first, true);
     AttendUnit u{};
 
     if (warp == kLoadWarp) {
@@ -249,7 +230,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
         };
         if constexpr (NT == 1) {
             // scores run one tile ahead of weights, across units
-            Units<PROMPT> ahead(a, sh, s.run, first);
+            Units<PROMPT> ahead(a, sh, s.run, first, true);
             AttendUnit w{};
             bool have = ahead.next(w);
             int wt = w.tile;
@@ -574,31 +555,14 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                         uint32_t o[32];
                         tc_load(tm_o + 32 * k, o);
                         if (any_odd && real) {
-                            // the values taken out of V go where they are seen
-                            int g = 0;
-                            for (int tile = u.tile; tile < u.tile_end; ++tile) {
-                                const Tile tl = tile_of<PROMPT>(u, tile);
-                                if (!tl.masked)
-                                    continue;
-                                for (int key = 0; key < tl.valid; ++key) {
-                                    if (!(odd[g * 4 + (key >> 5)] >> (key & 31) & 1))
-                                        continue;
-                                    bool sees;
-                                    if (tl.nodes)
-                                        sees = (a.mask ? a.mask[(size_t)u.b * a.seq.T + tok] : (2ull << tok) - 1) >> key & 1;
-                                    else
-                                        sees = tile * kKeys + key <= u.seq.prefix + tok;
-                                    const T *v = value_row<T>(a, u, tl, tile, key);
-                                    if (sees)
+                            uint32_t x[32];  // rare; the call keeps only this copy in memory
 #pragma unroll
-                                        for (int e = 0; e < 32; ++e) {
-                                            const float f = Storage<T>::at(v, 32 * k + e);
-                                            if (!(fabsf(f) <= 3.0e38f))
-                                                o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
-                                        }
-                                }
-                                ++g;
-                            }
+                            for (int e = 0; e < 32; ++e)
+                                x[e] = o[e];
+                            put_back32<T, PROMPT>(a, u, odd, tok, 32 * k, x);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = x[e];
                         }
                         if (real) {
                             if (whole) {
@@ -707,8 +671,18 @@ bool attend_tc_takes(const AttendArgs &a, spec_dtype dt)
 
 cudaError_t launch_attend_tc(const AttendArgs &a, spec_dtype dt, cudaStream_t st)
 {
-    if (!a.seq.cu && a.seq.T * a.G <= 64)
+    // Small units two to an SM, or large ones with two chains each?  Rounds: small
+    // up to 64 rows a key head (decoding at batch 32 41 us, 47 with one large
+    // unit an SM); up to 128 rows take one query tile of attend_tc_kernel.
+    // Prompts: small up to kShortPrompt tokens a sequence on average, where a
+    // unit's start and end cost more than its tiles (mean 158 tokens: 22.5 us
+    // against 28.7; 200: 32.8, 36.9; 512: equal; 1200: 139, 135; 2000: 295, 276).
+    if (a.seq.cu) {
+        if (a.seq.M <= (long long)kShortPrompt * a.seq.B)
+            return launch_attend_few(a, dt, st);
+    } else if (a.seq.T * a.G <= 64) {
         return launch_attend_few(a, dt, st);
+    }
     if (a.cache.D == 64)
         return dt == SPEC_BF16 ? launch_tc_d<__nv_bfloat16, 64>(a, st) : launch_tc_d<__half, 64>(a, st);
     return dt == SPEC_BF16 ? launch_tc_d<__nv_bfloat16, 128>(a, st) : launch_tc_d<__half, 128>(a, st);

@@ -376,6 +376,61 @@ __device__ __forceinline__ const T *value_row(const AttendArgs &a, const AttendU
                D;
 }
 
+// Adds the values that the guard took out of V to columns col .. col + 31 of
+// the row of query token `tok`, where it sees their keys.  Their weights are
+// positive, so that what is not finite stays as it is.
+template <typename T, bool PROMPT>
+__device__ __noinline__ void put_back32(const AttendArgs &a, const AttendUnit &u, const uint32_t *odd, int tok, int col,
+                                        uint32_t *o)
+{
+    int g = 0;
+    for (int tile = u.tile; tile < u.tile_end; ++tile) {
+        const Tile tl = tile_of<PROMPT>(u, tile);
+        if (!tl.masked)
+            continue;
+        for (int key = 0; key < tl.valid; ++key) {
+            if (!(odd[g * 4 + (key >> 5)] >> (key & 31) & 1))
+                continue;
+            bool sees;
+            if (tl.nodes)
+                sees = (a.mask ? a.mask[(size_t)u.b * a.seq.T + tok] : (2ull << tok) - 1) >> key & 1;
+            else
+                sees = tile * kKeys + key <= u.seq.prefix + tok;
+            if (!sees)
+                continue;
+            const T *v = value_row<T>(a, u, tl, tile, key) + col;
+            for (int e = 0; e < 32; ++e) {
+                const float f = Storage<T>::at(v, e);
+                if (!(fabsf(f) <= 3.4e38f))
+                    o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
+            }
+        }
+        ++g;
+    }
+}
+
+// Walks the units of a CTA: a prompt's one, or a round's run.
+template <bool PROMPT>
+struct Units {
+    UnitWalk walk;
+    AttendUnit one;
+    bool fresh;
+    // some: whether the prompt has one for this CTA
+    __device__ Units(const AttendArgs &a, const Shape &sh, const Run &r, const AttendUnit &u, bool some)
+        : walk(a, sh, r), one(u), fresh(some)
+    {
+    }
+    __device__ bool next(AttendUnit &u)
+    {
+        if (!PROMPT)
+            return walk.next(u);
+        u = one;
+        const bool was = fresh;
+        fresh = false;
+        return was;
+    }
+};
+
 // Bounded wait of one thread for a phase; after one that gave up (`abort`
 // set) every other wait of the CTA returns too.
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, int *abort)
