@@ -443,7 +443,7 @@ SPEC_API int spec_tree_plan(int B, int T, const int32_t *parent, const int32_t *
  * [L, 2, B, H, T, D] at node i, or with staged NULL to cache slot
  * pad + len - 1 + i.  Flagged: len < 1, pad < 0, a slot past S, an index
  * outside [0, N); and, where the cache is written, a repeated index.
- * qkv and q_out must not overlap.
+ * qkv, q_out and the layer or staged block written must not overlap.
  */
 SPEC_API int spec_append_round(const void *qkv, spec_dtype dt, int B, int T, int Hq, void *kv, int L, int N, int H,
                       int S, int D, int layer, const int32_t *len, const int32_t *pad, const int32_t *idx,
@@ -480,9 +480,9 @@ SPEC_API size_t spec_attend_workspace_bytes(int T, int Hq, int H, int D);
  * or with staged NULL from slots pad + len - 1 ..  A query that sees nothing
  * (len 1, mask 0) gives zeros.  Slots no query of the sequence sees may hold
  * anything, and a value that is not finite reaches only the queries that see
- * it.  T = 1 is plain decoding.  An index may be repeated.  scale > 0.  Statistics and sums are
- * fp32; the same inputs give the same bits.  q and out must not
- * overlap.
+ * it.  T = 1 is plain decoding.  An index may be repeated.  scale > 0, and
+ * scale * |q.k| within fp32's range.  Statistics and sums are fp32; the same
+ * inputs give the same bits.  out must not overlap q, the layer or staged.
  */
 SPEC_API int spec_attend_round(const void *q, spec_dtype dt, int B, int T, int Hq, const void *kv, int L, int N,
                       int H, int S, int D, int layer, const int32_t *len, const int32_t *pad,

@@ -16,11 +16,26 @@ int dtype_bytes(int dt) { return dt == SPEC_F32 ? 4 : 2; }
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 int launched(cudaError_t e) { return e == cudaSuccess ? SPEC_OK : SPEC_ECUDA; }
 
-// whether two byte ranges share a byte
-bool overlap(const void *a, long long na, const void *b, long long nb)
+// A large tensor of a call, in bytes (null: none).
+struct Span {
+    uintptr_t at, n;
+};
+// n elements of e bytes from element `first` of p; sizes past what memory can
+// hold are cut to that, so that nothing wraps
+Span span(const void *p, double first, double n, int e)
 {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+    const double top = 1e18;
+    const double f = first * e, x = n * e;
+    return Span{p ? reinterpret_cast<uintptr_t>(p) + (uintptr_t)(f < top ? f : top) : 0,
+                p ? (uintptr_t)(x < top ? x : top) : 0};
+}
+bool overlap(const Span &a, const Span &b) { return a.n && b.n && a.at < b.at + b.n && b.at < a.at + a.n; }
+
+// one layer of a cache [L, 2, N, H, S, D]
+Span layer_span(const void *kv, int N, int H, int S, int D, int layer, int e)
+{
+    const double n = 2.0 * N * H * S * D;
+    return span(kv, n * layer, n, e);
 }
 
 // sizes shared by every call on a layer of a cache; `heads` query heads
@@ -63,8 +78,9 @@ struct Append {
 };
 
 // the part of the two append calls that does not depend on the packing;
-// `tokens` rows of qkv
-int check_append(const Append &p, const void *kv, int H, int D, long long tokens)
+// `tokens` rows of qkv; layer: the layer of the cache, staged: that of the
+// staged block or none
+int check_append(const Append &p, const void *kv, int H, int D, long long tokens, const Span &layer, const Span &staged)
 {
     if (!p.qkv || !p.q_out || !kv || !(p.eps >= 0.0f) || !isfinite(p.eps))
         return SPEC_EINVAL;
@@ -72,10 +88,12 @@ int check_append(const Append &p, const void *kv, int H, int D, long long tokens
         return SPEC_EINVAL;
     if (tokens * p.Hq > INT_MAX)
         return SPEC_EINVAL;
-    const long long row = (long long)D * dtype_bytes(p.dt);
-    if (overlap(p.qkv, tokens * (p.Hq + 2LL * H) * row, p.q_out, tokens * p.Hq * row))
+    const int e = dtype_bytes(p.dt);
+    const Span in = span(p.qkv, 0, (double)tokens * (p.Hq + 2.0 * H) * D, e);
+    const Span out = span(p.q_out, 0, (double)tokens * p.Hq * D, e);
+    const Span &keys = staged.n ? staged : layer;  // where keys and values go
+    if (overlap(in, out) || overlap(in, keys) || overlap(out, keys))
         return SPEC_EINVAL;
-    const size_t e = dtype_bytes(p.dt);
     if (!aligned(p.qkv, e) || !aligned(p.q_out, e) || !aligned(kv, e) || !aligned(p.q_weight, e) ||
         !aligned(p.k_weight, e) || !aligned(p.inv_freq, 4))
         return SPEC_EALIGN;
@@ -100,13 +118,17 @@ AppendArgs append_args(const Append &p, void *kv, int N, int H, int S, int D, in
     return a;
 }
 
-int check_attend(const void *q, int dt, long long tokens, int Hq, const void *kv, float scale, const void *out)
+int check_attend(const void *q, int dt, long long tokens, int Hq, int D, const void *kv, const Span &layer,
+                 const Span &staged, float scale, const void *out)
 {
     if (!q || !kv || !out || !(scale > 0.0f) || !isfinite(scale * 1.44269504088896340736f))
         return SPEC_EINVAL;
     if (tokens * Hq > INT_MAX)
         return SPEC_EINVAL;
-    const size_t e = dtype_bytes(dt);
+    const int e = dtype_bytes(dt);
+    const Span to = span(out, 0, (double)tokens * Hq * D, e);
+    if (overlap(to, span(q, 0, (double)tokens * Hq * D, e)) || overlap(to, layer) || overlap(to, staged))
+        return SPEC_EINVAL;
     return aligned(q, e) && aligned(kv, e) && aligned(out, e) ? SPEC_OK : SPEC_EALIGN;
 }
 
@@ -140,7 +162,9 @@ int spec_append_round(const void *qkv, spec_dtype dt, int B, int T, int Hq, void
     if (rc != SPEC_OK || B == 0)
         return rc;
     const Append p = {qkv, dt, Hq, q_weight, k_weight, eps, inv_freq, R, interleaved != 0, q_out};
-    rc = check_append(p, kv, H, D, (long long)B * T);
+    const int e = dtype_bytes(dt);
+    rc = check_append(p, kv, H, D, (long long)B * T, layer_span(kv, N, H, S, D, layer, e),
+                      layer_span(staged, B, H, T, D, layer, e));
     if (rc != SPEC_OK)
         return rc;
     if (!len || (!idx && B > N))
@@ -168,7 +192,7 @@ int spec_append_prompt(const void *qkv, spec_dtype dt, int M, int Hq, void *kv, 
         return rc;
     const Append p = {qkv, dt, Hq, q_weight, k_weight, eps, inv_freq, R, interleaved != 0, q_out};
     if (M > 0) {
-        rc = check_append(p, kv, H, D, M);
+        rc = check_append(p, kv, H, D, M, layer_span(kv, N, H, S, D, layer, dtype_bytes(dt)), Span{});
         if (rc != SPEC_OK)
             return rc;
     }
@@ -198,11 +222,12 @@ int spec_attend_round(const void *q, spec_dtype dt, int B, int T, int Hq, const 
     int rc = check_layer(dt, L, N, H, S, D, layer, Hq);
     if (rc != SPEC_OK || B == 0)
         return rc;
-    rc = check_attend(q, dt, (long long)B * T, Hq, kv, scale, out);
+    const int e = dtype_bytes(dt);
+    rc = check_attend(q, dt, (long long)B * T, Hq, D, kv, layer_span(kv, N, H, S, D, layer, e),
+                      layer_span(staged, B, H, T, D, layer, e), scale, out);
     if (rc != SPEC_OK)
         return rc;
-    const long long nq = (long long)B * T * Hq * D * dtype_bytes(dt);
-    if (!len || (!idx && B > N) || overlap(q, nq, out, nq))
+    if (!len || (!idx && B > N))
         return SPEC_EINVAL;
     // tiles of 64 keys for 16 query rows each: the kernels count them in 31 bits
     const long long groups = ((long long)T * (Hq / H) + 15) / 16, tiles = (S + 63LL) / 64 + 1;
@@ -240,12 +265,11 @@ int spec_attend_prompt(const void *q, spec_dtype dt, int M, int Hq, const void *
     if (rc != SPEC_OK || B == 0)
         return rc;
     if (M > 0) {
-        rc = check_attend(q, dt, M, Hq, kv, scale, out);
+        rc = check_attend(q, dt, M, Hq, D, kv, layer_span(kv, N, H, S, D, layer, dtype_bytes(dt)), Span{}, scale, out);
         if (rc != SPEC_OK)
             return rc;
     }
-    const long long nq = (long long)M * Hq * D * dtype_bytes(dt);
-    if (!cu || (!idx && B > N) || (M > 0 && overlap(q, nq, out, nq)))
+    if (!cu || (!idx && B > N))
         return SPEC_EINVAL;
     if (!int_arrays_ok(cu, start, pad, idx, flags))
         return SPEC_EALIGN;
@@ -298,9 +322,10 @@ int spec_commit_tree(const void *staged, void *kv, spec_dtype dt, int L, int B, 
         return SPEC_OK;
     if (!staged || !kv || !len || !path || !n_emit || (!idx && B > N) || B > 65535)
         return SPEC_EINVAL;
-    const long long row = (long long)D * dtype_bytes(dt);
-    if ((long long)L * 2 * H > INT_MAX || row * T * 8 > INT_MAX ||
-        overlap(staged, (long long)L * 2 * B * H * T * row, kv, (long long)L * 2 * N * H * S * row))
+    const int e = dtype_bytes(dt);
+    // slabs, rounded up to a CTA's eight, and the bytes of eight are counted in 31 bits
+    if ((long long)L * 2 * H > INT_MAX - 8 || (long long)D * e * T * 8 > INT_MAX ||
+        overlap(span(staged, 0, 2.0 * L * B * H * T * D, e), span(kv, 0, 2.0 * L * N * H * S * D, e)))
         return SPEC_EINVAL;
     if (!aligned(staged, dtype_bytes(dt)) || !aligned(kv, dtype_bytes(dt)) ||
         !int_arrays_ok(len, pad, path, n_emit, idx) || !aligned(flags, 4))

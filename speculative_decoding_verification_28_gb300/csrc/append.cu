@@ -90,25 +90,30 @@ __device__ Token find_token(const AppendArgs &a, long long m)
     return t;
 }
 
+// Flags, sequence b's by warp b of the grid and so on around, after its token:
+// a repeated row costs a look at every sequence's, which one CTA would do B
+// times over.  By whole warps.
 __device__ void append_flags(const AppendArgs &a)
 {
-    if (blockIdx.x != 0 || !a.flags)
+    if (!a.flags)
+        return;
+    const int lane = threadIdx.x & 31;
+    const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
+    long long b = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    if (b >= a.seq.B)
         return;
     bool broken = false;  // packed offsets that descend anywhere: no sequence of the call is taken
     if (a.seq.cu) {
-        for (int b = threadIdx.x; b < a.seq.B; b += blockDim.x)
-            broken |= a.seq.cu[b + 1] < a.seq.cu[b];
-        broken = __syncthreads_or(broken);
+        for (int c = lane; c < a.seq.B; c += 32)
+            broken |= a.seq.cu[c + 1] < a.seq.cu[c];
+        broken = __any_sync(0xFFFFFFFFu, broken);
     }
-    for (int b = threadIdx.x; b < a.seq.B; b += blockDim.x)
-        a.flags[b] = !broken && load_seq(a.seq, a.cache.N, a.cache.S, b).ok ? 0u : SPEC_FLAG_BAD_STATE;
-    if (a.seq.idx && writes_cache(a.seq)) {
-        __syncthreads();
-        for (int b = threadIdx.x >> 5; b < a.seq.B; b += blockDim.x >> 5) {  // warp-uniform
-            const bool twice = repeated_row(a.seq.idx, a.seq.B, a.seq.idx[b]);
-            if (twice && (threadIdx.x & 31) == 0)
-                a.flags[b] = SPEC_FLAG_BAD_STATE;
-        }
+    for (; b < a.seq.B; b += warps) {
+        bool ok = !broken && load_seq(a.seq, a.cache.N, a.cache.S, (int)b).ok;
+        if (a.seq.idx && writes_cache(a.seq))
+            ok = !repeated_row(a.seq.idx, a.seq.B, a.seq.idx[b]) && ok;
+        if (lane == 0)
+            a.flags[b] = ok ? 0u : SPEC_FLAG_BAD_STATE;
     }
 }
 
@@ -255,13 +260,12 @@ __device__ __forceinline__ uint2 ld_stream8(const uint2 *p)
 // the loads in flight: 64 registers for a fourth CTA of 256 or loads for the
 // next head behind each head measured 130 and 154 us, two warps a token 139.
 template <typename T, int LPH>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a, int tokens, int share)
+__device__ __forceinline__ void append_token(const AppendArgs &a, int tokens, int share)
 {
     using H8 = Half8<T>;
     constexpr int NP = H8::kPairs;                 // pairs of elements in 8 bytes
     constexpr int D = LPH * 16 / (int)sizeof(T);
     constexpr int HPW = 32 / LPH;                  // heads a warp holds at a time
-    append_flags(a);
     const int lane = threadIdx.x & 31, ln = lane % LPH;
     const uint32_t gw = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
     const uint32_t m = gw / (uint32_t)share;
@@ -373,17 +377,26 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a, in
     }
 }
 
+template <typename T, int LPH>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a, int tokens,
+                                                                int share)
+{
+    append_token<T, LPH>(a, tokens, share);
+    append_flags(a);
+}
+
 // Any head size and any R <= D: one warp per head, the head in shared memory.
 constexpr int kMaxHeadDim = SPEC_MAX_HEAD_DIM;
 template <typename T>
-__global__ void __launch_bounds__(kAppendThreads) append_any_kernel(AppendArgs a)
+__global__ void __launch_bounds__(kAppendThreads) append_any_kernel(const __grid_constant__ AppendArgs a)
 {
     __shared__ float s_x[kAppendThreads / 32][kMaxHeadDim];
     __shared__ float2 s_turn[kMaxHeadDim / 2];
-    append_flags(a);
-    const Token tok = find_token(a, blockIdx.x);
-    if (!tok.live)
+    const Token tok = a.seq.M || !a.seq.cu ? find_token(a, blockIdx.x) : Token{};
+    if (!tok.live) {  // the whole CTA
+        append_flags(a);
         return;
+    }
     const int D = a.cache.D, half = a.R / 2;
     for (int i = threadIdx.x; i < half; i += kAppendThreads)
         s_turn[i] = turn(tok.pos, a.inv_freq[i]);
@@ -425,6 +438,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_any_kernel(AppendArgs a
             dst[d] = to_storage<T>(x[d]);
         __syncwarp();
     }
+    append_flags(a);
 }
 
 template <typename T>

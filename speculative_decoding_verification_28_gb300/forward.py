@@ -40,6 +40,9 @@ def _streamed(fn):
     def call(*args, stream=None, **kw):
         if stream is None:
             return fn(*args, **kw)
+        for t in (*args, *kw.values()):
+            if isinstance(t, torch.Tensor) and t.device != stream.device:
+                raise ValueError(f"stream on {stream.device}, a tensor on {t.device}")
         with torch.cuda.stream(stream):
             return fn(*args, **kw)
 
@@ -84,6 +87,9 @@ def _ws(given, kind, nbytes, device, head):
         buf = getattr(given, "buf", given)
         _need(buf, torch.uint8, "workspace", device)
         return buf
+    if _device_now() != device.index:
+        with torch.cuda.device(device):
+            return _ws(given, kind, nbytes, device, head)
     capturing = _capturing()
     if not capturing:
         key = kind, device.index, _raw_stream(device.index)

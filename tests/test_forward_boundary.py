@@ -152,3 +152,24 @@ def test_host_tensors_are_refused():
     for call in calls:
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_overlaps_are_refused(lib):
+    """What a call writes within what it reads: layer 1 of kv [2, 2, 2, 2, 64, 64]
+    in 16 bits begins 65536 bytes in and is as long; a staged layer of 2 x 4
+    nodes begins 4096 in and ends at 8192."""
+    layer1, last, staged = 0x100000000 + 65536, 0x100000000 + 131072 - 2, 0x30000000
+    for x in (layer1, last):
+        assert append_round(lib, qkv=at(x)) == -1
+        assert append_round(lib, q=at(x)) == -1
+        assert append_prompt(lib, qkv=at(x)) == -1
+        assert append_prompt(lib, q=at(x)) == -1
+        assert attend_round(lib, out=at(x), layer=1) == -1
+        assert attend_prompt(lib, out=at(x), layer=1) == -1
+    for x in (staged + 4096, staged + 8192 - 2):
+        st = at(staged)
+        assert append_round(lib, qkv=at(x), staged=st) == -1
+        assert append_round(lib, q=at(x), staged=st) == -1
+        assert attend_round(lib, out=at(x), staged=st, layer=1) == -1
+    big = 1 << 30  # sizes whose bytes pass 64 bits do not wrap around
+    assert attend_round(lib, out=at(0x100000000 + big), L=big, S=big, N=big // 2, H=1, Hq=4, D=256) == -1

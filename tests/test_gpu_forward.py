@@ -348,6 +348,41 @@ def test_attend_prompt_longer_than_tiles(dt, G, H, D):
     check_prompt(prompt_case(22, DT[dt], G, H, D, 900, [513, 700]))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("G,H,D", [(1, 2, 64), (1, 1, 128), (4, 1, 128), (7, 1, 64)])
+@pytest.mark.parametrize("lens,past", [((600, 3, 1300, 705), None), ((1, 1537), None), ((520, 811), (129, 0)),
+                                       ((1, 0, 1, 1400), (0, 5, 700, 63))])
+def test_attend_prompt_of_long_and_mixed_lengths(dt, G, H, D, lens, past):
+    check_prompt(prompt_case(35, DT[dt], G, H, D, 1700, lens, past=past, tail=2))
+
+
+@pytest.mark.parametrize("dt,G", [("bf16", 71), ("f16", 8)])
+def test_attend_prompt_of_long_ones_with_many_heads_to_a_key_head(dt, G):
+    check_prompt(prompt_case(38, DT[dt], G, 1, 64, 540, [514, 515][:1 if G > 8 else 2]))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_prompt_later_values_that_are_not_finite_in_a_long_one(dt, D):
+    """Two rows of a tile's V, one of the tile after; the first is seen from
+    row 600 on, the second from 640 (the end of a tile), the third from 645."""
+    c = prompt_case(36, DT[dt], 2, 1, D, 900, [800])
+    at = int(c["pad"][0])
+    for pos, d, x in ((600, 3, float("-inf")), (640, 7, float("inf")), (645, D - 1, NAN)):
+        c["kv"][0, 1, 0, 0, at + pos, d] = x
+    o, _ = run_prompt(c)
+    want, tol = ref.attend_prompt(c["q"], c["kv"], 0, c["cu"], c["pad"], c["start"])
+    lo = 0
+    hidden = []
+    for pos, d, inf in ((600, 3, True), (640, 7, True), (645, D - 1, False), (800, 0, True)):
+        keep = [x for x in range(D) if x not in hidden]
+        close(o[lo:pos][..., keep], want[lo:pos][..., keep], tol[lo:pos][..., keep])
+        if pos < 800:
+            assert (torch.isinf if inf else torch.isnan)(o[pos:, :, d]).all()
+            hidden.append(d)
+        lo = pos
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 def test_attend_prompt_in_pieces(dt):
     check_prompt(prompt_case(23, DT[dt], 4, 2, 64, 700, [40, 1, 129, 64], past=[300, 77, 128, 0], pool=6, tail=1))
@@ -591,6 +626,33 @@ def test_append_flags_and_repeated_rows():
     kv.copy_(before)
     _, flags = sv.spec_append_prompt(qkv[:2].reshape(6, 4, D), kv, 0, cu, None, None)
     assert flags.tolist() == [16] * 5 and torch.equal(kv, before)
+
+
+@pytest.mark.parametrize("D", [64, 80])
+def test_append_flags_of_more_sequences_than_tokens(D):
+    """Sequences without a token are flagged like the others."""
+    g = gen(37)
+    B, N = 300, 400
+    lens = np.zeros(B, np.int64)
+    lens[[7, 150, 299]] = 1
+    cu = i32(np.concatenate([[0], np.cumsum(lens)])).cuda()
+    idx = np.random.default_rng(37).permutation(N)[:B]
+    idx[3] = idx[200]
+    idx[299] = N
+    qkv = randn(g, (3, 3, D), torch.bfloat16).cuda()
+    kv = torch.zeros((1, 2, N, 1, 4, D), dtype=torch.bfloat16, device="cuda")
+    _, flags = sv.spec_append_prompt(qkv, kv, 0, cu, None, None, idx=i32(idx).cuda())
+    want = np.zeros(B, int)
+    want[[3, 200, 299]] = 16
+    assert flags.tolist() == want.tolist()
+    wrote = torch.zeros(N, dtype=torch.bool)
+    wrote[[int(idx[7]), int(idx[150])]] = True
+    assert torch.equal((kv[0, 0, :, 0, 0] != 0).any(-1).cpu(), wrote)
+    # a round's dead nodes as well
+    n = torch.zeros(B, dtype=torch.int32, device="cuda")
+    _, flags = sv.spec_append_round(randn(g, (B, 1, 3, D), torch.bfloat16).cuda(), kv, 0, n + 1, None, None,
+                                    idx=i32(idx).cuda(), n_nodes=n)
+    assert flags.tolist() == want.tolist()
 
 
 # ---------------------------------------------------------------------------
