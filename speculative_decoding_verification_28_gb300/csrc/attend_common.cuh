@@ -284,15 +284,92 @@ __device__ inline bool prompt_unit(const AttendArgs &a, const Shape &sh, AttendU
     return true;
 }
 
+// Joins up to P parts of a unit: a thread takes I times 4 Q columns of a row at
+// once, and everything that those need comes in one round of loads.
+template <typename T, int ROWS, int P, int I, int Q>
+__device__ __forceinline__ void join_few_parts(const AttendArgs &a, const AttendUnit &u, int t, int threads)
+{
+    const int D = a.cache.D, dp = part_cols(D), quads = dp / 4, items = u.n_rows * ((quads + Q - 1) / Q);
+    T *out = reinterpret_cast<T *>(a.out);
+    const bool wide = D % 8 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
+    for (int w0 = t; w0 < items; w0 += I * threads) {
+        float mp[I][P], lp[I][P];
+        float4 x[I][P][Q];
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            const int w = w0 + i * threads, g = w / u.n_rows, r = w - g * u.n_rows;
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const bool in = w < items && p < u.n_parts;
+                const float *slot = part_slot<ROWS>(a, u.first_cta + p, p);
+                mp[i][p] = in ? __ldcg(slot + (size_t)ROWS * dp + r) : -INFINITY;
+                lp[i][p] = in ? __ldcg(slot + (size_t)ROWS * dp + ROWS + r) : 0.0f;
+#pragma unroll
+                for (int k = 0; k < Q; ++k)
+                    x[i][p][k] = in && Q * g + k < quads
+                                     ? __ldcg(reinterpret_cast<const float4 *>(slot + part_quad<ROWS>(Q * g + k, r)))
+                                     : make_float4(0, 0, 0, 0);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            const int w = w0 + i * threads, g = w / u.n_rows, r = w - g * u.n_rows;
+            if (w >= items)
+                break;
+            float m = -INFINITY, l = 0.0f, o[4 * Q] = {};
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                m = fmaxf(m, mp[i][p]);
+            const float m0 = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const float f = exp2f(mp[i][p] - m0);
+                l = fmaf(f, lp[i][p], l);
+#pragma unroll
+                for (int k = 0; k < Q; ++k) {
+                    o[4 * k] = fmaf(f, x[i][p][k].x, o[4 * k]);
+                    o[4 * k + 1] = fmaf(f, x[i][p][k].y, o[4 * k + 1]);
+                    o[4 * k + 2] = fmaf(f, x[i][p][k].z, o[4 * k + 2]);
+                    o[4 * k + 3] = fmaf(f, x[i][p][k].w, o[4 * k + 3]);
+                }
+            }
+            const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+            T *dst = out + row_place(a, u, r) + 4 * Q * g;
+            T v[4 * Q];
+#pragma unroll
+            for (int e = 0; e < 4 * Q; ++e)
+                v[e] = round_to<T>(o[e] * inv);
+#pragma unroll
+            for (int e = 0; e < 4 * Q; e += 8) {
+                if (4 * Q * g + e >= D)
+                    break;
+                if (wide) {
+#pragma unroll
+                    for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
+                        uint4 y;
+                        memcpy(&y, v + e + 16 / sizeof(T) * k, 16);
+                        reinterpret_cast<uint4 *>(dst + e)[k] = y;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (4 * Q * g + e + k < D)
+                            dst[e + k] = v[e + k];
+                }
+            }
+        }
+    }
+}
+
 // Joins a unit's parts: O = sum 2^(m_p - m) O_p / sum 2^(m_p - m) l_p.  Called
 // by all `threads` threads of which this is t, after every part was seen;
 // `sync` is a barrier among them that orders their writes to the workspace
-// (false: it gave up).  A thread joins 16 columns of a row at a time; what that
-// costs is its loads' latency.  Where a thread has many to join, every row's
-// factors are formed first, in place of the parts' maxima, which leaves one
-// round of loads each (252 rows: 18000 -> 8000 cycles); where it has few, the
-// factors come with the sums (4 rows: two rounds and no barrier).  A row that
-// no part saw anything for (every l zero) gives zeros.
+// (false: it gave up).  What a join costs is its rounds of loads, a latency
+// each: with few parts everything comes in one (join_few_parts; decoding at
+// batch 32 43 -> 40 us, trees of 64 nodes and 7 heads 119 -> 115).  Else every
+// row's factors are formed first where a thread has many rows to join, in
+// place of the parts' maxima, or come with the sums where it has few.  A row
+// that no part saw anything for (every l zero) gives zeros.
 template <typename T, int ROWS, typename Sync>
 __device__ bool join_parts(const AttendArgs &a, const AttendUnit &u, int t, int threads, Sync sync)
 {
@@ -313,6 +390,14 @@ __device__ bool join_parts(const AttendArgs &a, const AttendUnit &u, int t, int 
         inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
     };
     const bool many = u.n_rows * groups > 4 * threads;
+    if (!many && u.n_parts <= 4) {
+        join_few_parts<T, ROWS, 4, 1, 2>(a, u, t, threads);
+        return true;
+    }
+    if (many && u.n_parts == 2) {
+        join_few_parts<T, ROWS, 2, 2, 4>(a, u, t, threads);
+        return true;
+    }
     if (many) {
         for (int r = t; r < u.n_rows; r += threads) {
             float m0, inv;
