@@ -247,18 +247,82 @@ __device__ __forceinline__ uint2 ld_stream8(const uint2 *p)
     return r;
 }
 
-// `share` warps per token (1 where there are tokens enough to fill the GPU,
-// up to 8 where there are not).  LPH lanes hold one head: 8 bytes of its first
-// half and the same 8 of its second, so that a rotation's pairs are in one
-// lane, as are the angles and norm weights of all heads of a token.  Rotation
-// over the whole head (R == D) or none.  The first loads are asked for before
-// anything else: what decides the token's place and angles is a chain of
-// three loads itself.  A first form with a CTA a token and 16 contiguous bytes
-// a lane (8 shuffles a vector for the pairs, angles and weights from shared
-// memory) was bound by its instructions: 216 us for 26624 tokens of 48 heads
-// of 128 in bf16, where HBM needs 96.  This one takes 129 us (5.1 TB/s), bound by
-// the loads in flight: 64 registers for a fourth CTA of 256 or loads for the
-// next head behind each head measured 130 and 154 us, two warps a token 139.
+// Both kernels below: LPH lanes hold one head, 8 bytes of its first half and
+// the same 8 of its second, so that a rotation's pairs are in one lane, as are
+// the angles and norm weights of all heads of a token.  Rotation over the whole
+// head (R == D) or none.  The first loads are asked for before anything else:
+// what decides the token's place and angles is a chain of three loads itself.
+// 26624 tokens of 48 heads of 128 in bf16, where HBM needs 96 us: a first form
+// with a CTA a token and 16 contiguous bytes a lane (8 shuffles a vector for the
+// pairs, angles and weights from shared memory) took 216, a warp a token with
+// all kinds of heads in one loop 129 (an issue slot in two was taken), this
+// split 105 (6.2 TB/s).  What bounds it is the loads in flight and what issues
+// between them: 2, 3 or 8 loads ahead instead of 4 measured 117, 114 and 110, 72
+// registers instead of 64 (7 CTAs instead of 8) 107.
+
+// cosines, sines and minus sines of a lane's pairs.  Half split: pair i of the
+// lane turns with frequency 2 NP ln + i; interleaved: elements (2 i, 2 i + 1)
+// of each half with NP ln + i and D / 4 + NP ln + i
+template <int NP, int D>
+__device__ __forceinline__ void turns(const AppendArgs &a, int pos, int ln, uint64_t *cs, uint64_t *sn, uint64_t *ns)
+{
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const int f0 = a.interleaved ? NP * ln + i : 2 * NP * ln + 2 * i;
+        const int f1 = a.interleaved ? D / 4 + NP * ln + i : f0 + 1;
+        const float2 t0 = turn(pos, a.inv_freq[f0]), t1 = turn(pos, a.inv_freq[f1]);
+        cs[i] = two(t0.x, t1.x);
+        sn[i] = two(t0.y, t1.y);
+        ns[i] = two(-t0.y, -t1.y);
+    }
+}
+// sum of the squares of a head, in each of its LPH lanes
+template <int NP, int LPH>
+__device__ __forceinline__ float square_sum(const uint64_t *x)
+{
+    uint64_t sq = two_mul(x[0], x[0]);
+#pragma unroll
+    for (int i = 1; i < 2 * NP; ++i)
+        sq = two_fma(x[i], x[i], sq);
+    const float2 q2 = parts(sq);
+    float sum = q2.x + q2.y;
+#pragma unroll
+    for (int k = LPH / 2; k > 0; k >>= 1)
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, k);
+    return sum;
+}
+template <int NP>
+__device__ __forceinline__ void scale(float inv, uint64_t *x, const uint64_t *g)
+{
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i)
+        x[i] = two_mul(two_mul(x[i], two(inv, inv)), g[i]);
+}
+template <int NP, int LPH, int D>
+__device__ __forceinline__ void norm(float eps, uint64_t *x, const uint64_t *g)
+{
+    scale<NP>(rsqrtf(square_sum<NP, LPH>(x) * (1.0f / D) + eps), x, g);
+}
+template <int NP>
+__device__ __forceinline__ void rotate(int interleaved, uint64_t *x, const uint64_t *cs, const uint64_t *sn,
+                                       const uint64_t *ns)
+{
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        if (!interleaved) {
+            const uint64_t l = x[i], h = x[NP + i];
+            x[i] = two_fma(l, cs[i], two_mul(h, ns[i]));
+            x[NP + i] = two_fma(h, cs[i], two_mul(l, sn[i]));
+        } else {
+            const float2 c = parts(cs[i]), s = parts(sn[i]), l = parts(x[i]), h = parts(x[NP + i]);
+            x[i] = two(l.x * c.x - l.y * s.x, l.y * c.x + l.x * s.x);
+            x[NP + i] = two(h.x * c.y - h.y * s.y, h.y * c.y + h.x * s.y);
+        }
+    }
+}
+
+// `share` warps per token, where there are not tokens enough to fill the GPU
+// with one each (2 to 8); all kinds of heads in one loop, as a warp has few.
 template <typename T, int LPH>
 __device__ __forceinline__ void append_token(const AppendArgs &a, int tokens, int share)
 {
@@ -304,20 +368,8 @@ __device__ __forceinline__ void append_token(const AppendArgs &a, int tokens, in
             q0 = head_dst<T>(a, tok, 0) + ln * 2 * NP;
             k0 = head_dst<T>(a, tok, a.Hq) + ln * 2 * NP;
             v0 = head_dst<T>(a, tok, a.Hq + a.cache.H) + ln * 2 * NP;
-            if (a.R) {
-                // half split: pair i of the lane turns with frequency 2 NP ln + i;
-                // interleaved: elements (2 i, 2 i + 1) of each half with
-                // NP ln + i and D / 4 + NP ln + i
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    const int f0 = a.interleaved ? NP * ln + i : 2 * NP * ln + 2 * i;
-                    const int f1 = a.interleaved ? D / 4 + NP * ln + i : f0 + 1;
-                    const float2 t0 = turn(tok.pos, a.inv_freq[f0]), t1 = turn(tok.pos, a.inv_freq[f1]);
-                    cs[i] = two(t0.x, t1.x);
-                    sn[i] = two(t0.y, t1.y);
-                    ns[i] = two(-t0.y, -t1.y);
-                }
-            }
+            if (a.R)
+                turns<NP, D>(a, tok.pos, ln, cs, sn, ns);
         }
 #pragma unroll
         for (int u = 0; u < kAppendAhead; ++u) {
@@ -332,37 +384,12 @@ __device__ __forceinline__ void append_token(const AppendArgs &a, int tokens, in
                 H8::load(mine ? hi[u] : make_uint2(0, 0), x + NP);
                 const bool is_q = head < a.Hq;
                 if (a.q_weight || a.k_weight) {  // the same for every thread
-                    uint64_t sq = two_mul(x[0], x[0]);
-#pragma unroll
-                    for (int i = 1; i < 2 * NP; ++i)
-                        sq = two_fma(x[i], x[i], sq);
-                    const float2 q2 = parts(sq);
-                    float sum = q2.x + q2.y;
-#pragma unroll
-                    for (int k = LPH / 2; k > 0; k >>= 1)
-                        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, k);
-                    if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr) {
-                        const float inv = rsqrtf(sum * (1.0f / D) + a.eps);
-#pragma unroll
-                        for (int i = 0; i < 2 * NP; ++i)
-                            x[i] = two_mul(two_mul(x[i], two(inv, inv)), is_q ? gq[i] : gk[i]);
-                    }
+                    const float sum = square_sum<NP, LPH>(x);
+                    if (is_q ? a.q_weight != nullptr : a.k_weight != nullptr)
+                        scale<NP>(rsqrtf(sum * (1.0f / D) + a.eps), x, is_q ? gq : gk);
                 }
-                if (a.R && !a.interleaved) {
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) {
-                        const uint64_t l = x[i], h = x[NP + i];
-                        x[i] = two_fma(l, cs[i], two_mul(h, ns[i]));
-                        x[NP + i] = two_fma(h, cs[i], two_mul(l, sn[i]));
-                    }
-                } else if (a.R) {
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) {
-                        const float2 c = parts(cs[i]), s = parts(sn[i]), l = parts(x[i]), h = parts(x[NP + i]);
-                        x[i] = two(l.x * c.x - l.y * s.x, l.y * c.x + l.x * s.x);
-                        x[NP + i] = two(h.x * c.y - h.y * s.y, h.y * c.y + h.x * s.y);
-                    }
-                }
+                if (a.R)
+                    rotate<NP>(a.interleaved, x, cs, sn, ns);
                 if (!is_v) {
                     ol = H8::store(x);
                     oh = H8::store(x + NP);
@@ -377,11 +404,107 @@ __device__ __forceinline__ void append_token(const AppendArgs &a, int tokens, in
     }
 }
 
+// A warp a token, the heads of a kind after one another: what a head is, its
+// weights and where it goes are then the same for the whole warp.
+template <typename T, int LPH>
+__device__ __forceinline__ void append_whole_token(const AppendArgs &a, int tokens)
+{
+    using H8 = Half8<T>;
+    constexpr int NP = H8::kPairs, D = LPH * 16 / (int)sizeof(T), HPW = 32 / LPH, UP = kAppendAhead;
+    const int lane = threadIdx.x & 31, ln = lane % LPH, sub = lane / LPH;
+    const uint32_t m = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    if (m >= (uint32_t)tokens)
+        return;
+    const int H = a.cache.H;
+    const T *src = reinterpret_cast<const T *>(a.qkv) + ((size_t)m * (a.Hq + 2 * H) + sub) * D + ln * 2 * NP;
+    uint2 lo[UP], hi[UP];
+    // heads at + u HPW + sub of the n from p on
+    auto load = [&](const T *p, int at, int n) {
+#pragma unroll
+        for (int u = 0; u < UP; ++u)
+            if (at + u * HPW + sub < n) {
+                lo[u] = ld_stream8(reinterpret_cast<const uint2 *>(p + (size_t)at * D + u * HPW * D));
+                hi[u] = ld_stream8(reinterpret_cast<const uint2 *>(p + (size_t)at * D + u * HPW * D + D / 2));
+            }
+    };
+    load(src, 0, a.Hq);
+    uint64_t g[NP * 2];
+    auto weights = [&](const void *w) {
+        const T *p = reinterpret_cast<const T *>(w) + ln * 2 * NP;
+        H8::load(__ldg(reinterpret_cast<const uint2 *>(p)), g);
+        H8::load(__ldg(reinterpret_cast<const uint2 *>(p + D / 2)), g + NP);
+    };
+    if (a.q_weight)
+        weights(a.q_weight);
+    const Token tok = find_token(a, m);
+    if (!tok.live)
+        return;  // the whole warp
+    uint64_t cs[NP], sn[NP], ns[NP];
+    if (a.R)
+        turns<NP, D>(a, tok.pos, ln, cs, sn, ns);
+    auto turn_store = [&](T *dst, long long head_step, int at, int n, const void *w) {
+        dst += ln * 2 * NP + (at + sub) * head_step;
+#pragma unroll
+        for (int u = 0; u < UP; ++u) {
+            if (at + u * HPW >= n)
+                break;
+            uint64_t x[2 * NP];
+            H8::load(lo[u], x);
+            H8::load(hi[u], x + NP);
+            if (w)
+                norm<NP, LPH, D>(a.eps, x, g);
+            if (a.R)
+                rotate<NP>(a.interleaved, x, cs, sn, ns);
+            if (at + u * HPW + sub < n) {
+                T *d = dst + u * HPW * head_step;
+                *reinterpret_cast<uint2 *>(d) = H8::store(x);
+                *reinterpret_cast<uint2 *>(d + D / 2) = H8::store(x + NP);
+            }
+        }
+    };
+    T *q0 = head_dst<T>(a, tok, 0), *k0 = head_dst<T>(a, tok, a.Hq), *v0 = head_dst<T>(a, tok, a.Hq + H);
+    for (int at = 0;;) {
+        turn_store(q0, D, at, a.Hq, a.q_weight);
+        at += UP * HPW;
+        if (at >= a.Hq)
+            break;
+        load(src, at, a.Hq);
+    }
+    src += (size_t)a.Hq * D;
+    load(src, 0, H);
+    if (a.k_weight)
+        weights(a.k_weight);
+    for (int at = 0;;) {
+        turn_store(k0, tok.head_step, at, H, a.k_weight);
+        at += UP * HPW;
+        if (at >= H)
+            break;
+        load(src, at, H);
+    }
+    src += (size_t)H * D;
+    for (int at = 0; at < H; at += UP * HPW) {
+        load(src, at, H);
+        T *dst = v0 + ln * 2 * NP + (at + sub) * tok.head_step;
+#pragma unroll
+        for (int u = 0; u < UP; ++u)
+            if (at + u * HPW + sub < H) {
+                *reinterpret_cast<uint2 *>(dst + u * HPW * tok.head_step) = lo[u];
+                *reinterpret_cast<uint2 *>(dst + u * HPW * tok.head_step + D / 2) = hi[u];
+            }
+    }
+}
+
 template <typename T, int LPH>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a, int tokens,
                                                                 int share)
 {
     append_token<T, LPH>(a, tokens, share);
+    append_flags(a);
+}
+template <typename T, int LPH>
+__global__ void __launch_bounds__(kAppendThreads, 8) append_whole_kernel(const __grid_constant__ AppendArgs a, int tokens)
+{
+    append_whole_token<T, LPH>(a, tokens);
     append_flags(a);
 }
 
@@ -456,7 +579,14 @@ cudaError_t launch_append_t(const AppendArgs &a, cudaStream_t st)
             share *= 2;
         const long long warps = (long long)tokens * share, per = kAppendThreads / 32;
         const unsigned grid = (unsigned)(warps > 0 ? (warps + per - 1) / per : 1);
-        if (bytes == 512)
+        if (share == 1) {
+            if (bytes == 512)
+                append_whole_kernel<T, 32><<<grid, kAppendThreads, 0, st>>>(a, tokens);
+            else if (bytes == 256)
+                append_whole_kernel<T, 16><<<grid, kAppendThreads, 0, st>>>(a, tokens);
+            else
+                append_whole_kernel<T, 8><<<grid, kAppendThreads, 0, st>>>(a, tokens);
+        } else if (bytes == 512)
             append_kernel<T, 32><<<grid, kAppendThreads, 0, st>>>(a, tokens, share);
         else if (bytes == 256)
             append_kernel<T, 16><<<grid, kAppendThreads, 0, st>>>(a, tokens, share);

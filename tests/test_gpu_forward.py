@@ -581,6 +581,35 @@ def test_append_many_sequences(dt):
         close(kvd, want_kv, tol_kv)
 
 
+@pytest.mark.parametrize("dt,D", [("f32", 128), ("f32", 32), ("bf16", 128), ("bf16", 64), ("f16", 256), ("f16", 128)])
+@pytest.mark.parametrize("G,H,inter,norm,rot", [(3, 3, False, "qk", True), (1, 9, True, "q", True), (7, 1, False, "k", False)])
+def test_append_many_tokens(dt, D, G, H, inter, norm, rot):
+    """Tokens enough for a warp each; numbers of heads that leave a warp's last
+    step, or its step itself, part empty."""
+    g = gen(39)
+    B, n, S = 5, 1001, 1010
+    M, Hq = B * n, G * H
+    qkv = randn(g, (M + 2, Hq + 2 * H, D), DT[dt])
+    qw = randn(g, (D,), DT[dt]) if "q" in norm else None
+    kw = randn(g, (D,), DT[dt]) if "k" in norm else None
+    inv = freqs(D) if rot else None
+    kv = torch.full((1, 2, B, H, S, D), 7.0, dtype=DT[dt], device="cuda")
+    cu = torch.arange(B + 1, dtype=torch.int32, device="cuda") * n
+    pad = i32([0, 9, 3, 1, 7])
+    q, flags = sv.spec_append_prompt(qkv.cuda(), kv, 0, cu, pad.cuda(), cu_(inv), q_weight=cu_(qw), k_weight=cu_(kw),
+                                     interleaved=inter)
+    assert (flags == 0).all()
+    want, k, v = append_ref(qkv[:M], H, torch.arange(n).repeat(B), qw, kw, 1e-6, inv, inter)
+    close(q[:M], want, ref.append_tol(want, DT[dt]))
+    for b in range(B):
+        p = int(pad[b])
+        got = kv[0, :, b].cpu()
+        wk = k[b * n:(b + 1) * n].transpose(0, 1)
+        close(got[0, :, p:p + n], wk, ref.append_tol(wk, DT[dt]))
+        assert torch.equal(got[1, :, p:p + n].double(), v[b * n:(b + 1) * n].transpose(0, 1).double())
+        assert (got[:, :, :p] == 7).all() and (got[:, :, p + n:] == 7).all()
+
+
 def test_append_extreme_heads():
     """All-zero heads, large and tiny ones, one that is not finite."""
     g = gen(33)
