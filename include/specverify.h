@@ -3,7 +3,9 @@
  * hot path of batch speculative decoding: per-round verification of k draft
  * tokens against k+1 target logit rows, and the ragged-to-rectangular
  * realignment of a contiguous left-padded KV cache, position IDs and
- * attention mask that variable acceptance forces.
+ * attention mask that variable acceptance forces; and for the forward pass
+ * around a round (last part): appending to that cache, attention over it, and
+ * drafted trees.
  *
  * Pages the operations are defined on (cited by title and section):
  *   "Correctness Forensics for Batch Speculative Decoding: Diagnosing the
@@ -28,7 +30,8 @@
  *     spec_workspace_bytes(B, k, V) bytes, 256-byte aligned.  It must be
  *     zero-filled before its first use (spec_workspace_init does that); every
  *     call that completes leaves its counters at zero again, so later calls
- *     need no re-zeroing.  Calls that share one workspace must be ordered
+ *     need no re-zeroing (calls whose workspace differs say so).  Calls that
+ *     share one workspace must be ordered
  *     (the same stream, or events); concurrent calls need separate
  *     workspaces.
  */

@@ -20,7 +20,17 @@
 //                   rows do not see them (0 * inf would reach those rows)
 // NT = 1 (up to 128 query rows): S has two buffers, so the next tile's scores
 // form while this tile's weights do.  NT = 2: the two tiles take turns on the
-// tensor pipe.
+// tensor pipe, one's product runs under the other's softmax.
+//
+// Bound by the softmax's chain (scores from TMEM, maximum, exponentials,
+// weights to TMEM) against the tensor pipe, which is busy 60% of the time: two
+// prompts of 8192 tokens, 32 / 8 heads of 128, take 760 us (1.45 PFLOP/s, 0.76
+// of a large matrix product).  Slower were: all 128 scores held in registers
+// (776 us at the time, against 760), weights handed over by halves (829, 813),
+// products of transposed operands and two chains to a CTA for few rows (159 and
+// 145 us for chains, against 127).  A round of 32 trees of 64 nodes, 28 / 4
+// heads, takes 115 us: units of some 20 tiles, whose start, end and join do not
+// overlap.
 #include "tcgen.cuh"
 
 namespace spec {
@@ -673,7 +683,9 @@ cudaError_t launch_attend_tc(const AttendArgs &a, spec_dtype dt, cudaStream_t st
 {
     // Small units two to an SM, or large ones with two chains each?  Rounds: small
     // up to 64 rows a key head (decoding at batch 32 41 us, 47 with one large
-    // unit an SM); up to 128 rows take one query tile of attend_tc_kernel.
+    // unit an SM); up to 128 rows take one query tile of attend_tc_kernel (72
+    // rows, 32 sequences: 70 us, 84 with two; but 126 rows, 8 sequences, whose
+    // units are cut in many parts: 55, 47).
     // Prompts: small up to kShortPrompt tokens a sequence on average, where a
     // unit's start and end cost more than its tiles (mean 158 tokens: 22.5 us
     // against 28.7; 200: 32.8, 36.9; 512: equal; 1200: 139, 135; 2000: 295, 276).
