@@ -70,9 +70,12 @@ def _at(t, dtype, name, dev, shape):
     return t.data_ptr()
 
 
-def _out(t, shape, dtype, dev, name):
+def _out(t, shape, dtype, dev, name, like=None):
+    """t checked, or when None a new tensor; like: a checked tensor of the same
+    kind, where there is one (allocations are half of a small call's time, and
+    this one is shorter)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=dev) if like is None else torch.empty_like(like)
     _at(t, dtype, name, dev, shape)
     return t
 
@@ -168,10 +171,11 @@ def spec_append_round(qkv, kv, layer, length, pad, inv_freq, q_weight=None, k_we
     dev, dt, (L, N, H, S, D), Hq, x, qw, kw, inv, R = _append_common(qkv, kv, layer, inv_freq, q_weight, k_weight, 2)
     B, T = qkv.shape[:2]
     rows = B,
+    length_at = _at(length, _I32, "length", dev, rows)
     q_out = _out(q_out, (B, T, Hq, D), dt, dev, "q_out")
-    flags = _out(flags, rows, _I32, dev, "flags")
+    flags = _out(flags, rows, _I32, dev, "flags", length)
     _call(_lib.load().spec_append_round, dev, x, _DT[dt], B, T, Hq, kv.data_ptr(), L, N, H, S, D, layer,
-          _at(length, _I32, "length", dev, rows), _at(pad, _I32, "pad", dev, rows), _rows(idx, B, N, dev),
+          length_at, _at(pad, _I32, "pad", dev, rows), _rows(idx, B, N, dev),
           _at(n_nodes, _I32, "n_nodes", dev, rows), _at(depth, _I32, "depth", dev, (B, T)),
           _at(staged, dt, "staged", dev, (L, 2, B, H, T, D)), qw, kw, eps, inv, R, 1 if interleaved else 0,
           q_out.data_ptr(), flags.data_ptr())
@@ -215,15 +219,16 @@ def spec_attend_round(q, kv, layer, length, pad, tree_mask=None, n_nodes=None, i
     if Dq != D:
         raise ValueError(f"q must be [B, T, Hq, {D}]")
     rows = B,
-    out = _out(out, shape, dt, dev, "out")
-    flags = _out(flags, rows, _I32, dev, "flags")
+    q_at, length_at = _at(q, dt, "q", dev, shape), _at(length, _I32, "length", dev, rows)
+    out = _out(out, shape, dt, dev, "out", q)
+    flags = _out(flags, rows, _I32, dev, "flags", length)
     lib = _lib.load()
     need = _attend_bytes.get((T, Hq, H, D))
     if need is None:
         need = _attend_bytes[T, Hq, H, D] = lib.spec_attend_workspace_bytes(T, Hq, H, D)
     ws = _ws(workspace, "attend", need, dev, ATTEND_ZERO)
-    _call(lib.spec_attend_round, dev, _at(q, dt, "q", dev, shape), _DT[dt], B, T, Hq, kv.data_ptr(), L, N, H, S, D,
-          layer, _at(length, _I32, "length", dev, rows), _at(pad, _I32, "pad", dev, rows), _rows(idx, B, N, dev),
+    _call(lib.spec_attend_round, dev, q_at, _DT[dt], B, T, Hq, kv.data_ptr(), L, N, H, S, D,
+          layer, length_at, _at(pad, _I32, "pad", dev, rows), _rows(idx, B, N, dev),
           _at(n_nodes, _I32, "n_nodes", dev, rows), _at(tree_mask, torch.int64, "tree_mask", dev, (B, T)),
           _at(staged, dt, "staged", dev, (L, 2, B, H, T, D)), D ** -0.5 if scale is None else scale, out.data_ptr(),
           flags.data_ptr(), ws.data_ptr(), ws.numel())
@@ -241,9 +246,10 @@ def spec_attend_prompt(q, kv, layer, cu, pad, start=None, idx=None, scale=None, 
         raise ValueError(f"q must be [M, Hq, {D}]")
     B = cu.shape[0] - 1
     rows = B,
-    out = _out(out, shape, dt, dev, "out")
+    q_at = _at(q, dt, "q", dev, shape)
+    out = _out(out, shape, dt, dev, "out", q)
     flags = _out(flags, rows, _I32, dev, "flags")
-    _call(_lib.load().spec_attend_prompt, dev, _at(q, dt, "q", dev, shape), _DT[dt], M, Hq, kv.data_ptr(), L, N, H, S,
+    _call(_lib.load().spec_attend_prompt, dev, q_at, _DT[dt], M, Hq, kv.data_ptr(), L, N, H, S,
           D, layer, B, _at(cu, _I32, "cu", dev, (B + 1,)), _at(start, _I32, "start", dev, rows),
           _at(pad, _I32, "pad", dev, rows), _rows(idx, B, N, dev), D ** -0.5 if scale is None else scale,
           out.data_ptr(), flags.data_ptr())
@@ -266,15 +272,16 @@ def spec_verify_tree(target_logits, tokens, parent, n_nodes=None, eos_id=-1, rem
     if dt not in _DT:
         raise ValueError(f"unsupported logits dtype {dt}")
     rows, nodes = (B,), (B, T)
-    out_tokens = _out(out_tokens, nodes, _I32, dev, "out_tokens")
-    path = _out(path, nodes, _I32, dev, "path")
+    parent_at = _at(parent, _I32, "parent", dev, nodes)
+    out_tokens = _out(out_tokens, nodes, _I32, dev, "out_tokens", parent)
+    path = _out(path, nodes, _I32, dev, "path", parent)
     n_accept = _out(n_accept, rows, _I32, dev, "n_accept")
-    n_emit = _out(n_emit, rows, _I32, dev, "n_emit")
-    flags = _out(flags, rows, _I32, dev, "flags")
+    n_emit = _out(n_emit, rows, _I32, dev, "n_emit", n_accept)
+    flags = _out(flags, rows, _I32, dev, "flags", n_accept)
     lib = _lib.load()
     ws = _ws(workspace, "tree", 256 * B, dev, 0)  # at least what the call needs
     _call(lib.spec_verify_tree, dev, target_logits.data_ptr(), _DT[dt], B, T, V, _at(tokens, _I32, "tokens", dev, nodes),
-          _at(parent, _I32, "parent", dev, nodes), _at(n_nodes, _I32, "n_nodes", dev, rows), int(eos_id),
+          parent_at, _at(n_nodes, _I32, "n_nodes", dev, rows), int(eos_id),
           _at(remaining, _I32, "remaining", dev, rows), out_tokens.data_ptr(), path.data_ptr(), n_accept.data_ptr(),
           n_emit.data_ptr(), flags.data_ptr(), ws.data_ptr(), ws.numel())
     return out_tokens, path, n_accept, n_emit, flags
@@ -289,9 +296,10 @@ def spec_commit_tree(staged, kv, length, pad, path, n_emit, idx=None, flags=None
     dt = kv.dtype
     B, T = path.shape
     rows = B,
-    flags = _out(flags, rows, _I32, dev, "flags")
+    length_at = _at(length, _I32, "length", dev, rows)
+    flags = _out(flags, rows, _I32, dev, "flags", length)
     _call(_lib.load().spec_commit_tree, dev, _at(staged, dt, "staged", dev, (L, 2, B, H, T, D)), kv.data_ptr(), _DT[dt],
-          L, B, T, N, H, S, D, _at(length, _I32, "length", dev, rows), _at(pad, _I32, "pad", dev, rows),
+          L, B, T, N, H, S, D, length_at, _at(pad, _I32, "pad", dev, rows),
           _at(path, _I32, "path", dev, (B, T)), _at(n_emit, _I32, "n_emit", dev, rows), _rows(idx, B, N, dev),
           flags.data_ptr())
     return flags
