@@ -124,6 +124,13 @@ def test_attend_round_long_context_is_split(dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,G,D", [(1, 1, 64), (3, 2, 128), (9, 4, 64), (20, 5, 128), (64, 4, 128), (64, 7, 64), (13, 3, 36)])
+def test_attend_round_units_of_two_to_many_parts(dt, T, G, D):
+    """Few units, cut every two tiles: parts from 2 on, joined in each of the ways there are."""
+    check_round(round_case(40, DT[dt], 5, T, G, 2, D, 1400, [130, 250, 400, 700, 1250], tree=T > 1, staged=T > 1))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("D", [64, 80])
 def test_attend_round_rows_that_see_nothing_give_zeros(dt, D):
     c = round_case(9, DT[dt], 4, 6, 2, 2, D, 200, [1, 1, 1, 150], tree=True, staged=True, full=True)
@@ -836,3 +843,95 @@ def test_commit_tree_flags():
     assert flags.tolist() == [0, 0, 16, 16, 0, 16, 16, 0]
     for r in (2, 3, 5, 6):
         assert torch.equal(kv[:, :, r], before[:, :, r])
+
+
+# ---------------------------------------------------------------------------
+# all of them
+# ---------------------------------------------------------------------------
+def test_offsets_past_32_bits():
+    """Append, prompt attention and commit at the far end of a cache of more
+    than 2^32 elements, and a walk over logits of more than 2^31."""
+    free, _ = torch.cuda.mem_get_info()
+    N, H, S, D = 33, 2, 1 << 18, 128
+    if free < 2 * N * H * S * D * 2 + (8 << 30):
+        pytest.skip("not enough memory")
+    g = gen(60)
+    kv = torch.empty((1, 2, N, H, S, D), dtype=torch.bfloat16, device="cuda")
+    idx, pad, n = i32([N - 1, N - 2]), i32([S - 110, 3]), [100, 77]
+    cu = i32([0, 100, 177])
+    qkv = randn(g, (177, 4 + 2 * H, D), torch.bfloat16)
+    q, flags = sv.spec_append_prompt(qkv.cuda(), kv, 0, cu.cuda(), pad.cuda(), None, idx=idx.cuda())
+    assert (flags == 0).all() and torch.equal(q.cpu(), qkv[:, :4])
+    small = torch.zeros((1, 2, 2, H, 120, D), dtype=torch.bfloat16)
+    for b in range(2):
+        x, p = qkv[cu[b]:cu[b + 1]], int(pad[b])
+        small[0, 0, b, :, :n[b]] = x[:, 4:4 + H].transpose(0, 1)
+        small[0, 1, b, :, :n[b]] = x[:, 4 + H:].transpose(0, 1)
+        assert torch.equal(kv[0, :, int(idx[b]), :, p:p + n[b]].cpu(), small[0, :, b, :, :n[b]])
+    o, flags = sv.spec_attend_prompt(q, kv, 0, cu.cuda(), pad.cuda(), idx=idx.cuda())
+    want, tol = ref.attend_prompt(qkv[:, :4], small, 0, cu, i32([0, 0]), i32([0, 0]))
+    assert (flags == 0).all()
+    close(o, want, tol)
+    st = randn(g, (1, 2, 2, H, 5, D), torch.bfloat16)
+    path = i32([[0, 2, 4, -1, -1], [0, 1, -1, -1, -1]])
+    flags = sv.spec_commit_tree(st.cuda(), kv, i32([101, 78]).cuda(), pad.cuda(), path.cuda(), i32([3, 2]).cuda(), idx=idx.cuda())
+    assert (flags == 0).all()
+    for b, rows in ((0, [0, 2, 4]), (1, [0, 1])):
+        at = int(pad[b]) + n[b]
+        assert torch.equal(kv[0, :, int(idx[b]), :, at:at + len(rows)].cpu(), st[0, :, b][:, :, rows])
+    del kv
+    B, T, V = 2, 64, 17_000_000
+    x = torch.zeros((B, T, V), dtype=torch.bfloat16, device="cuda")
+    assert x.numel() > 1 << 31
+    best = [[int(v) for v in torch.randint(0, V, (T,), generator=g)] for _ in range(B)]
+    for b in range(B):
+        for i in range(T):
+            x[b, i, best[b][i]] = 1
+    parent = i32([list(range(-1, T - 1))] * B)
+    tokens = i32([[0] + r[:-1] for r in best])
+    out, path, acc, emit, flags = sv.spec_verify_tree(x, tokens.cuda(), parent.cuda())
+    assert (flags == 0).all() and emit.tolist() == [T] * B and acc.tolist() == [T - 1] * B
+    assert out.tolist() == best and path.tolist() == [list(range(T))] * B
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_calls_on_two_streams_at_once(dt):
+    """Two rounds of calls on streams of their own, and two captured ones
+    replayed side by side, give what each gives alone."""
+    cases = [round_case(61, DT[dt], 6, 9, 4, 2, 64, 900, [800, 500, 60, 700, 3, 350]),
+             round_case(62, DT[dt], 3, 64, 4, 2, 128, 700, [600, 20, 333], tree=True, staged=True)]
+    dev = [{k: cu_(v) for k, v in c.items()} for c in cases]
+    g = gen(63)
+    logits = randn(g, (7, 9, 5000), DT[dt]).cuda()
+    parent = i32([list(range(-1, 8))] * 7).cuda()
+    tokens = torch.cat([parent[:, :1], logits.float().argmax(-1).to(torch.int32)[:, :-1]], 1)
+
+    def work(d):
+        o, f = sv.spec_attend_round(d["q"], d["kv"], 1, d["length"], d["pad"], tree_mask=d["mask"], n_nodes=d["n"],
+                                    staged=d["staged"], out=torch.zeros_like(d["q"]))
+        return (o, f) + sv.spec_verify_tree(logits, tokens, parent)
+
+    alone = [work(d) for d in dev]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in dev]
+    got = [[], []]
+    for _ in range(20):
+        for i, (s, d) in enumerate(zip(streams, dev)):
+            with torch.cuda.stream(s):
+                got[i].append(work(d))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, y) for r in got[i] for x, y in zip(r, alone[i]))
+    graphs, outs = [], []
+    for d in dev:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append([work(d) for _ in range(10)])
+        graphs.append(gr)
+    for _ in range(3):
+        for s, gr in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                gr.replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(x, y) for r in outs[i] for x, y in zip(r, alone[i]))
