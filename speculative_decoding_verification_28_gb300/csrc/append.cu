@@ -54,18 +54,19 @@ __device__ Token find_token(const AppendArgs &a, long long m)
     int b, i;
     if (a.seq.cu) {
         // the sequences that end at or before m come before m's: counted by
-        // each warp in one pass over cu, which also looks at its order
-        const int lane = threadIdx.x & 31;
+        // each warp in one pass over cu, which also looks at its order (the
+        // lanes' counts meet at the end, so that the loads need not wait for
+        // one another)
         int before = 0;
-        unsigned broken = 0;
-        for (int c = 0; c < a.seq.B; c += 32) {
-            const bool in = c + lane < a.seq.B;
-            const int lo = in ? a.seq.cu[c + lane] : 0, hi = in ? a.seq.cu[c + lane + 1] : 0;
-            before += __popc(__ballot_sync(0xFFFFFFFFu, in && hi <= m));
-            broken |= __ballot_sync(0xFFFFFFFFu, hi < lo);
+        bool broken = false;
+#pragma unroll 8
+        for (int c = threadIdx.x & 31; c < a.seq.B; c += 32) {
+            const int lo = a.seq.cu[c], hi = a.seq.cu[c + 1];
+            before += hi <= m;
+            broken |= hi < lo;
         }
-        b = before;
-        if (b >= a.seq.B || broken)
+        b = __reduce_add_sync(0xFFFFFFFFu, before);
+        if (b >= a.seq.B || __any_sync(0xFFFFFFFFu, broken))
             return t;
     } else {
         b = (int)((uint32_t)m / (uint32_t)a.seq.T);

@@ -232,38 +232,62 @@ __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float x) { retu
 template <>
 __device__ __forceinline__ __half round_to<__half>(float x) { return __float2half_rn(x); }
 
-// The CTA that covers prompt unit blockIdx.x of key head blockIdx.y: units are
-// numbered from the last sequence's last rows down, so that the longest of a
-// sequence start first.  Every warp finds it from cu; false: no such unit.
-__device__ inline bool prompt_unit(const AttendArgs &a, const Shape &sh, AttendUnit &u)
+// inclusive sums over the warp's lanes
+__device__ __forceinline__ uint32_t warp_sums(uint32_t x)
 {
     const int lane = threadIdx.x & 31;
-    long long left = blockIdx.x;
-    unsigned broken = 0;
-    int b = -1, which = 0;
-    for (int c = 0; c < a.seq.B; c += 32) {
-        const int i = a.seq.B - 1 - (c + lane);
-        long long groups = 0;
-        bool bad = false;
-        if (i >= 0) {
-            groups = unit_groups(load_seq(a.seq, a.cache.N, a.cache.S, i), sh);
-            bad = a.seq.cu[i + 1] < a.seq.cu[i];
-        }
-        broken |= __ballot_sync(0xFFFFFFFFu, bad);
-        long long x = groups;
 #pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const long long o = __shfl_up_sync(0xFFFFFFFFu, x, m);
-            if (lane >= m)
-                x += o;
+    for (int m = 1; m < 32; m <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, x, m);
+        if (lane >= m)
+            x += o;
+    }
+    return x;
+}
+
+// The CTA that covers prompt unit blockIdx.x of key head blockIdx.y: units are
+// numbered from the last sequence's last rows down, so that the longest of a
+// sequence start first.  Every warp finds it from cu: each lane adds up the
+// units of B / 32 sequences, whose loads need not wait for one another, then
+// the warp goes over those of the lane that has it (against 32 sequences at a
+// time: 2000 prompts of 40 tokens 1235 us, 1814; 256 of 60 176, 225).  False:
+// no such unit.
+__device__ inline bool prompt_unit(const AttendArgs &a, const Shape &sh, AttendUnit &u)
+{
+    const int lane = threadIdx.x & 31, B = a.seq.B, share = (B + 31) / 32;
+    // units of the j-th sequence from the end; those of a call are fewer than 2^31
+    auto units = [&](int j) { return (uint32_t)unit_groups(load_seq(a.seq, a.cache.N, a.cache.S, B - 1 - j), sh); };
+    uint32_t left = blockIdx.x, mine = 0;
+    bool bad = false;
+    const int j0 = lane * share, j1 = min(B, j0 + share);
+#pragma unroll 4
+    for (int j = j0; j < j1; ++j) {
+        mine += units(j);
+        bad |= a.seq.cu[B - j] < a.seq.cu[B - 1 - j];
+    }
+    const bool broken = __any_sync(0xFFFFFFFFu, bad);
+    int b = -1, which = 0;
+    const uint32_t upto = warp_sums(mine);
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, left < upto);
+    if (hit) {
+        const int l = __ffs(hit) - 1;
+        if (share == 1) {
+            b = B - 1 - l;
+            which = (int)(__shfl_sync(0xFFFFFFFFu, upto, l) - 1 - left);  // last group first
+        } else {
+            left -= __shfl_sync(0xFFFFFFFFu, upto - mine, l);
+            for (int c = 0; c < share && b < 0; c += 32) {
+                const int j = l * share + c + lane;
+                const uint32_t x = warp_sums(c + lane < share && j < B ? units(j) : 0);
+                const unsigned in = __ballot_sync(0xFFFFFFFFu, left < x);
+                if (in) {
+                    const int k = __ffs(in) - 1;
+                    b = B - 1 - (l * share + c + k);
+                    which = (int)(__shfl_sync(0xFFFFFFFFu, x, k) - 1 - left);
+                }
+                left -= __shfl_sync(0xFFFFFFFFu, x, 31);
+            }
         }
-        const unsigned hit = __ballot_sync(0xFFFFFFFFu, left >= 0 && left < x);
-        if (b < 0 && hit) {
-            const int l = __ffs(hit) - 1;
-            b = a.seq.B - 1 - (c + l);
-            which = (int)(__shfl_sync(0xFFFFFFFFu, x, l) - 1 - left);  // last group first
-        }
-        left -= __shfl_sync(0xFFFFFFFFu, x, 31);
     }
     if (blockIdx.x == 0 && blockIdx.y == 0 && a.flags)
         for (int i = threadIdx.x; i < a.seq.B; i += blockDim.x)
