@@ -684,8 +684,7 @@ cudaError_t launch_attend_tc(const AttendArgs &a, spec_dtype dt, cudaStream_t st
     // Small units two to an SM, or large ones with two chains each?  Rounds: small
     // up to 64 rows a key head (decoding at batch 32 41 us, 47 with one large
     // unit an SM); up to 128 rows take one query tile of attend_tc_kernel (72
-    // rows, 32 sequences: 70 us, 84 with two; but 126 rows, 8 sequences, whose
-    // units are cut in many parts: 55, 47).
+    // rows, 32 sequences: 70 us, 84 with two; 126 rows, 8 sequences: 47 and 47).
     // Prompts: small up to kShortPrompt tokens a sequence on average, where a
     // unit's start and end cost more than its tiles (mean 158 tokens: 22.5 us
     // against 28.7; 200: 32.8, 36.9; 512: equal; 1200: 139, 135; 2000: 295, 276).
