@@ -391,9 +391,10 @@ def _own(s):
     c = s["case"]
     op = c["op"]
     if op == "attend":
-        # nodes behind a ragged tree's last are not written: the buffer is the program's, cleared once
         if "out" not in s:
-            s["out"] = torch.zeros_like(s["q"])
+            s["out"] = torch.empty_like(s["q"])
+        if c["tree"]:  # nodes behind a ragged tree's last are not written
+            s["out"].zero_()
         tree = dict(tree_mask=s["seen"], n_nodes=s["n"], staged=s["staged"]) if c["tree"] else {}
         return sv.spec_attend_round(s["q"], s["kv"], 0, s["length"], s["pad"], out=s["out"], **tree)[0]
     if op == "prompt":
@@ -404,7 +405,9 @@ def _own(s):
             q = sv.spec_append_prompt(s["qkv"], s["kv"], 0, s["cu"], s["pad"], s["inv_freq"], start=s["start"], **norm)[0]
             return {"q": q, "k_v": s["kv"]}
         if "q" not in s:
-            s["q"] = torch.zeros((c["B"], c["T"], c["Hq"], c["D"]), dtype=s["qkv"].dtype, device=s["qkv"].device)
+            s["q"] = torch.empty((c["B"], c["T"], c["Hq"], c["D"]), dtype=s["qkv"].dtype, device=s["qkv"].device)
+        if c["tree"]:
+            s["q"].zero_()
         tree = dict(depth=s["depth"], n_nodes=s["n"], staged=s["staged"]) if c["tree"] else {}
         q = sv.spec_append_round(s["qkv"], s["kv"], 0, s["length"], s["pad"], s["inv_freq"], q_out=s["q"], **norm,
                                  **tree)[0]
