@@ -503,6 +503,14 @@ SPEC_API int spec_attend_prompt(const void *q, spec_dtype dt, int M, int Hq, con
                        const int32_t *pad, const int32_t *idx, float scale, void *out, uint32_t *flags,
                        void *cuda_stream);
 
+/*
+ * For tests of SPEC_FLAG_TIMEOUT: the calling thread's next attention call, if
+ * it runs on the tensor cores (16-bit elements, heads of 64 or 128), waits for
+ * queries that never come and gives up after `clocks` (> 0) of an SM.  It ends
+ * like any other call, some seconds later; its outputs are undefined.
+ */
+SPEC_API int spec_attend_starve_next(int clocks);
+
 /* Workspace of spec_verify_tree (256-byte aligned; no initial value). */
 SPEC_API size_t spec_tree_workspace_bytes(int B);
 

@@ -61,6 +61,7 @@ SIGNATURES["spec_attend_round"] = ([_vp, _i32, _i32, _i32, _i32, _vp, _i32, _i32
                                     _vp, _vp, _vp, _f32, _vp, _vp, _vp, _sz, _vp], _i32)
 SIGNATURES["spec_attend_prompt"] = ([_vp, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp,
                                      _vp, _vp, _f32, _vp, _vp, _vp], _i32)
+SIGNATURES["spec_attend_starve_next"] = ([_i32], _i32)
 SIGNATURES["spec_tree_workspace_bytes"] = ([_i32], _sz)
 SIGNATURES["spec_verify_tree"] = ([_vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp,
                                    _vp, _vp, _sz, _vp], _i32)

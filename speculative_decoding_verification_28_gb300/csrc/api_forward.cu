@@ -132,6 +132,17 @@ int check_attend(const void *q, int dt, long long tokens, int Hq, int D, const v
     return aligned(q, e) && aligned(kv, e) && aligned(out, e) ? SPEC_OK : SPEC_EALIGN;
 }
 
+// How long an attention call's waits last before they give up, about 2 s; or,
+// for the thread's next call after spec_attend_starve_next, as long as that says.
+constexpr long long kWaitClocks = 4000000000ll;
+thread_local int starve_clocks = 0;
+void set_waits(AttendArgs &a)
+{
+    a.wait_clocks = starve_clocks > 0 ? starve_clocks : kWaitClocks;
+    a.starve = starve_clocks > 0;
+    starve_clocks = 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -252,6 +263,7 @@ int spec_attend_round(const void *q, spec_dtype dt, int B, int T, int Hq, const 
     a.scale_log2 = scale * 1.44269504088896340736f;
     a.flags = flags;
     a.ws = workspace;
+    set_waits(a);
     return launched(launch_attend(a, dt, (cudaStream_t)cuda_stream));
 }
 
@@ -282,7 +294,16 @@ int spec_attend_prompt(const void *q, spec_dtype dt, int M, int Hq, const void *
     a.G = Hq / H;
     a.scale_log2 = scale * 1.44269504088896340736f;
     a.flags = flags;
+    set_waits(a);
     return launched(launch_attend(a, dt, (cudaStream_t)cuda_stream));
+}
+
+int spec_attend_starve_next(int clocks)
+{
+    if (clocks < 1)
+        return SPEC_EINVAL;
+    starve_clocks = clocks;
+    return SPEC_OK;
 }
 
 size_t spec_tree_workspace_bytes(int B) { return tree_workspace(B); }

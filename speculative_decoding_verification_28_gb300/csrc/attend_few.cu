@@ -36,7 +36,8 @@ struct FewShape {
 template <int STAGES>
 struct FewShared {
     uint64_t kv_full[STAGES], kv_empty[STAGES];
-    uint64_t q_full, q_empty, s_full, p_full, pv_done, joined;
+    uint64_t q_full, q_empty, s_full, p_full, pv_done, joined, settled;
+    uint32_t asked_kv, asked_q;  // copies that the load warp asked for in all
     uint32_t scan[8];
     Run run;
     uint32_t tmem;
@@ -77,6 +78,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         mbar_init(&s.p_full, 4);
         mbar_init(&s.pv_done, 1);
         mbar_init(&s.joined, 4);
+        mbar_init(&s.settled, 1);
         fence_mbar_init();
         s.abort = 0;
         s.run.begin = s.run.end = 0;
@@ -103,8 +105,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     tc_fence_after();
     const uint32_t tmem = s.tmem, tm_o = tmem + 128;
 
+    const long long limit = a.wait_clocks;  // by itself: the waits' reference to all of `a` would put it on the stack
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
-        return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, &s.abort));
+        return __all_sync(0xFFFFFFFFu, wait_phase(bar, parity, &s.abort, limit));
     };
     Units<PROMPT> units(a, sh, s.run, first, some);
     AttendUnit u{};
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
 #pragma unroll
                     for (int kv = 0; kv < 2; ++kv) {
                         const int sg = it % ST;
-                        ok = ok && wait_phase(&s.kv_empty[sg], ((it / ST) & 1) ^ 1, &s.abort);
+                        ok = ok && wait_phase(&s.kv_empty[sg], ((it / ST) & 1) ^ 1, &s.abort, limit);
                         if (!ok)
                             break;
                         mbar_arrive_expect_tx(&s.kv_full[sg], k.bytes);
@@ -132,7 +135,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                                         &s.kv_full[sg]);
                         ++it;
                         if (tile == u.tile && kv == 0) {
-                            ok = wait_phase(&s.q_empty, (n & 1) ^ 1, &s.abort);
+                            ok = wait_phase(&s.q_empty, (n & 1) ^ 1, &s.abort, limit);
                             if (!ok)
                                 break;
                             mbar_arrive_expect_tx(&s.q_full, Sh::kPanels * box.q_tok * a.G * 128);
@@ -145,14 +148,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     }
                 }
             }
-            if (!ok) {
-                // after a wait that gave up: the copies in flight land first
-                for (uint32_t i = it > ST ? it - ST : 0; i < it; ++i)
-                    for (int k = 0; k < kTcWaitLimit && !mbar_try_wait(&s.kv_full[i % ST], (i / ST) & 1); ++k)
-                        ;
-                for (int k = 0; n > 0 && k < kTcWaitLimit && !mbar_try_wait(&s.q_full, (n - 1) & 1); ++k)
-                    ;
-            }
+            s.asked_kv = it;
+            s.asked_q = n;
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -428,6 +425,14 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         atomicOr(a.flags + u.b, SPEC_FLAG_TIMEOUT);
     tc_fence_before();
     __syncthreads();
+    if (s.abort) {
+        if (warp == kLoadWarp && lane == 0) {
+            await_copies<ST>(s.kv_full, s.asked_kv);
+            await_copies<1>(&s.q_full, s.asked_q);
+        }
+        if (warp == kMmaWarp)
+            await_products(&s.settled);
+    }
     if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem));
 }

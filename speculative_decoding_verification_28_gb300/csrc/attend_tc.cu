@@ -59,7 +59,8 @@ template <int STAGES>
 struct TcShared {
     uint64_t kv_full[STAGES], kv_empty[STAGES], q_full[2], q_empty[2];
     uint64_t v_ok[STAGES];  // guarded tiles: a stage's next one waits for its own consumption
-    uint64_t s_full[2], p_full[2], pv_done[2], joined;
+    uint64_t s_full[2], p_full[2], pv_done[2], joined, settled;
+    uint32_t asked_kv, asked_q;  // copies that the load warp asked for in all
     uint32_t scan[16];
     Run run;
     uint32_t tmem;
@@ -117,6 +118,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
             mbar_init(&s.pv_done[i], 1);
         }
         mbar_init(&s.joined, Sh::kSoftmax);
+        mbar_init(&s.settled, 1);
         fence_mbar_init();
         s.abort = 0;
         s.run.begin = s.run.end = 0;
@@ -141,7 +143,8 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
 
     // a bounded wait; after one that gave up every role leaves its loop.
     // wait1 is one lane's, wait the whole warp's (its answer is the warp's)
-    auto wait1 = [&](uint64_t *bar, uint32_t parity) -> bool { return wait_phase(bar, parity, &s.abort); };
+    const long long limit = a.wait_clocks;  // by itself: the waits' reference to all of `a` would put it on the stack
+    auto wait1 = [&](uint64_t *bar, uint32_t parity) -> bool { return wait_phase(bar, parity, &s.abort, limit); };
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
         return __all_sync(0xFFFFFFFFu, wait1(bar, parity));
     };
@@ -157,7 +160,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
         if constexpr (NT == 2 && !PROMPT)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (lane == 0) {
-            uint32_t it = 0, n = 0;
+            uint32_t it = 0, n = 0;  // tiles of keys and values, of queries
             bool ok = true;
             while (ok && units.next(u)) {
                 const int qb = n % Sh::kQBuf;
@@ -172,6 +175,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                     for (int p = 0; p < Sh::kPanels; ++p)
                         tma_load_4d(q_smem + (qb * NT + t) * Sh::kTile + p * Sh::kPanel, &maps.q, p * 64, 0, u.h,
                                     tok + t * box.tok_tile, &s.q_full[qb]);
+                ++n;
                 for (int tile = u.tile; ok && tile < u.tile_end; ++tile) {
                     const KvBox k = kv_box<Sh::kPanels>(a, maps, box, u, tile, !PROMPT && tile == u.n_tiles - 1);
 #pragma unroll
@@ -188,18 +192,9 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                         ++it;
                     }
                 }
-                ++n;
             }
-            if (!ok) {
-                // after a wait that gave up: the copies in flight land first
-                for (uint32_t i = it > ST ? it - ST : 0; i < it; ++i)
-                    for (int k = 0; k < kTcWaitLimit && !mbar_try_wait(&s.kv_full[i % ST], (i / ST) & 1); ++k)
-                        ;
-                for (uint32_t i = n > 0 ? n - 1 : 0; i <= n; ++i)
-                    for (int k = 0; k < kTcWaitLimit && !mbar_try_wait(&s.q_full[i % Sh::kQBuf], (i / Sh::kQBuf) & 1); ++k)
-                        if (i == n && k > 8)
-                            break;  // unit n's queries may not have been asked for
-            }
+            s.asked_kv = it;
+            s.asked_q = n;
         }
         __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -627,6 +622,14 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
         atomicOr(a.flags + u.b, SPEC_FLAG_TIMEOUT);
     tc_fence_before();
     __syncthreads();
+    if (s.abort) {
+        if (warp == kLoadWarp && lane == 0) {
+            await_copies<ST>(s.kv_full, s.asked_kv);
+            await_copies<Sh::kQBuf>(s.q_full, s.asked_q);
+        }
+        if (warp == kMmaWarp)
+            await_products(&s.settled);
+    }
     if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }

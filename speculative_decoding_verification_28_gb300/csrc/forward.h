@@ -113,6 +113,8 @@ struct AttendArgs {
     float scale_log2;      // scale * log2(e)
     uint32_t *flags;
     void *ws;
+    long long wait_clocks;  // SM clocks after which a wait gives up
+    int starve;             // test: queries that never seem whole (spec_attend_starve_next)
 };
 cudaError_t launch_attend(const AttendArgs &a, spec_dtype dt, cudaStream_t st);
 size_t attend_workspace(int T, int Hq, int H, int D);

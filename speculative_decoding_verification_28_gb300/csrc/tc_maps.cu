@@ -76,6 +76,8 @@ bool tc_make_maps(const AttendArgs &a, bool bf16, int tile_rows, TcMaps *maps, T
         if (!make_map(&maps->node, bf16, p, 3, dim, stride, bx))
             return false;
     }
+    if (a.starve)
+        ++box->q_tok;  // bytes are waited for that no copy brings
     return true;
 }
 

@@ -14,7 +14,6 @@ namespace spec {
 
 constexpr int kKeys = 128;  // keys of a tile
 constexpr int kTcWaitLimit = 2000;  // probes of up to ~1 ms, after a wait that gave up
-constexpr long long kTcWaitClocks = 4000000000ll;  // about 2 s
 constexpr float kLazy = 8.0f;       // base-2 headroom of the running maximum
 constexpr int kGuardRing = 8;       // units whose guard words may be live at once
 
@@ -433,7 +432,7 @@ struct Units {
 
 // Bounded wait of one thread for a phase; after one that gave up (`abort`
 // set) every other wait of the CTA returns too.
-__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, int *abort)
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, int *abort, long long limit)
 {
     if (mbar_poll(bar, parity))
         return true;
@@ -441,12 +440,33 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, int *
     while (!mbar_poll(bar, parity)) {
         if (*reinterpret_cast<volatile int *>(abort))
             return false;
-        if (clock64() - t0 > kTcWaitClocks) {
+        if (clock64() - t0 > limit) {
             *reinterpret_cast<volatile int *>(abort) = 1;
             return false;
         }
     }
     return true;
+}
+
+// What a CTA whose waits gave up does before it frees TMEM and leaves: its own
+// copies into shared memory and its own products have to land first (each with
+// a bounded wait), or they would write to memory that is another CTA's by then.
+// The last `n` copies into a ring of RING barriers; one thread.
+template <int RING>
+__device__ __forceinline__ void await_copies(uint64_t *full, uint32_t n)
+{
+    for (uint32_t i = n > RING ? n - RING : 0; i < n; ++i)
+        for (int k = 0; k < kTcWaitLimit && !mbar_try_wait(&full[i % RING], (i / RING) & 1); ++k)
+            ;
+}
+// All products; by the warp that issued them.
+__device__ __forceinline__ void await_products(uint64_t *bar)
+{
+    if (elect_one())
+        tc_commit(bar);
+    for (int k = 0; k < kTcWaitLimit && !mbar_try_wait(bar, 0); ++k)
+        ;
+    __syncwarp();
 }
 
 // K and V tile of a unit: one box of the cache's map or the nodes' map per
