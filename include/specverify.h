@@ -74,7 +74,9 @@ enum {
 #define SPEC_FLAG_BAD_STATE 16u /* a length, padding, count, index or offset out of range */
 #define SPEC_FLAG_BAD_TREE 32u  /* n_nodes outside [0, T], or a parent that is no earlier node */
 
-#define SPEC_FLAG_TIMEOUT 64u   /* a bounded wait gave up (never expected): output undefined */
+/* A bounded wait of an attention call gave up (never expected): set for every
+ * sequence of the call, whose outputs are all undefined. */
+#define SPEC_FLAG_TIMEOUT 64u
 
 /* Values of the realignment error word. */
 #define SPEC_REALIGN_OK 0
@@ -469,8 +471,9 @@ SPEC_API int spec_append_prompt(const void *qkv, spec_dtype dt, int M, int Hq, v
 
 /* Workspace of spec_attend_round (does not depend on B or S; 256-byte
  * aligned; its first SPEC_ATTEND_ZERO bytes zero before its first use, and
- * again after each call, unless one ended in SPEC_FLAG_TIMEOUT: clear them
- * then). */
+ * again after each call, unless one ended in SPEC_FLAG_TIMEOUT: every later
+ * call on the workspace then reports that too, with outputs as undefined, until
+ * they are cleared, as by spec_workspace_init). */
 #define SPEC_ATTEND_ZERO 2048
 SPEC_API size_t spec_attend_workspace_bytes(int T, int Hq, int H, int D);
 

@@ -88,6 +88,49 @@ __device__ uint32_t block_exclusive(uint32_t v, uint32_t *s, uint32_t *total)
     return before + x - v;
 }
 
+// ---------------------------------------------------------------------------
+// waits that gave up
+// ---------------------------------------------------------------------------
+constexpr size_t kPartHead = SPEC_ATTEND_ZERO;
+// the head's last word: not 0 once a wait of a call on the workspace gave up
+constexpr int kGaveUpWord = kPartHead / sizeof(int) - 1;
+static_assert(2 * kAttendCtas <= kGaveUpWord, "one counter per CTA");
+// A CTA that gives up leaves the rest of its run undone, and parts of cut units
+// uncounted, so that the counters say nothing any more: SPEC_FLAG_TIMEOUT is
+// the whole call's, and every later round's on the workspace until its head is
+// cleared.  (A prompt call's flags are written by its first CTA as it starts,
+// seconds before any wait can run out.)
+__device__ __forceinline__ bool gave_up(const AttendArgs &a)
+{
+    return *reinterpret_cast<const volatile int *>(static_cast<const int *>(a.ws) + kGaveUpWord) != 0;
+}
+// by one whole warp, as are the next two
+__device__ __forceinline__ void flag_timeout(const AttendArgs &a)
+{
+    if (a.flags)
+#pragma unroll 1
+        for (int b = threadIdx.x & 31; b < a.seq.B; b += 32)
+            atomicOr(a.flags + b, SPEC_FLAG_TIMEOUT);
+}
+// by a CTA that gave up
+__device__ __forceinline__ void give_up(const AttendArgs &a)
+{
+    if (a.ws && (threadIdx.x & 31) == 0)
+        atomicExch(static_cast<int *>(a.ws) + kGaveUpWord, 1);
+    __syncwarp();
+    __threadfence();
+    flag_timeout(a);
+}
+// By CTA 0 of a round after it wrote the flags (and a barrier of its threads).
+// Either this sees the word of a CTA that gave up, or that CTA's flags come
+// after those written here.
+__device__ __forceinline__ void flag_if_gave_up(const AttendArgs &a)
+{
+    __threadfence();
+    if (gave_up(a))
+        flag_timeout(a);
+}
+
 // Every thread takes a contiguous range of sequences; s_run is complete after
 // the caller's next __syncthreads.  CTA 0 writes the flags.
 template <int THREADS>
@@ -95,12 +138,13 @@ __device__ void find_run(const AttendArgs &a, const Shape &sh, uint32_t *s_scan,
 {
     const int per_thread = (a.seq.B + THREADS - 1) / THREADS;
     const int b0 = threadIdx.x * per_thread, b1 = min(a.seq.B, b0 + per_thread);
+    const uint32_t off = blockIdx.x == 0 && gave_up(a) ? SPEC_FLAG_TIMEOUT : 0u;  // a call before this one
     uint32_t w = 0;
     for (int b = b0; b < b1; ++b) {
         const Seq s = load_seq(a.seq, a.cache.N, a.cache.S, b);
         w += round_weight(s, sh, a.cache.H);
         if (blockIdx.x == 0 && a.flags)
-            a.flags[b] = s.ok ? 0u : SPEC_FLAG_BAD_STATE;
+            a.flags[b] = (s.ok ? 0u : SPEC_FLAG_BAD_STATE) | off;
     }
     uint32_t total;
     uint32_t at = block_exclusive<THREADS>(w, s_scan, &total);
@@ -186,13 +230,11 @@ struct UnitWalk {
 // ---------------------------------------------------------------------------
 // parts in the workspace
 // ---------------------------------------------------------------------------
-// [counters: one per CTA, zero between calls] [slots: two per CTA, one for the
+// [head: counters, one per CTA, zero between calls] [slots: two per CTA, one for the
 // unit that it finishes for others or passes on, one for the unit that starts
 // in it and is cut]; a slot is the sums, four columns of all ROWS rows after
 // another (threads that hold a row each then write and read side by side), ROWS
 // maxima (base 2) and ROWS sums of weights.
-constexpr size_t kPartHead = SPEC_ATTEND_ZERO;
-static_assert(2 * kAttendCtas * sizeof(int) <= kPartHead, "one counter per CTA");
 __host__ __device__ inline int part_cols(int D) { return (D + 3) & ~3; }
 template <int ROWS>
 __host__ __device__ inline size_t part_floats(int D)

@@ -212,6 +212,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         }
     } else {
         // ---------------------------------------------------------- softmax
+        if (!PROMPT && blockIdx.x == 0 && warp == 0)
+            flag_if_gave_up(a);
         const int r = tid;  // row of the unit = TMEM lane
         const uint32_t lanes = (uint32_t)warp << 21, tm_s = tmem + lanes;
         const float c = a.scale_log2;
@@ -421,8 +423,6 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             ++n;
         }
     }
-    if (*reinterpret_cast<volatile int *>(&s.abort) && lane == 0 && a.flags && u.seq.ok)
-        atomicOr(a.flags + u.b, SPEC_FLAG_TIMEOUT);
     tc_fence_before();
     __syncthreads();
     if (s.abort) {
@@ -430,8 +430,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
             await_copies<ST>(s.kv_full, s.asked_kv);
             await_copies<1>(&s.q_full, s.asked_q);
         }
-        if (warp == kMmaWarp)
+        if (warp == kMmaWarp) {
             await_products(&s.settled);
+            give_up(a);
+        }
     }
     if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem));

@@ -385,6 +385,8 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
         // ---------------------------------------------------------- softmax
         if constexpr (NT == 2 && !PROMPT)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        if (!PROMPT && blockIdx.x == 0 && warp == 0)
+            flag_if_gave_up(a);
         const int t = NT == 1 ? 0 : warp >> 2;
         const int r = (warp & 3) * 32 + lane;        // row of the tile = TMEM lane
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
@@ -618,8 +620,6 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
             ++n;
         }
     }
-    if (*reinterpret_cast<volatile int *>(&s.abort) && lane == 0 && a.flags && u.seq.ok)
-        atomicOr(a.flags + u.b, SPEC_FLAG_TIMEOUT);
     tc_fence_before();
     __syncthreads();
     if (s.abort) {
@@ -627,8 +627,10 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
             await_copies<ST>(s.kv_full, s.asked_kv);
             await_copies<Sh::kQBuf>(s.q_full, s.asked_q);
         }
-        if (warp == kMmaWarp)
+        if (warp == kMmaWarp) {
             await_products(&s.settled);
+            give_up(a);
+        }
     }
     if (warp == kMmaWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));

@@ -16,6 +16,10 @@ def starve():
     assert _lib.load().spec_attend_starve_next(CLOCKS) == 0
 
 
+def all_timed_out(flags):
+    return flags.tolist() == [TIMEOUT] * flags.numel()
+
+
 def i32(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
@@ -74,4 +78,48 @@ def test_calls_off_the_tensor_cores_do_not_wait():
     want, _ = sv.spec_attend_round(q, kv, 0, i32([30, 5]), None)
     starve()
     out, flags = sv.spec_attend_round(q, kv, 0, i32([30, 5]), None)
+    assert (flags == 0).all() and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("T,G,D", ROUNDS)
+def test_a_round_that_gives_up_flags_every_sequence(T, G, D):
+    """More units than CTAs: each CTA stands on the first of its run when it gives up."""
+    lens = [130 + 17 * (b % 23) for b in range(200)]
+    call, ws = a_round(T, G, D, torch.float16, lens)
+    want, flags = call()
+    assert (flags == 0).all()
+    starve()
+    _, flags = call()
+    assert all_timed_out(flags)
+    # and so does every later call on the workspace, until it is cleared
+    _, flags = call()
+    assert all_timed_out(flags)
+    ws[:sv.ATTEND_ZERO].zero_()
+    out, flags = call()
+    assert (flags == 0).all() and torch.equal(out, want)
+
+
+def test_prompts_that_give_up_flag_every_sequence():
+    lens = [40, 0, 100, 7]
+    cu = i32([sum(lens[:b]) for b in range(5)])
+    kv = torch.randn((1, 2, 4, 2, 128, 64), device="cuda").bfloat16()
+    q = torch.randn((147, 4, 64), device="cuda").bfloat16()
+    starve()
+    _, flags = sv.spec_attend_prompt(q, kv, 0, cu, None)
+    assert all_timed_out(flags)
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,G", [(1, 1), (9, 4), (20, 5), (64, 4)])
+def test_rounds_on_a_workspace_of_a_call_that_gave_up(dt, T, G):
+    """Whatever kernel comes next: its counters may be off, and it says so."""
+    call, ws = a_round(T, G, 64, dt, [300, 40, 700])
+    want, _ = call()
+    ws[:sv.ATTEND_ZERO].view(torch.int32)[-1] = 1
+    for _ in range(2):
+        _, flags = call()
+        assert all_timed_out(flags)
+    assert not ws[:sv.ATTEND_ZERO - 4].any()
+    ws[:sv.ATTEND_ZERO].zero_()
+    out, flags = call()
     assert (flags == 0).all() and torch.equal(out, want)
