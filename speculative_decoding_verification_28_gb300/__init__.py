@@ -43,11 +43,13 @@ from .forward import (  # noqa: F401,E402
     ATTEND_ZERO,
     FLAG_BAD_STATE,
     FLAG_BAD_TREE,
+    FLAG_TIMEOUT,
     MAX_HEAD_DIM,
     MAX_NODES,
     spec_append_prompt,
     spec_append_round,
     spec_attend_prompt,
+    spec_attend_reset,
     spec_attend_round,
     spec_attend_workspace_bytes,
     spec_commit_tree,

@@ -9,7 +9,9 @@ device), on which its outputs and scratch are allocated.  The tensors' device
 is made current for the call.  Scratch that is not passed
 in comes from a per-stream buffer; while a stream is being captured every call
 gets a buffer of its own from the graph's memory (cleared inside the graph),
-so captured graphs share none and may be replayed side by side.
+so captured graphs share none and may be replayed side by side.  After an attention
+call that reported FLAG_TIMEOUT (never expected) spec_attend_reset makes a
+stream's buffer good again.
 """
 from __future__ import annotations
 
@@ -20,7 +22,7 @@ import torch
 from . import _lib
 from .api import _DT, _check, _need
 
-FLAG_BAD_STATE, FLAG_BAD_TREE = 16, 32
+FLAG_BAD_STATE, FLAG_BAD_TREE, FLAG_TIMEOUT = 16, 32, 64
 MAX_NODES = 64
 MAX_HEAD_DIM = 256
 ATTEND_ZERO = 2048
@@ -204,6 +206,19 @@ _attend_bytes = {}  # spec_attend_workspace_bytes by its arguments
 
 def spec_attend_workspace_bytes(T, Hq, H, D):
     return int(_lib.load().spec_attend_workspace_bytes(int(T), int(Hq), int(H), int(D)))
+
+
+@_streamed
+def spec_attend_reset(device=None):
+    """After a spec_attend_round that reported FLAG_TIMEOUT: clears the head of
+    the scratch kept for the current stream (or stream=) of the device (default:
+    the current one), which every round on that stream reports FLAG_TIMEOUT for
+    until then.  A workspace of one's own: workspace[:ATTEND_ZERO].zero_()."""
+    i = None if device is None else torch.device(device).index
+    i = _device_now() if i is None else i
+    buf = _scratch.get(("attend", i, _raw_stream(i)))
+    if buf is not None:
+        buf[:ATTEND_ZERO].zero_()
 
 
 @_streamed

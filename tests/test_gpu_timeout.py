@@ -123,3 +123,34 @@ def test_rounds_on_a_workspace_of_a_call_that_gave_up(dt, T, G):
     ws[:sv.ATTEND_ZERO].zero_()
     out, flags = call()
     assert (flags == 0).all() and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_reset_of_the_scratch_kept_for_a_stream(own_stream):
+    """Calls without a workspace of their own, after one that gave up."""
+    kv = torch.randn((1, 2, 3, 2, 900, 128), device="cuda").bfloat16()
+    q = torch.randn((3, 5, 8, 128), device="cuda").bfloat16()
+    length = i32([800, 30, 500])
+    kw = {"stream": torch.cuda.Stream()} if own_stream else {}
+    torch.cuda.synchronize()
+
+    def call():
+        out, flags = sv.spec_attend_round(q, kv, 0, length, None, **kw)
+        torch.cuda.synchronize()
+        return out, flags
+
+    want, flags = call()
+    assert (flags == 0).all()
+    starve()
+    assert all_timed_out(call()[1]) and all_timed_out(call()[1])
+    # a captured call has scratch of its own
+    graph, o = torch.cuda.CUDAGraph(), torch.empty_like(q)
+    f = torch.empty_like(length)
+    with torch.cuda.graph(graph):
+        sv.spec_attend_round(q, kv, 0, length, None, out=o, flags=f)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert (f == 0).all() and torch.equal(o, want)
+    sv.spec_attend_reset(**kw)
+    out, flags = call()
+    assert (flags == 0).all() and torch.equal(out, want)
