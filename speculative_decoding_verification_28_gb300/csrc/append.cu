@@ -7,9 +7,9 @@
 // over the pairs j = i + R/2 (or (2i, 2i + 1) when interleaved); dimensions
 // past R are not turned.  Everything between the load and the store is fp32,
 // rounded once.  Values are copied.  The angle is a product of an integer
-// position and an fp32 frequency whose turns are what matters: it is formed
-// and reduced in fp64 (a position of 1e5 in fp32 would be off by 4e-3 turns),
-// once per token and pair, not per head.
+// position and an fp32 frequency, of which the fraction of its turns matters: it
+// is reduced to that by `turn` (rounded to fp32 as it is, a position of 1e5
+// would be off by 6e-4 turns), once per token and pair, not per head.
 //
 // Roofline: HBM, 2 * (Hq + 2H) * D * sizeof(T) bytes per token.
 #include "forward.h"
@@ -118,26 +118,34 @@ __device__ void append_flags(const AppendArgs &a)
     }
 }
 
-// cos and sin of pos * f.  Only the fraction of pos * f / (2 pi) turns counts,
-// and it is formed exactly enough for any position: f / (2 pi) is a pair g + h
-// of fp32 numbers (48 bits), pos * g is split by an FMA into its rounded value,
-// whose fraction is exact, and its error.  Below 2^24, where an fp32 pos is
-// exact, what is left off is under 2e-8 turns; beyond, fp64 (two lanes a clock
-// on this part, 10 times the time) does the same.
+// cos and sin of pos * f.  Only the fraction of pos * f / (2 pi) turns counts.
+// f / (2 pi) is a pair g + gl of fp32 numbers (48 bits); pos * g is split by an
+// FMA into its rounded value t, whose fraction is exact, and the rest e, and the
+// sum of the two keeps what its rounding leaves off (d).  For |pos * f| < 2^22,
+// and below 2^24 where an fp32 pos is exact, the error is then that of 48 bits
+// at 2^22 / (2 pi) turns: under 1e-8 turns.  Past either limit the same in fp64
+// (two lanes a clock on this part, 10 times the time), with an error below that
+// of the result's last place.
 __device__ __forceinline__ float2 turn(int pos, float f)
 {
-    float h, d = 0.0f;  // half turns in [-1, 1], and what its rounding left off
-    if (pos < (1 << 24)) {
+    float h, d;  // half turns in [-1, 1], and what its rounding left off, in radians
+    constexpr float kPi = 3.14159265358979f;
+    const float p = (float)pos;
+    if (pos < (1 << 24) && fabsf(p * f) < 4194304.0f) {
         constexpr float kHi = 0.15915493667125702f, kLo = 6.420638243e-09f;  // 1 / (2 pi)
-        const float p = (float)pos;
         const float g = f * kHi, gl = fmaf(f, kHi, -g) + f * kLo;
         const float t = p * g, e = fmaf(p, g, -t) + p * gl;
-        h = 2.0f * ((t - rintf(t)) + e);
+        const float a = t - rintf(t), s = a + e, b = s - a;
+        h = 2.0f * (s - rintf(s));
+        d = 2.0f * kPi * ((a - (s - b)) + (e - b));
     } else {
-        double t = (double)pos * (double)f * 0.15915494309189533577;
-        t = 2.0 * (t - rint(t));
-        h = (float)t;
-        d = (float)(t - (double)h) * 3.14159265358979f;
+        constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;  // 1 / (2 pi)
+        const double x = pos, y = f, z = x * y;
+        const double t = z * kHi, e = fma(z, kHi, -t) + (z * kLo + fma(x, y, -z) * kHi);
+        double r = (t - rint(t)) + e;
+        r = 2.0 * (r - rint(r));
+        h = (float)r;
+        d = (float)(r - (double)h) * kPi;
     }
     float s, c;
     sincospif(h, &s, &c);
