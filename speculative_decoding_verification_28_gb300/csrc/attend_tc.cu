@@ -371,9 +371,6 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                     continue;
                 }
                 guard_tile<T, Sh::kPanels>(ring_p + sg * Sh::kTile, tl, odd, g);
-                __threadfence_block();
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&s.v_ok[sg]);
                     mbar_arrive(&s.kv_empty[sg]);

@@ -85,14 +85,13 @@ __device__ __forceinline__ uint32_t elect_one()
     return one;
 }
 
-// D = A B (+ D): A and B in shared memory.  A_HI: A's upper word
-template <uint32_t A_HI = kOperandHi>
+// D = A B (+ D): A and B in shared memory
 __device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc)
 {
     asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-                 "mov.b64 x, {%1, %7};\n\tmov.b64 y, {%2, %6};\n\t"
+                 "mov.b64 x, {%1, %6};\n\tmov.b64 y, {%2, %6};\n\t"
                  "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
-                 "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(one), "n"(kOperandHi), "n"(A_HI)
+                 "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(one), "n"(kOperandHi)
                  : "memory");
 }
 // A in TMEM
@@ -105,7 +104,6 @@ __device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uin
                  : "memory");
 }
 
-#define SPEC_R4(x, i) x[i], x[i + 1], x[i + 2], x[i + 3]
 #define SPEC_OUT4(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3])
 #define SPEC_IN4(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3])
 
@@ -276,10 +274,10 @@ __device__ __forceinline__ void hide32(uint32_t *v, uint32_t seen)
 
 // instruction descriptor: fp32 accumulators, both operands T, M = 128
 template <typename T>
-__device__ __forceinline__ uint32_t tc_idesc(int n, bool b_rows_summed, bool a_rows_summed = false)
+__device__ __forceinline__ uint32_t tc_idesc(int n, bool b_rows_summed)
 {
-    return (1u << 4) | (TcType<T>::kFmt << 7) | (TcType<T>::kFmt << 10) | ((a_rows_summed ? 1u : 0u) << 15) |
-           ((b_rows_summed ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
+    return (1u << 4) | (TcType<T>::kFmt << 7) | (TcType<T>::kFmt << 10) | ((b_rows_summed ? 1u : 0u) << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
 struct TcMaps {
