@@ -13,6 +13,7 @@
 //
 // Roofline: HBM, 2 * (Hq + 2H) * D * sizeof(T) bytes per token.
 #include "forward.h"
+#include "packed.cuh"
 #include "spec_common.cuh"
 
 namespace spec {
@@ -167,49 +168,23 @@ __device__ __forceinline__ T *head_dst(const AppendArgs &a, const Token &t, int 
     return base + slab * row_len + t.kv_off + h * t.head_step;
 }
 
-// two fp32 operations in one instruction
-__device__ __forceinline__ uint64_t two(float lo, float hi)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 parts(uint64_t v)
-{
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-    return f;
-}
-__device__ __forceinline__ uint64_t two_mul(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t two_fma(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 // 8 bytes of storage as fp32 pairs (one for fp32, two for 16-bit types)
 template <typename T>
 struct Half8;
 template <>
 struct Half8<float> {
     static constexpr int kPairs = 1;
-    __device__ static void load(uint2 u, uint64_t *x) { x[0] = two(__uint_as_float(u.x), __uint_as_float(u.y)); }
+    __device__ static void load(uint2 u, uint64_t *x) { x[0] = pair(__uint_as_float(u.x), __uint_as_float(u.y)); }
     __device__ static uint2 store(const uint64_t *x)
     {
-        const float2 f = parts(x[0]);
+        const float2 f = unpair(x[0]);
         return make_uint2(__float_as_uint(f.x), __float_as_uint(f.y));
     }
 };
 template <>
 struct Half8<__nv_bfloat16> {
     static constexpr int kPairs = 2;
-    __device__ static uint64_t word(uint32_t w) { return two(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+    __device__ static uint64_t word(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
     __device__ static void load(uint2 u, uint64_t *x)
     {
         x[0] = word(u.x);
@@ -217,7 +192,7 @@ struct Half8<__nv_bfloat16> {
     }
     __device__ static uint32_t back(uint64_t x)
     {
-        const float2 f = parts(x);
+        const float2 f = unpair(x);
         uint32_t r;
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
         return r;
@@ -232,7 +207,7 @@ struct Half8<__half> {
         __half2 h;
         memcpy(&h, &w, 4);
         const float2 f = __half22float2(h);
-        return two(f.x, f.y);
+        return pair(f.x, f.y);
     }
     __device__ static void load(uint2 u, uint64_t *x)
     {
@@ -241,7 +216,7 @@ struct Half8<__half> {
     }
     __device__ static uint32_t back(uint64_t x)
     {
-        const float2 f = parts(x);
+        const float2 f = unpair(x);
         uint32_t r;
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(f.y), "f"(f.x));
         return r;
@@ -280,20 +255,20 @@ __device__ __forceinline__ void turns(const AppendArgs &a, int pos, int ln, uint
         const int f0 = a.interleaved ? NP * ln + i : 2 * NP * ln + 2 * i;
         const int f1 = a.interleaved ? D / 4 + NP * ln + i : f0 + 1;
         const float2 t0 = turn(pos, a.inv_freq[f0]), t1 = turn(pos, a.inv_freq[f1]);
-        cs[i] = two(t0.x, t1.x);
-        sn[i] = two(t0.y, t1.y);
-        ns[i] = two(-t0.y, -t1.y);
+        cs[i] = pair(t0.x, t1.x);
+        sn[i] = pair(t0.y, t1.y);
+        ns[i] = pair(-t0.y, -t1.y);
     }
 }
 // sum of the squares of a head, in each of its LPH lanes
 template <int NP, int LPH>
 __device__ __forceinline__ float square_sum(const uint64_t *x)
 {
-    uint64_t sq = two_mul(x[0], x[0]);
+    uint64_t sq = mul2(x[0], x[0]);
 #pragma unroll
     for (int i = 1; i < 2 * NP; ++i)
-        sq = two_fma(x[i], x[i], sq);
-    const float2 q2 = parts(sq);
+        sq = fma2(x[i], x[i], sq);
+    const float2 q2 = unpair(sq);
     float sum = q2.x + q2.y;
 #pragma unroll
     for (int k = LPH / 2; k > 0; k >>= 1)
@@ -305,7 +280,7 @@ __device__ __forceinline__ void scale(float inv, uint64_t *x, const uint64_t *g)
 {
 #pragma unroll
     for (int i = 0; i < 2 * NP; ++i)
-        x[i] = two_mul(two_mul(x[i], two(inv, inv)), g[i]);
+        x[i] = mul2(mul2(x[i], pair(inv, inv)), g[i]);
 }
 template <int NP, int LPH, int D>
 __device__ __forceinline__ void norm(float eps, uint64_t *x, const uint64_t *g)
@@ -320,12 +295,12 @@ __device__ __forceinline__ void rotate(int interleaved, uint64_t *x, const uint6
     for (int i = 0; i < NP; ++i) {
         if (!interleaved) {
             const uint64_t l = x[i], h = x[NP + i];
-            x[i] = two_fma(l, cs[i], two_mul(h, ns[i]));
-            x[NP + i] = two_fma(h, cs[i], two_mul(l, sn[i]));
+            x[i] = fma2(l, cs[i], mul2(h, ns[i]));
+            x[NP + i] = fma2(h, cs[i], mul2(l, sn[i]));
         } else {
-            const float2 c = parts(cs[i]), s = parts(sn[i]), l = parts(x[i]), h = parts(x[NP + i]);
-            x[i] = two(l.x * c.x - l.y * s.x, l.y * c.x + l.x * s.x);
-            x[NP + i] = two(h.x * c.y - h.y * s.y, h.y * c.y + h.x * s.y);
+            const float2 c = unpair(cs[i]), s = unpair(sn[i]), l = unpair(x[i]), h = unpair(x[NP + i]);
+            x[i] = pair(l.x * c.x - l.y * s.x, l.y * c.x + l.x * s.x);
+            x[NP + i] = pair(h.x * c.y - h.y * s.y, h.y * c.y + h.x * s.y);
         }
     }
 }
