@@ -1,5 +1,5 @@
 // attend_common.cuh -- how attention's work is split over CTAs and joined
-// again, shared by its two kernels (attend_simt.cu, attend_tc.cu).
+// again, shared by its three kernels (attend_simt.cu, attend_few.cu, attend_tc.cu).
 //
 // A unit is (sequence, key head, group of query rows); its keys are cut into
 // tiles.  The query rows of a key head are packed token-major: row r is token

@@ -9,10 +9,11 @@
 // two CTAs share an SM, each with one buffer of everything (TMEM: 128 columns
 // of scores and weights, 128 of O; a ring of two or three tiles), and one's
 // chain runs while the other's keys arrive.  Measured: 256 chains of 9 tokens,
-// 32 / 8 heads of 128 over 2.3 GB of keys, 383 us (5.9 TB/s, 0.88 of a copy);
-// 64 of them 129 us (4.5 TB/s); decoding at batch 32 over 109 MB 40 us with a
+// 32 / 8 heads of 128 over 2.3 GB of keys, 378 us (6.0 TB/s, 0.89 of a copy);
+// 64 of them 129 us (4.5 TB/s); decoding at batch 32 over 109 MB 41 us with a
 // cold cache, of which 6 pass before the first tile is there and 4 in joins;
-// 8 prompts of 158 tokens on average 22 us, all of it latency.
+// 8 prompts of 158 tokens on average 22 us, all of it latency.  The weights are
+// rounded to the storage type as in attend_tc.cu.
 #include "tcgen.cuh"
 
 namespace spec {

@@ -11,11 +11,14 @@
 // the output of the same rows and columns 4 tx + 64 j, so that a row's maximum,
 // sum and rescaling stay with the 16 lanes of its ty.  K and then V take the
 // same shared buffer as fp32, the next of them on its way in registers; the
-// weights pass through shared memory.  IR = 4 is bound by the FMA pipe (64
-// FMAs to 8 shared loads in the scores, 32 to 3 in the output); IR = 1, for up
-// to 16 rows, by shared memory and latency (4 rows, 32 sequences: 162 us, 365
-// with IR = 4; 16 rows, 16 sequences: 176, 391).  fp32 prompts run at 30 TFLOP/s,
-// trees of 64 nodes at 17; the smallest rounds take 9 us, all of it latency.
+// weights pass through shared memory.  IR = 4 has 64 FMAs to 8 shared loads in
+// the scores, 32 to 3 in the output; IR = 1, for up to 16 rows, is bound by shared
+// memory and latency (4 rows, 32 sequences: 162 us, 365 with IR = 4; 16 rows, 16
+// sequences: 176, 391).  fp32 prompts (2 of 2048 tokens, 32 / 8 heads of 128)
+// run at 29 TFLOP/s, 32 rounds of 64 nodes and 28 / 4 heads at 25: the FMA pipes
+// are 40% busy, shared memory 60%, issue slots 61%, and what is waited for are
+// shared loads, with 16 warps an SM (two CTAs of 128 registers a thread; spills
+// are 0.5% of the instructions).  The smallest rounds take 9 us, all latency.
 #include "attend_common.cuh"
 #include "verify_common.cuh"
 

@@ -7,7 +7,11 @@
 // with one pass over the keys.  A row's m is a running maximum that is only
 // moved when a tile's maximum is more than 2^8 above it: O and the sum are
 // then rescaled.  Between moves the weights exceed 1 by at most 2^8, which
-// fp32 sums and bf16 / fp16 weights hold without loss of precision.
+// costs neither fp32 sums nor 16-bit weights range or precision.  The weights
+// are rounded to the storage type, half a step each (bf16 2^-8, fp16 2^-11 of
+// their value), because one tcgen05 product takes both operands in one 16-bit
+// type: against 64 bits the results are 1.2 to 1.4 times as far off as with fp32
+// weights, where the result's own rounding remains.  Sums add the fp32 weights.
 //
 // A CTA holds NT tiles of 128 query rows of one key head (the G query heads
 // that share it, token-major) and streams its keys once:
@@ -28,9 +32,9 @@
 // of a large matrix product).  Slower were: all 128 scores held in registers
 // (776 us at the time, against 760), weights handed over by halves (829, 813),
 // products of transposed operands and two chains to a CTA for few rows (159 and
-// 145 us for chains, against 127).  A round of 32 trees of 64 nodes, 28 / 4
-// heads, takes 115 us: units of some 20 tiles, whose start, end and join do not
-// overlap.
+// 145 us for chains, against 127).  A round of 32 times 64 nodes, 28 / 4 heads,
+// over 500 to 4000 keys takes 109 us: units of some 20 tiles, whose start, end
+// and join do not overlap.
 #include "tcgen.cuh"
 
 namespace spec {

@@ -158,8 +158,9 @@ __device__ uint64_t row_key(const T *row, int lo, int hi, uint64_t *s_red)
 // the next node.  So only the rows of the path are read (V * sizeof(T) bytes
 // each, HBM), and a step costs a load, a reduction and the barrier: with few
 // sequences that latency times the longest path is the call's time: 64 trees of
-// 26 nodes with V = 151936 in bf16 take 16.5 us (54 MB of rows, 8 us of HBM), 4
-// of 13 nodes with V = 32000 in fp32 take 8.2.
+// 26 nodes with V = 151936 in bf16 take 22 us (54 MB of rows, 8 us of a copy; 17
+// when the rows are still in L2), 34 with paths of five nodes each (97 MB); 4 of
+// 13 nodes with V = 32000 in fp32 take 8.4.
 // Two candidate slots in turn are enough: a CTA writes a slot again only
 // after the barrier of the step between, which every CTA reaches after
 // reading it.
