@@ -18,7 +18,8 @@
  *
  * Conventions for every entry point
  *   - Pointers are DEVICE pointers owned by the caller unless stated; the
- *     library allocates nothing and keeps no state between calls.
+ *     library allocates nothing and keeps no state between calls (but for
+ *     spec_attend_starve_next, which only tests need).
  *   - Every call is asynchronous on `cuda_stream` (a cudaStream_t, NULL =
  *     the legacy default stream) and returns once its kernels are enqueued.
  *   - Return value: SPEC_OK, or a negative SPEC_E* code for an argument error
