@@ -272,10 +272,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     mx *= c;
                     if (tile == u.tile) {
                         m = mx;
-                    } else if (__any_sync(0xFFFFFFFFu, mx > m + kLazy)) {
+                    } else if (__any_sync(0xFFFFFFFFu, mx > m + TcType<T>::kLazy)) {
                         // O is at rest: these scores came after its last product
                         float f = 1.0f;
-                        if (mx > m + kLazy) {
+                        if (mx > m + TcType<T>::kLazy) {
                             f = exp2_sfu(m - mx);  // 0 when nothing was seen before
                             m = mx;
                         }
@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                         }
                     }
                     const float m0 = m == -INFINITY ? 0.0f : m;
-                    const uint64_t m2 = pair(-m0, -m0);
+                    const uint64_t m2 = pair(TcType<T>::kShift - m0, TcType<T>::kShift - m0);
                     uint64_t sum[2] = {0, 0};
                     // weights of chunk k, in the upper half of the scores'
                     // columns: from the top down they replace scores that

@@ -5,13 +5,14 @@
 //   O += P V in TMEM, fp32
 //
 // with one pass over the keys.  A row's m is a running maximum that is only
-// moved when a tile's maximum is more than 2^8 above it: O and the sum are
-// then rescaled.  Between moves the weights exceed 1 by at most 2^8, which
-// costs neither fp32 sums nor 16-bit weights range or precision.  The weights
-// are rounded to the storage type, half a step each (bf16 2^-8, fp16 2^-11 of
-// their value), because one tcgen05 product takes both operands in one 16-bit
-// type: against 64 bits the results are 1.2 to 1.4 times as far off as with fp32
-// weights, where the result's own rounding remains.  Sums add the fp32 weights.
+// moved when a tile's maximum is more than 2^kLazy above it: O and the sum are
+// then rescaled.  Between moves the weights exceed 2^kShift by at most 2^kLazy
+// (TcType), which costs neither fp32 sums nor 16-bit weights range or precision.
+// The weights are rounded to the storage type, by up to half a step (bf16 2^-8,
+// fp16 2^-11 of their value), because one tcgen05 product takes both operands in
+// one 16-bit type: against 64 bits the results are 1.2 to 1.4 times as far off as
+// with fp32 weights, where the result's own rounding remains.  Sums add the fp32
+// weights.
 //
 // A CTA holds NT tiles of 128 query rows of one key head (the G query heads
 // that share it, token-major) and streams its keys once:
@@ -461,8 +462,8 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                     float f = 1.0f;
                     if (tile == u.tile) {
                         m = mx;
-                    } else if (__any_sync(0xFFFFFFFFu, mx > m + kLazy)) {
-                        if (mx > m + kLazy) {
+                    } else if (__any_sync(0xFFFFFFFFu, mx > m + TcType<T>::kLazy)) {
+                        if (mx > m + TcType<T>::kLazy) {
                             f = exp2_sfu(m - mx);  // 0 when nothing was seen before
                             m = mx;
                         }
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(TcShape<D, NT>::kThreads, 1)
                         }
                     }
                     const float m0 = m == -INFINITY ? 0.0f : m;
-                    const uint64_t c2 = pair(c, c), m2 = pair(-m0, -m0);
+                    const uint64_t c2 = pair(c, c), m2 = pair(TcType<T>::kShift - m0, TcType<T>::kShift - m0);
                     uint64_t sum[2] = {0, 0};
                     auto weigh32 = [&](const uint32_t *v, int k) {
                         uint32_t pk[16];

@@ -15,7 +15,6 @@ namespace spec {
 
 constexpr int kKeys = 128;  // keys of a tile
 constexpr int kTcWaitLimit = 2000;  // probes of up to ~1 ms, after a wait that gave up
-constexpr float kLazy = 8.0f;       // base-2 headroom of the running maximum
 constexpr int kGuardRing = 8;       // units whose guard words may be live at once
 
 // ---------------------------------------------------------------------------
@@ -175,11 +174,18 @@ __device__ __forceinline__ float max32(const uint32_t *r)
     return fmaxf(m[0], m[1]);
 }
 
+// kShift: weights are 2^kShift times as large as the softmax's; kLazy: base-2
+// headroom of the running maximum.  An fp16 weight of less than 2^-14 has steps
+// of 2^-24: unshifted, weights under 2^-25 of a row's largest would all be 0, and
+// thousands of them may be most of its result.  At 2^11 they keep their 11 bits
+// down to 2^-25 and vanish under 2^-36, and 2^(11 + 4) is within fp16's range.
+// bf16 has fp32's range.
 template <typename T>
 struct TcType;
 template <>
 struct TcType<__nv_bfloat16> {
     static constexpr uint32_t kFmt = 1;
+    static constexpr float kShift = 0.0f, kLazy = 8.0f;
     __device__ static uint32_t pack(float lo, float hi)
     {
         uint32_t r;
@@ -194,6 +200,7 @@ struct TcType<__nv_bfloat16> {
 template <>
 struct TcType<__half> {
     static constexpr uint32_t kFmt = 0;
+    static constexpr float kShift = 11.0f, kLazy = 4.0f;
     __device__ static uint32_t pack(float lo, float hi)
     {
         uint32_t r;
