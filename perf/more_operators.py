@@ -1,0 +1,528 @@
+"""A paged cache in 4 bits around a speculative round, as measured cases.
+
+The pool [L, 2, P, H, page * 17 * D / 32] holds blocks of `page` tokens of one
+head: `page` rows of D / 2 bytes of codes (dimension 2 j in the low half of
+byte j), then `page` rows of D / 32 bytes of scales.  A group of 32 values x has
+the scale s = max |x| / 7, rounded to even to five exponent and three mantissa
+bits (byte b stands for the half whose bits are b << 7; 1 .. 223, and 255 = NaN
+where a value is not finite) and codes min(max(rint(x / s), -7), 7) + 8.  Row r of
+table [N, MP] names the pages of a sequence, held [N] says how many it has (-1
+behind them) and refs [P] how often each page is named.
+
+  attend  attention of a round's nodes over the paged prefix and the staged
+          16-bit keys and values of the nodes that they descend from
+  keep    rows of a 16-bit block (an accepted path, or a run of a prompt's
+          slots) stored into pages, and the same positions loaded back as the
+          values that they stand for
+  branch  sequences forked into several that share their pages, room reserved
+          for the next round (shared pages that will be written get a copy of
+          their own), those copies made
+  turn    half of the sequences end and free their pages, the live ones are
+          moved to the front of the pool, new sequences take their places
+
+`own` false: each is computed by elementary torch operations in 32 bits, with
+one rounding at the end.  `own` true: the library's calls.  exact() is the
+definition in 64 bits.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+DTYPES = {"bf16": torch.bfloat16, "f16": torch.float16}
+GROUP = 32
+TOP = 223  # largest scale's byte: 7680
+
+
+def listed():
+    return [
+        # the smallest round: one sequence, one token, a small head
+        dict(name="token_tiny_f16", op="attend", dtype="f16", B=1, T=1, Hq=4, H=4, D=64, page=16, lo=33, hi=33, tree=0),
+        # a chain of four proposals, ragged, between batches of decoding
+        dict(name="chain_small", op="attend", dtype="bf16", B=4, T=5, Hq=16, H=4, D=64, page=32, lo=17, hi=301, tree=0),
+        # a single token per sequence: plain decoding
+        dict(name="token_b32", op="attend", dtype="f16", B=32, T=1, Hq=32, H=8, D=128, page=64, lo=128, hi=1536, tree=0),
+        # decoding over long documents, eight query heads to a key head
+        dict(name="token_long", op="attend", dtype="bf16", B=6, T=1, Hq=64, H=8, D=128, page=128, lo=20000, hi=120001,
+             tree=0),
+        # the largest batch: eight proposals each, long ragged contexts
+        dict(name="chain_b256", op="attend", dtype="bf16", B=256, T=9, Hq=32, H=8, D=128, page=64, lo=256, hi=4000,
+             tree=0),
+        # wide trees of up to 64 nodes over long contexts, seven query heads to a key head
+        dict(name="tree_g7", op="attend", dtype="bf16", B=32, T=64, Hq=28, H=4, D=128, page=64, lo=500, hi=4000, tree=1),
+        # the accepted rows of a small draft model
+        dict(name="keep_draft", op="keep", dtype="f16", L=2, B=8, T=26, H=12, D=64, page=16, lo=64, hi=512, path=1),
+        # the accepted rows of every layer of a target
+        dict(name="keep_path", op="keep", dtype="bf16", L=28, B=64, T=26, H=4, D=128, page=64, lo=64, hi=200, path=1),
+        # a piece of each of a batch of prompts, one layer
+        dict(name="keep_prompt", op="keep", dtype="bf16", L=1, B=32, T=2048, H=8, D=128, page=64, lo=100, hi=1999, path=0),
+        # two samples of a short prompt on a draft model's pages
+        dict(name="branch_small", op="branch", L=2, B=2, K=2, H=4, D=64, page=16, lo=20, hi=90, room=5, spare=20),
+        # eight samples of each of 32 prompts
+        dict(name="branch_k8", op="branch", L=16, B=32, K=8, H=4, D=128, page=64, lo=500, hi=4000, room=9, spare=500),
+        # half of a batch is replaced, and the pool kept dense
+        dict(name="turn_b128", op="turn", L=4, B=128, H=4, D=128, page=64, lo=200, hi=4000, spare=200),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["attend", "attend", "attend", "keep", "keep", "branch", "turn"])
+    H = rng.choice([1, 2, 4, 8])
+    D = rng.choice([64, 128, 128])
+    page = rng.choice([16, 32, 64, 128, 256])
+    if op == "attend":
+        B = _log(rng, 1, 96)
+        top = _log(rng, 40, max(200, min(60000, 200000 // B)))
+        return dict(op=op, dtype=rng.choice(["bf16", "f16"]), B=B, T=rng.choice([1, _log(rng, 2, 16), _log(rng, 10, 64)]),
+                    Hq=H * rng.choice([1, 2, 4, 5, 7, 8]), H=H, D=D, page=page, lo=max(1, top // 4), hi=top,
+                    tree=rng.randint(0, 1))
+    if op == "keep":
+        path = rng.randint(0, 1)
+        top = _log(rng, 16, 2000)
+        return dict(op=op, dtype=rng.choice(["bf16", "f16"]), L=rng.randint(1, 16 if path else 2), B=_log(rng, 1, 32),
+                    T=rng.randint(2, 64) if path else top + rng.randint(0, 40), H=H, D=D, page=page, lo=max(1, top // 5),
+                    hi=top, path=path)
+    top = _log(rng, 20, 3000)
+    c = dict(op=op, L=rng.randint(1, 6), B=_log(rng, 2, 48), H=H, D=D, page=page, lo=max(1, top // 5), hi=top,
+             spare=rng.randint(1, 100))
+    return dict(c, K=rng.randint(2, 8), room=rng.randint(1, 64)) if op == "branch" else c
+
+
+# ---------------------------------------------------------------------------
+# inputs
+# ---------------------------------------------------------------------------
+def _block(page, D):
+    return page * 17 * D // 32
+
+
+def _lengths(r, lo, hi, B):
+    """B lengths spread over [lo, hi] whose sum is the range's mean times B, so that a case has one amount of work."""
+    n = r.randint(lo, hi + 1, B)
+    off = B * (lo + hi) // 2 - int(n.sum())
+    for b in r.permutation(B):
+        to = min(hi, max(lo, int(n[b]) + off))
+        off -= to - int(n[b])
+        n[b] = to
+    return n.astype(np.int32)
+
+
+def _tree(r, B, T, tree):
+    """parents, node counts, visible sets and depths of B rounds of T nodes"""
+    i = np.arange(T)
+    if tree:
+        lo, hi = np.maximum(i - 1, 0) // 4, np.maximum(i - 1, 0) // 2
+        parent = lo + (r.rand(B, T) * (hi - lo + 1)).astype(np.int64)
+        n = r.randint((T + 1) // 2, T + 1, B)
+    else:
+        parent, n = np.broadcast_to(i - 1, (B, T)).copy(), np.full(B, T)
+    seen = np.zeros((B, T), np.uint64)
+    b = np.arange(B)
+    for k in range(T):
+        seen[:, k] = np.uint64(1) << np.uint64(k)
+        if k:
+            seen[:, k] |= seen[b, parent[:, k]]
+    return parent, n.astype(np.int32), seen.view(np.int64)
+
+
+def _tables(r, pages, MP, P):
+    """table, held and refs of sequences with pages[b] pages, spread over a pool of P in no order"""
+    free = r.permutation(P)[:int(pages.sum())]
+    table = np.full((len(pages), MP), -1, np.int32)
+    table[np.arange(MP) < pages[:, None]] = free
+    refs = np.zeros(P, np.int32)
+    refs[free] = 1
+    return table, pages.astype(np.int32), refs
+
+
+def _fill(g, L, P, H, page, D):
+    """a pool of normally distributed keys and values"""
+    pool = torch.empty((L, 2, P, H, _block(page, D)), dtype=torch.uint8, device="cuda")
+    rows = pool.view(L * 2 * P * H, -1)
+    step = max(1, (1 << 27) // (page * D))
+    for i in range(0, rows.shape[0], step):
+        n = min(step, rows.shape[0] - i)
+        codes, scales = _pack(torch.randn((n, page, D), generator=g, device="cuda", dtype=torch.bfloat16))
+        rows[i:i + n] = torch.cat([codes.flatten(1), scales.flatten(1)], 1)
+    return pool
+
+
+def prepare(case, seed):
+    r = np.random.RandomState(seed % (1 << 31))
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    op, B, H, D, page = (case[k] for k in ("op", "B", "H", "D", "page"))
+    put = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    randn = lambda shape: torch.randn(shape, generator=g, device="cuda", dtype=DTYPES[case["dtype"]])  # noqa: E731
+    n = _lengths(r, case["lo"], case["hi"], B)
+    s = {"case": case}
+    h = {}
+    if op == "attend":
+        T = case["T"]
+        h["length"] = n
+        pages = -(-(n - 1) // page)
+        table, held, refs = _tables(r, pages, -(-case["hi"] // page), int(pages.sum()) + 3)
+        _, h["n"], h["seen"] = _tree(r, B, T, case["tree"])
+        h["table"] = table
+        s["pool"] = _fill(g, 1, len(refs), H, page, D)
+        s["q"] = randn((B, T, case["Hq"], D))
+        s["staged"] = randn((1, 2, B, H, T, D))
+    elif op == "keep":
+        T = case["T"]
+        if case["path"]:  # the path that a verification accepted, behind n - 1 tokens in the cache
+            parent, nodes, _ = _tree(r, B, T, 1)
+            path = np.full((B, T), -1, np.int32)
+            count = np.zeros(B, np.int32)
+            for b in range(B):
+                at, k = 0, 0
+                while True:
+                    path[b, k] = at
+                    k += 1
+                    kids = [c for c in range(at + 1, nodes[b]) if parent[b, c] == at]
+                    if not kids or r.rand() > 0.7:
+                        break
+                    at = int(r.choice(kids))
+                count[b] = k
+            h.update(path=path, count=count, pos=n - 1, slot=np.zeros(B, np.int32))
+            S = T
+        else:  # the slots of a left-padded batch that hold a prompt's next tokens
+            S = case["hi"] + 5
+            h.update(count=n, pos=r.randint(0, 3 * page, B).astype(np.int32), slot=(S - n - r.randint(0, 5, B)).astype(np.int32))
+        pages = -(-(h["pos"] + h["count"]) // page)
+        table, held, refs = _tables(r, pages, int(pages.max()), int(pages.sum()) + 3)
+        h["table"] = table
+        s["pool"] = torch.zeros((case["L"], 2, len(refs), H, _block(page, D)), dtype=torch.uint8, device="cuda")
+        s["kv"] = randn((case["L"], 2, B, H, S, D))
+        s["back"] = torch.zeros((case["L"], 2, B, H, T, D), dtype=DTYPES[case["dtype"]], device="cuda")
+    else:
+        L, K = case["L"], case.get("K", 1)
+        N = B * K
+        if op == "branch":
+            # the first row of K holds a prompt; the others hold what a round before this one left them
+            pages = np.repeat(-(-n // page), K)
+            most, P = -(-(case["hi"] + case["room"]) // page), K * int(n.sum()) // page + N * (2 + -(-case["room"] // page))
+            h.update(src=np.arange(N, dtype=np.int32) // K * K, first=np.repeat(n, K), total=np.repeat(n, K) + case["room"])
+        else:
+            pages = -(-n // page)
+            half = (r.permutation(B) < B // 2).astype(np.int32)
+            h.update(ends=half, lengths=n)
+            most, P = -(-case["hi"] // page), int(n.sum()) // page + B
+        h["table"], h["held"], h["refs"] = _tables(r, pages, most, P + case["spare"])
+        s["pool"] = torch.randint(0, 256, (L, 2, P + case["spare"], H, _block(page, D)), generator=g, device="cuda",
+                                  dtype=torch.uint8)
+        if op == "turn":
+            whole = lambda keep: put(np.where(keep, n, 0).astype(np.int32))  # noqa: E731
+            s["stay"] = [whole(half == 0), whole(half == 1)]
+            s["at"] = 0
+    for k, v in h.items():
+        s[k] = put(v)
+    s["host"] = h
+    return s
+
+
+# ---------------------------------------------------------------------------
+# the plain forms
+# ---------------------------------------------------------------------------
+def _pack(x):
+    """x [..., D] -> codes [..., D / 2] and scales [..., D / 32], bytes"""
+    x = x.float().unflatten(-1, (-1, GROUP))
+    f = (x.abs().amax(-1).double() / 7).float()  # next to a border 32 bits say which side only if rounded once
+    odd = ~torch.isfinite(f)
+    f = torch.where(odd, 1.0, f)
+    bits = f.view(torch.int32)
+    bits = (bits + 0x7FFFF + (bits >> 20 & 1) >> 20) - (112 << 3)
+    byte = torch.where(f < 2.0 ** -14, torch.round(f * 2.0 ** 17).int(), bits).clamp(1, TOP)
+    code = torch.round(x / _scale(byte)[..., None]).clamp(-7, 7)
+    code = torch.where(odd[..., None], 0.0, code).int() + 8
+    code = code.flatten(-2).unflatten(-1, (-1, 2))
+    return (code[..., 0] | code[..., 1] << 4).to(torch.uint8), torch.where(odd, 255, byte).to(torch.uint8)
+
+
+def _scale(byte):
+    """what scale bytes stand for"""
+    return (byte.int() << 7).to(torch.int16).view(torch.float16).float()
+
+
+def _unpack(codes, scales, wide=torch.float32):
+    code = torch.stack([codes & 15, codes >> 4], -1).flatten(-2).to(wide) - 8
+    return (code.unflatten(-1, (-1, GROUP)) * _scale(scales)[..., None].to(wide)).flatten(-2)
+
+
+def _rows_of(pool, page, D):
+    """codes [..., page, D / 2] and scales [..., page, D / 32] of a pool, as views"""
+    return (pool[..., :page * D // 2].unflatten(-1, (page, D // 2)),
+            pool[..., page * D // 2:].unflatten(-1, (page, D // 32)))
+
+
+def _softmax_times(score, sees, v):
+    """softmax over the seen places times v; a row that sees nothing gives zeros."""
+    score = score.masked_fill_(~sees, -math.inf)
+    top = score.amax(-1, keepdim=True)
+    e = torch.exp(score - torch.where(top == -math.inf, 0.0, top))
+    return (e @ v) / e.sum(-1, keepdim=True).clamp(min=1e-30)
+
+
+def _plain_attend(s):
+    c = s["case"]
+    B, T, Hq, H, D, page = (c[k] for k in ("B", "T", "Hq", "H", "D", "page"))
+    G = Hq // H
+    dev = s["q"].device
+    width = int(s["host"]["length"].max()) - 1
+    codes, scales = _rows_of(s["pool"][0], page, D)
+    pages = s["table"][:, :-(-width // page)].long().clamp(min=0).T
+
+    def prefix(kv):  # keys or values [B, H, width + T, D]
+        x = _unpack(codes[kv][pages], scales[kv][pages])  # [pages, B, H, page, D]
+        return torch.cat([x.permute(1, 2, 0, 3, 4).flatten(2, 3)[:, :, :width], s["staged"][0, kv].float()], 2)
+
+    node = torch.arange(T, device=dev)
+    new = (s["seen"][:, :, None] >> node & 1).bool() & (node < s["n"][:, None])[:, None, :]  # [B, T, T]
+    old = (torch.arange(width, device=dev) < s["length"][:, None] - 1)[:, None, None]
+    sees = torch.cat([old.expand(B, 1, T, width), new[:, None]], 3).repeat_interleave(G, 2)
+    q = s["q"].float().view(B, T, H, G, D).permute(0, 2, 1, 3, 4).reshape(B, H, T * G, D)
+    out = _softmax_times((q @ prefix(0).transpose(2, 3)) * (1.0 / math.sqrt(D)), sees, prefix(1))
+    out = out.view(B, H, T, G, D).permute(0, 2, 1, 3, 4).reshape(B, T, Hq, D)
+    real = (node < s["n"][:, None])[:, :, None, None]
+    return torch.where(real, out, 0.0).to(s["q"].dtype)
+
+
+def _places(s):
+    """Of the tokens that a keep case stores: sequence, place among its tokens, source row, page and row in it."""
+    c = s["case"]
+    k = torch.arange(c["T"], device=s["kv"].device)
+    b, k = (k < s["count"][:, None]).nonzero(as_tuple=True)
+    pos = s["pos"][b] + k
+    row = s["path"][b, k] if c["path"] else s["slot"][b] + k
+    return b, k, row.long(), s["table"][b, pos // c["page"]].long(), pos % c["page"]
+
+
+def _plain_keep(s):
+    b, k, row, at, r = _places(s)
+    page, D = s["case"]["page"], s["case"]["D"]
+    codes, scales = _rows_of(s["pool"], page, D)
+    # [tokens, L, 2, H, ..]: indices of tokens on both sides of the head's axis
+    x, y = _pack(s["kv"][:, :, b, :, row])
+    codes[:, :, at, :, r], scales[:, :, at, :, r] = x, y
+    s["back"][:, :, b, :, k] = _unpack(codes[:, :, at, :, r], scales[:, :, at, :, r]).to(s["back"].dtype)
+    return s["back"]
+
+
+def _pages_of(tokens, page):
+    return (tokens + page - 1) // page
+
+
+def _named(refs, pages, mask, by):
+    """adds `by` to refs for the pages under mask"""
+    refs.index_add_(0, pages.clamp(min=0).flatten(), by * mask.flatten().to(refs.dtype))
+
+
+def _plain_fork(s, src, length):
+    """row b becomes a fork of row src[b], with its pages for length[b] tokens"""
+    table, held, refs, page = s["table"], s["held"], s["refs"], s["case"]["page"]
+    col = torch.arange(table.shape[1], device=table.device)
+    n = _pages_of(length, page)
+    keep = col < n[:, None]
+    new = torch.where(keep, table[src.long()], -1)
+    _named(refs, table, col < held[:, None], -1)
+    _named(refs, new, keep, 1)
+    table.copy_(new)
+    held.copy_(n)
+
+
+def _plain_reserve(s, first, total):
+    """room for total[b] tokens in row b, of which those from first[b] on will be written; -> the copies to make"""
+    table, held, refs, page = s["table"], s["held"], s["refs"], s["case"]["page"]
+    N, MP = table.shape
+    dev = table.device
+    col = torch.arange(MP, device=dev)
+    n = _pages_of(total, page)[:, None]
+    has = col < held[:, None]
+    gone = has & (col >= n)
+    _named(refs, table, gone, -1)
+    # of the sequences that will write a shared page all get another, but the last where no other names it
+    write = has & (col >= (first // page)[:, None]) & (col < n) & (first < total)[:, None]
+    key = torch.where(write, table, len(refs) + torch.arange(N * MP, device=dev).view(N, MP)).flatten()
+    order = torch.sort(key, stable=True)
+    rank = torch.empty_like(key)
+    rank[order.indices] = torch.arange(N * MP, device=dev) - torch.searchsorted(order.values, order.values)
+    many = refs[table.clamp(min=0).long()]
+    swap = write & (many > 1) & (rank.view(N, MP) < many - 1)
+    fresh = swap | (~has & (col < n))
+    free = torch.sort((refs > 0).to(torch.uint8), stable=True).indices.int()
+    order = (fresh.flatten().cumsum(0) - 1).clamp(min=0, max=len(refs) - 1)
+    got = free[order].view(N, MP)
+    part = swap & (col == (first // page)[:, None]) & (first % page != 0)[:, None]
+    pairs = torch.stack([torch.where(part, table, -1).amax(1), torch.where(part, got, -1).amax(1)], 1)
+    _named(refs, table, swap, -1)
+    _named(refs, got, fresh, 1)
+    table.copy_(torch.where(fresh, got, torch.where(gone, -1, table)))
+    held.copy_(n[:, 0])
+    return pairs
+
+
+def _plain_compact(s):
+    """live pages to the lowest numbers, in order; -> the copies to make"""
+    refs, table = s["refs"], s["table"]
+    live = refs > 0
+    at = torch.arange(len(refs), device=refs.device)
+    n = live.sum()
+    to, frm = (~live & (at < n)).nonzero()[:, 0], (live & (at >= n)).nonzero()[:, 0]
+    new = at.int()
+    new[frm] = to.int()
+    refs[to] = refs[frm]
+    refs[frm] = 0
+    table.copy_(torch.where(table < 0, -1, new[table.clamp(min=0).long()]))
+    return torch.stack([frm, to], 1)
+
+
+def _plain_copy(pool, pairs):
+    pairs = pairs[pairs[:, 0] >= 0].long()
+    pool[:, :, pairs[:, 1]] = pool[:, :, pairs[:, 0]]
+
+
+# ---------------------------------------------------------------------------
+# one pass
+# ---------------------------------------------------------------------------
+def run(s):
+    return _own(s) if own else _plain(s)
+
+
+def _book(s):
+    # the pool's bytes are what a copy of pages moves: nothing in it is computed
+    return {"table": s["table"], "held": s["held"], "refs": s["refs"], "pool": s["pool"].view(torch.int32)}
+
+
+def _plain(s):
+    op = s["case"]["op"]
+    if op == "attend":
+        return _plain_attend(s)
+    if op == "keep":
+        return _plain_keep(s)
+    if op == "branch":
+        _plain_fork(s, s["src"], s["first"])
+        _plain_copy(s["pool"], _plain_reserve(s, s["first"], s["total"]))
+        return _book(s)
+    stay = s["stay"][s["at"]]
+    s["at"] ^= 1
+    _plain_reserve(s, stay, stay)
+    _plain_copy(s["pool"], _plain_compact(s))
+    _plain_reserve(s, stay, s["lengths"])
+    return _book(s)
+
+
+def _own(s):
+    import speculative_decoding_verification_28_gb300 as sv
+
+    c = s["case"]
+    op, page = c["op"], c["page"]
+    if op == "attend":
+        if "out" not in s:
+            s["out"] = torch.empty_like(s["q"])
+        if c["tree"]:  # nodes behind a ragged tree's last are not written
+            s["out"].zero_()
+        tree = dict(tree_mask=s["seen"], n_nodes=s["n"]) if c["tree"] else {}
+        return sv.spec_attend_round_q4(s["q"], s["pool"], 0, s["table"], s["length"], s["staged"], out=s["out"], **tree)[0]
+    if op == "keep":
+        path = dict(path=s["path"]) if c["path"] else dict(slot=s["slot"])
+        sv.spec_store_q4(s["kv"], s["pool"], s["table"], s["pos"], s["count"], **path)
+        sv.spec_load_q4(s["pool"], s["back"], s["table"], s["pos"], s["count"])
+        return s["back"]
+    book = s["table"], s["held"], s["refs"]
+    if op == "branch":
+        sv.spec_page_fork(*book, s["src"], page, length=s["first"])
+        sv.spec_page_copy(s["pool"], sv.spec_page_reserve(*book, s["first"], s["total"], page)[0])
+        return _book(s)
+    stay = s["stay"][s["at"]]
+    s["at"] ^= 1
+    sv.spec_page_reserve(*book, stay, stay, page)
+    sv.spec_page_copy(s["pool"], *sv.spec_page_compact(*book))
+    sv.spec_page_reserve(*book, stay, s["lengths"], page)
+    return _book(s)
+
+
+# ---------------------------------------------------------------------------
+# what a pass cannot do without
+# ---------------------------------------------------------------------------
+def work(case):
+    op, B, H, D, page = (case[k] for k in ("op", "B", "H", "D", "page"))
+    mean = (case["lo"] + case["hi"]) / 2
+    row = 17 * D / 32  # bytes of a token's keys, or values, of one head
+    if op == "attend":
+        T, Hq = case["T"], case["Hq"]
+        n = ((T + 1) // 2 + T) / 2 if case["tree"] else T
+        return {"bytes": B * (2 * H * (mean - 1) * row + 2 * D * n * (2 * H + 2 * Hq)),
+                "flops": 4.0 * B * n * Hq * D * (mean - 1 + n / 2)}
+    if op == "keep":
+        n = 2.2 if case["path"] else mean  # mean length of a path
+        rows = B * n * case["L"] * 2 * H
+        return {"bytes": rows * (4 * D + 2 * row), "flops": 8.0 * rows * D}
+    block = case["L"] * 2 * H * page * row
+    if op == "branch":  # a copy for all but one of the K that share a page that is part full
+        pairs = B * (case["K"] - 1) * (1 - 1 / page)
+    else:  # of the pages that half of the sequences leave, half lie among those that stay
+        pairs = B * (mean / page + 0.5) / 4
+    return {"bytes": 2 * pairs * block + 4.0 * B * case.get("K", 1) * mean / page, "flops": 0.0}
+
+
+# ---------------------------------------------------------------------------
+# the definitions in 64 bits
+# ---------------------------------------------------------------------------
+_HALF = torch.tensor([(b % 8) / 8.0 * 2.0 ** -14 if b < 8 else (1 + b % 8 / 8.0) * 2.0 ** (b // 8 - 15) for b in range(248)]
+                     + [math.nan] * 8, dtype=torch.float64)  # the scales by their bytes
+
+
+def _values(blocks, page, D):
+    """[tokens, D] of the blocks of a sequence"""
+    half = page * D // 2
+    code = torch.stack([blocks[:, :half] % 16, blocks[:, :half] // 16], 2).reshape(-1, D).double() - 8.0
+    return code * _HALF.to(blocks.device)[blocks[:, half:].long()].reshape(-1, D // 32).repeat_interleave(32, 1)
+
+
+def exact(case, seed):
+    if case["op"] in ("branch", "turn"):
+        return None  # whole numbers
+    s = prepare(case, seed)
+    h, B, H, D, page = s["host"], case["B"], case["H"], case["D"], case["page"]
+    f = torch.float64
+    if case["op"] == "keep":
+        out = torch.zeros(s["back"].shape, dtype=f, device="cuda")
+        mid = (_HALF[1:TOP] + _HALF[2:TOP + 1]).cuda() / 2  # between neighbouring scales
+        for b in range(B):
+            n = int(h["count"][b])
+            rows = h["path"][b, :n] if case["path"] else np.arange(n) + h["slot"][b]
+            x = s["kv"][:, :, b][:, :, :, torch.from_numpy(rows.astype(np.int64)).cuda()].to(f)
+            x = x.reshape(*x.shape[:-1], D // 32, 32)
+            want = x.abs().amax(-1) / 7.0
+            byte = 1 + (want[..., None] > mid).sum(-1)
+            tie = (want == mid[(byte - 1).clamp(max=len(mid) - 1)]) & (byte % 2 == 1)  # half way: to the even byte
+            scale = _HALF.cuda()[byte + tie.long()][..., None]
+            level = x / scale
+            down = torch.floor(level)
+            up = (level - down > 0.5) | ((level - down == 0.5) & (down % 2 != 0))
+            out[:, :, b, :, :n] = ((down + up).clamp(-7.0, 7.0) * scale).flatten(-2)
+        return out
+    T, Hq = case["T"], case["Hq"]
+    G = Hq // H
+    if B * H * float(h["length"].max()) * D > 2.5e9:
+        return None
+    out = torch.zeros(s["q"].shape, dtype=f, device="cuda")
+    seen = h["seen"].view(np.uint64)
+    for b in range(B):
+        n, past = int(h["n"][b]), int(h["length"][b]) - 1
+        bits = (seen[b, :n, None] >> np.arange(n, dtype=np.uint64)) & np.uint64(1)
+        see = torch.from_numpy(np.concatenate([np.ones((n, past)), bits.astype(float)], 1) > 0).cuda()
+        pages = s["table"][b, :-(-past // page)].long()
+        for head in range(H):
+            k, v = (torch.cat([_values(s["pool"][0, i, pages, head], page, D)[:past], s["staged"][0, i, b, head, :n].to(f)])
+                    for i in (0, 1))
+            q = s["q"][b, :n, head * G:(head + 1) * G].to(f)
+            w = torch.einsum("tgd,sd->tgs", q, k) / math.sqrt(D)
+            w = torch.softmax(w.masked_fill(~see[:, None], -math.inf), -1)
+            out[b, :n, head * G:(head + 1) * G] = torch.einsum("tgs,sd->tgd", w, v)
+    return out
+
