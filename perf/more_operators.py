@@ -426,11 +426,11 @@ def _own(s):
         if c["tree"]:  # nodes behind a ragged tree's last are not written
             s["out"].zero_()
         tree = dict(tree_mask=s["seen"], n_nodes=s["n"]) if c["tree"] else {}
-        return sv.spec_attend_round_q4(s["q"], s["pool"], 0, s["table"], s["length"], s["staged"], out=s["out"], **tree)[0]
+        return sv.spec_attend_pages(s["q"], s["pool"], 0, s["table"], s["length"], s["staged"], out=s["out"], **tree)[0]
     if op == "keep":
         path = dict(path=s["path"]) if c["path"] else dict(slot=s["slot"])
-        sv.spec_store_q4(s["kv"], s["pool"], s["table"], s["pos"], s["count"], **path)
-        sv.spec_load_q4(s["pool"], s["back"], s["table"], s["pos"], s["count"])
+        sv.spec_store_pages(s["kv"], s["pool"], s["table"], s["pos"], s["count"], **path)
+        sv.spec_load_pages(s["pool"], s["back"], s["table"], s["pos"], s["count"])
         return s["back"]
     book = s["table"], s["held"], s["refs"]
     if op == "branch":
