@@ -3,9 +3,9 @@
  * hot path of batch speculative decoding: per-round verification of k draft
  * tokens against k+1 target logit rows, and the ragged-to-rectangular
  * realignment of a contiguous left-padded KV cache, position IDs and
- * attention mask that variable acceptance forces; and for the forward pass
- * around a round (last part): appending to that cache, attention over it, and
- * drafted trees.
+ * attention mask that variable acceptance forces; for the forward pass around a
+ * round: appending to that cache, attention over it, and drafted trees; and (last
+ * part) a paged cache in 4 bits.
  *
  * Pages the operations are defined on (cited by title and section):
  *   "Correctness Forensics for Batch Speculative Decoding: Diagnosing the
@@ -551,6 +551,141 @@ SPEC_API int spec_verify_tree(const void *target_logits, spec_dtype dt, int B, i
 SPEC_API int spec_commit_tree(const void *staged, void *kv, spec_dtype dt, int L, int B, int T, int N, int H, int S,
                      int D, const int32_t *len, const int32_t *pad, const int32_t *path,
                      const int32_t *n_emit, const int32_t *idx, uint32_t *flags, void *cuda_stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * A paged cache in 4 bits: what a round reads of its prefix shrinks 3.8 times,
+ * nothing is ever moved to realign it, and sequences that come from one prompt
+ * share its pages.  The nodes of a round stay in 16 bits (`staged`) until their
+ * path is known; only what was accepted is stored.
+ *
+ * A pool [L, 2, P, H, block] bytes has P pages of `page` tokens (16, 32, 64, 128
+ * or 256).  A block, the keys or values of one head, is `page` rows of D / 2
+ * bytes of codes (dimension 2 j in the low half of byte j), then `page` rows of
+ * D / 32 bytes of scales: block = page * 17 * D / 32.  32 dimensions x share
+ *   s = max |x| / 7, rounded to even to five exponent and three mantissa bits,
+ * of which byte b stands for the half with bits b << 7: 1 .. 223 (2^-17 .. 7680)
+ * or, where a value of the 32 is not finite, 255 (NaN; all 32 load as NaN);
+ *   code = min(max(rint(x / s), -7), 7) + 8,  value = (code - 8) s.
+ * Quotients are exact at ties, so the bytes do not depend on the implementation;
+ * values have 7 significant bits, exact in both 16-bit types.  Magnitudes above
+ * 53760 saturate.  D is a multiple of 32 up to SPEC_MAX_HEAD_DIM; attention
+ * takes 64 and 128.
+ *
+ * The pages of sequences are in table [N, MP] int32: row r's token i is in page
+ * table[r, i / page].  held [N] says how many pages a row has, the entries
+ * behind are -1; refs [P] how many entries name a page (0: free).  A table of
+ * -1 and zeros elsewhere is an empty pool.  The three are changed only by the
+ * spec_page_* calls; the calls on keys and values read the table alone.
+ *
+ * A round: spec_append_round (staged) -> spec_attend_pages -> spec_verify_tree
+ * -> spec_page_reserve (first = len - 1, total = len - 1 + n_emit) and
+ * spec_page_copy of its copies -> spec_store_pages of the path.  Prompts run
+ * through a 16-bit cache of one layer (spec_append_prompt, spec_attend_prompt),
+ * which spec_store_pages then stores; pieces of prompts have their prefix back by
+ * spec_load_pages.  Pools and 16-bit blocks begin on 16 bytes.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Workspace of the spec_page_* calls (256-byte aligned; no initial value). */
+SPEC_API size_t spec_page_workspace_bytes(int B, int MP, int P);
+
+/*
+ * Row dst[b] (NULL: b) becomes a fork of row src[b]: it names the source's
+ * pages for the first length[b] tokens (length NULL: all that it has), and lets
+ * go of those that it had.  src[b] = -1: it only lets go, which frees a
+ * sequence.  All sources are read as they were before the call, so rows may be
+ * forked into one another, and src = dst shortens a row.  Pages are shared, not
+ * copied; spec_page_reserve gives a row its own before they are written.
+ * Flagged, and left as it is: a row outside [0, N) (src: [-1, N)) or a repeated
+ * dst, a negative length or one longer than the source's pages, entries outside the
+ * pool.
+ */
+SPEC_API int spec_page_fork(int32_t *table, int32_t *held, int32_t *refs, int N, int MP, int P, int page, int B,
+                   const int32_t *src, const int32_t *dst, const int32_t *length, uint32_t *flags,
+                   void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/*
+ * Row idx[b] (NULL: b) gets the pages for total[b] tokens, of which those from
+ * first[b] on may be written until the next call: pages behind them are let go,
+ * missing ones are added, and a page with a token from first[b] .. total[b] - 1
+ * that other rows name too is replaced by one of the row's own (of rows in this
+ * call that share it and name it alone, the last keeps it).  Where a replaced
+ * page also holds tokens before first[b], copies[b] is the pair (old, new) that
+ * spec_page_copy has to copy before anything is written, else (-1, -1).  The
+ * lowest free pages are taken, by sequences in order, by places in order within
+ * one.  Where there are too few, missing[0] says by how many; then pages have
+ * been let go, but no row has got any, and what is held is that.  Else it is 0.
+ * Flagged, and left as it is: a row outside [0, N) or repeated, first < 0,
+ * total < 0 or of more than MP pages, entries outside the pool.
+ */
+SPEC_API int spec_page_reserve(int32_t *table, int32_t *held, int32_t *refs, int N, int MP, int P, int page,
+                      int B, const int32_t *first, const int32_t *total, const int32_t *idx,
+                      int32_t *copies, int32_t *missing, uint32_t *flags, void *workspace,
+                      size_t workspace_bytes, void *cuda_stream);
+
+/*
+ * With n live pages, gives the live ones from n on the numbers of the free ones
+ * below n, in order, so that the pool ends at n: table and refs are renamed, and
+ * moves [P, 2] int32 has the pairs (old, new) for spec_page_copy, n_moves [1] how
+ * many.  No page is both old and new.
+ */
+SPEC_API int spec_page_compact(int32_t *table, int32_t *held, int32_t *refs, int N, int MP, int P, int32_t *moves,
+                      int32_t *n_moves, void *workspace, size_t workspace_bytes, void *cuda_stream);
+
+/*
+ * Copies whole pages of a pool of `slabs` slabs of P pages of page_bytes (a
+ * multiple of 16; for the pool above 2 L slabs of H * block bytes; pages of
+ * any kind will do): pairs [M, 2] int32 (from, to), of which the first n_pairs[0]
+ * count (NULL: M).  from = -1: none.  err [1] int32 or NULL: pairs left out
+ * because they are outside the pool.  A page that is written must not be
+ * named twice.
+ */
+SPEC_API int spec_page_copy(void *pool, int slabs, int P, size_t page_bytes, const int32_t *pairs, int M,
+                   const int32_t *n_pairs, int32_t *err, void *cuda_stream);
+
+/*
+ * Stores rows of a 16-bit block src [L, 2, N, H, S, D] (bf16 or fp16; the staged
+ * block of a round, or a cache) into layers layer .. layer + L - 1 of a pool
+ * [L_pool, 2, P, H, block]: for j < count[b] <= T, row slot[b] + path[b, j] of
+ * src row idx[b] (slot NULL: 0; path [B, T], T <= SPEC_MAX_NODES, or NULL: j;
+ * idx NULL: b) becomes position pos[b] + j of table row row[b] (NULL: b) of
+ * table [R, MP].  Flagged, and nothing stored: a count outside [0, T], positions
+ * past MP pages, rows outside the block or the table, a repeated table row.  A
+ * token whose page is outside the pool is left out, and flagged.  B <= 65535.
+ */
+SPEC_API int spec_store_pages(const void *src, spec_dtype dt, int L, int N, int H, int S, int D, void *pool, int L_pool,
+                  int P, int page, int layer, const int32_t *table, int R, int MP, int B, int T,
+                  const int32_t *pos, const int32_t *count, const int32_t *slot, const int32_t *idx,
+                  const int32_t *row, const int32_t *path, uint32_t *flags, void *cuda_stream);
+
+/*
+ * The reverse: positions pos[b] .. pos[b] + count[b] - 1 to rows slot[b] .. of
+ * dst [L, 2, N, H, S, D], as the values that the codes stand for.  Flagged as
+ * above, with repeated rows of dst in place of the table's.
+ */
+SPEC_API int spec_load_pages(const void *pool, int L_pool, int P, int page, int layer, void *dst, spec_dtype dt, int L,
+                 int N, int H, int S, int D, const int32_t *table, int R, int MP, int B, int T,
+                 const int32_t *pos, const int32_t *count, const int32_t *slot, const int32_t *idx,
+                 const int32_t *row, uint32_t *flags, void *cuda_stream);
+
+/* Workspace of spec_attend_pages; what spec_attend_workspace_bytes says of
+ * its own holds for it, and the two calls may share one that is large enough for both. */
+SPEC_API size_t spec_attend_pages_workspace_bytes(int T, int Hq, int H, int D);
+
+/*
+ * spec_attend_round with the prefix (positions 0 .. len - 2) in pages of the
+ * pool's layer `layer`, by table row idx[b] (NULL: b), and the nodes in staged
+ * [L, 2, B, H, T, D]; q, staged and out in bf16 or fp16, heads of 64 or 128.
+ * What lies in pages behind the prefix may be anything.  Flagged: len < 1 or
+ * past MP pages, a row outside [0, R), n_nodes outside [0, T]; and pages of
+ * the prefix outside the pool, where the outputs of the sequence are undefined.
+ */
+SPEC_API int spec_attend_pages(const void *q, spec_dtype dt, int B, int T, int Hq, const void *pool, int L, int P,
+                         int H, int page, int D, int layer, const int32_t *table, int R, int MP,
+                         const int32_t *len, const int32_t *idx, const int32_t *n_nodes,
+                         const uint64_t *tree_mask, const void *staged, float scale, void *out,
+                         uint32_t *flags, void *workspace, size_t workspace_bytes, void *cuda_stream);
 
 #ifdef __cplusplus
 }

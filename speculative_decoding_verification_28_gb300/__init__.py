@@ -57,3 +57,17 @@ from .forward import (  # noqa: F401,E402
     spec_tree_workspace_bytes,
     spec_verify_tree,
 )
+from .paged import (  # noqa: F401,E402
+    PAGE_SIZES,
+    Q4_GROUP,
+    q4_block_bytes,
+    spec_attend_pages_workspace_bytes,
+    spec_attend_pages,
+    spec_load_pages,
+    spec_page_compact,
+    spec_page_copy,
+    spec_page_fork,
+    spec_page_reserve,
+    spec_page_workspace_bytes,
+    spec_store_pages,
+)

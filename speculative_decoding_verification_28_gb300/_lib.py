@@ -68,6 +68,20 @@ SIGNATURES["spec_verify_tree"] = ([_vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, c
 SIGNATURES["spec_commit_tree"] = ([_vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp,
                                    _vp, _vp], _i32)
 
+SIGNATURES["spec_page_workspace_bytes"] = ([_i32, _i32, _i32], _sz)
+SIGNATURES["spec_page_fork"] = ([_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _i32)
+SIGNATURES["spec_page_reserve"] = ([_vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                    _vp], _i32)
+SIGNATURES["spec_page_compact"] = ([_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp], _i32)
+SIGNATURES["spec_page_copy"] = ([_vp, _i32, _i32, _sz, _vp, _i32, _vp, _vp, _vp], _i32)
+SIGNATURES["spec_store_pages"] = ([_vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _i32,
+                                _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32)
+SIGNATURES["spec_load_pages"] = ([_vp, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _i32,
+                               _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32)
+SIGNATURES["spec_attend_pages_workspace_bytes"] = ([_i32, _i32, _i32, _i32], _sz)
+SIGNATURES["spec_attend_pages"] = ([_vp, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i32,
+                                       _i32, _vp, _vp, _vp, _vp, _vp, _f32, _vp, _vp, _vp, _sz, _vp], _i32)
+
 _lib = None
 
 

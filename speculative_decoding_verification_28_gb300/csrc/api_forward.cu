@@ -5,6 +5,7 @@
 #include <math.h>
 
 #include "forward.h"
+#include "host_checks.h"
 #include "spec_common.cuh"
 
 using namespace spec;
@@ -13,24 +14,6 @@ namespace {
 
 bool dtype_ok(int dt) { return dt == SPEC_F32 || dt == SPEC_BF16 || dt == SPEC_F16; }
 int dtype_bytes(int dt) { return dt == SPEC_F32 ? 4 : 2; }
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-int launched(cudaError_t e) { return e == cudaSuccess ? SPEC_OK : SPEC_ECUDA; }
-
-// A large tensor of a call, in bytes (null: none).
-struct Span {
-    uintptr_t at, n;
-};
-// n elements of e bytes from element `first` of p; sizes past what memory can
-// hold are cut to that, so that nothing wraps
-Span span(const void *p, double first, double n, int e)
-{
-    const double top = 1e18;
-    const double f = first * e, x = n * e;
-    return Span{p ? reinterpret_cast<uintptr_t>(p) + (uintptr_t)(f < top ? f : top) : 0,
-                p ? (uintptr_t)(x < top ? x : top) : 0};
-}
-bool overlap(const Span &a, const Span &b) { return a.n && b.n && a.at < b.at + b.n && b.at < a.at + a.n; }
-
 // one layer of a cache [L, 2, N, H, S, D]
 Span layer_span(const void *kv, int N, int H, int S, int D, int layer, int e)
 {
@@ -60,11 +43,6 @@ LayerView layer_view(const void *kv, int N, int H, int S, int D, int layer)
     v.S = S;
     v.D = D;
     return v;
-}
-
-bool int_arrays_ok(const void *a, const void *b, const void *c, const void *d, const void *e)
-{
-    return aligned(a, 4) && aligned(b, 4) && aligned(c, 4) && aligned(d, 4) && aligned(e, 4);
 }
 
 struct Append {
@@ -138,12 +116,19 @@ constexpr long long kWaitClocks = 4000000000ll;
 thread_local int starve_clocks = 0;
 void set_waits(AttendArgs &a)
 {
-    a.wait_clocks = starve_clocks > 0 ? starve_clocks : kWaitClocks;
-    a.starve = starve_clocks > 0;
-    starve_clocks = 0;
+    const Waits w = next_waits();
+    a.wait_clocks = w.clocks;
+    a.starve = w.starve;
 }
 
 }  // namespace
+
+spec::Waits spec::next_waits()
+{
+    const Waits w{starve_clocks > 0 ? starve_clocks : kWaitClocks, starve_clocks > 0};
+    starve_clocks = 0;
+    return w;
+}
 
 extern "C" {
 

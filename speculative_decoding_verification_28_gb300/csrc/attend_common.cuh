@@ -132,18 +132,18 @@ __device__ __forceinline__ void flag_if_gave_up(const AttendArgs &a)
 }
 
 // Every thread takes a contiguous range of sequences; s_run is complete after
-// the caller's next __syncthreads.  CTA 0 writes the flags.
-template <int THREADS>
+// the caller's next __syncthreads.  CTA 0 writes the flags (FLAGS).
+template <int THREADS, bool FLAGS = true>
 __device__ void find_run(const AttendArgs &a, const Shape &sh, uint32_t *s_scan, Run *s_run)
 {
     const int per_thread = (a.seq.B + THREADS - 1) / THREADS;
     const int b0 = threadIdx.x * per_thread, b1 = min(a.seq.B, b0 + per_thread);
-    const uint32_t off = blockIdx.x == 0 && gave_up(a) ? SPEC_FLAG_TIMEOUT : 0u;  // a call before this one
+    const uint32_t off = FLAGS && blockIdx.x == 0 && gave_up(a) ? SPEC_FLAG_TIMEOUT : 0u;  // a call before this one
     uint32_t w = 0;
     for (int b = b0; b < b1; ++b) {
         const Seq s = load_seq(a.seq, a.cache.N, a.cache.S, b);
         w += round_weight(s, sh, a.cache.H);
-        if (blockIdx.x == 0 && a.flags)
+        if (FLAGS && blockIdx.x == 0 && a.flags)
             a.flags[b] = (s.ok ? 0u : SPEC_FLAG_BAD_STATE) | off;
     }
     uint32_t total;
