@@ -9,18 +9,13 @@
 // memory traffic that they arrive with.  A product's summed index may run in any
 // order as long as both operands have the same, so lane (g, t) takes the
 // dimensions of one run of bytes: t's quarter of key row g, g's eighth of value
-// rows 2t, 2t + 1, 2t + 8, 2t + 9.  A nibble c under the bits of 1024 (or of 64,
-// for a byte's upper one) is the half 1024 + c (64 + c); one multiply-add with
-// the scale s' = s / 128 and -1032 s' (-72 s') gives (c - 8) s' exactly (7
-// significant bits, and s' >= 2^-24).  S and O are then 128 times too small, which the
-// scale and the last division make good.
+// rows 2t, 2t + 1, 2t + 8, 2t + 9.  Expanded values, and so S and O, are 128
+// times too small (q4_expand.cuh), which the scale and the last division make good.
 //
-// Queries are fp16 too.  A bf16 row is multiplied by the power of two that puts
-// its largest value at 2^8: what falls under fp16's steps is less than 2^-32 of
-// the row's largest, less than fp32 sums keep.  Weights are fp16, 2^11 times as
-// large as the softmax's, under a maximum that moves only when a tile exceeds it by
-// more than 2^4 (tcgen.cuh says why).  The nodes' tile is in the staged type on
-// both sides, weights too.
+// Queries are fp16 too, bf16 rows times a power of two.  Weights are fp16, 2^11
+// times as large as the softmax's, under a maximum that moves only when a tile
+// exceeds it by more than 2^4 (tcgen.cuh says why).  The nodes' tile is in the
+// staged type on both sides, weights too.
 //
 // A CTA: four warps, each with its own running statistics and its share of the
 // unit's tiles of 64 keys, joined in shared memory at the unit's end; a fifth
@@ -30,7 +25,7 @@
 #include "attend_common.cuh"
 #include "bulk_copy.cuh"
 #include "paged.h"
-#include "q4.cuh"
+#include "q4_expand.cuh"
 #include "tcgen.cuh"
 
 namespace spec {
@@ -66,39 +61,6 @@ struct Q4Shared {
 __device__ __forceinline__ void q4_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 static_assert(32 * kQ4Warps == 128, "q4_sync");
 static_assert(3 * kAttendCtas <= kGaveUpWord, "one counter per CTA");
-
-__device__ __forceinline__ uint32_t hfma2_bits(uint32_t a, uint32_t b, uint32_t c)
-{
-    uint32_t r;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-    return r;
-}
-__device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
-// s' and its products of a pair of scales, halves with bits byte << 7
-struct Scale2 {
-    uint32_t s, low, high;
-    __device__ __forceinline__ explicit Scale2(uint32_t halves)
-    {
-        s = hmul2_bits(halves, 0x20002000u);  // 2^-7
-        low = hmul2_bits(s, 0xE408E408u);     // -1032
-        high = hmul2_bits(s, 0xD480D480u);    // -72
-    }
-};
-// nibbles 0, 1, 2, 3 of both halves of w, as values
-__device__ __forceinline__ void q4_expand(uint32_t w, const Scale2 &s, uint32_t *x)
-{
-    const uint32_t v = w >> 8;
-    x[0] = hfma2_bits((w & 0x000F000Fu) | 0x64006400u, s.s, s.low);
-    x[1] = hfma2_bits((w & 0x00F000F0u) | 0x54005400u, s.s, s.high);
-    x[2] = hfma2_bits((v & 0x000F000Fu) | 0x64006400u, s.s, s.low);
-    x[3] = hfma2_bits((v & 0x00F000F0u) | 0x54005400u, s.s, s.high);
-}
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
@@ -298,15 +260,6 @@ __device__ __forceinline__ void q4_tile(Q4State<D, NQ> &st, const unsigned char 
     }
 }
 
-// the eight 16-bit values of a 16-byte word as pairs (0, 4), (1, 5), (2, 6), (3, 7)
-__device__ __forceinline__ void pairs_of(const uint4 &x, uint32_t *p)
-{
-    p[0] = __byte_perm(x.x, x.z, 0x5410);
-    p[1] = __byte_perm(x.x, x.z, 0x7632);
-    p[2] = __byte_perm(x.y, x.w, 0x5410);
-    p[3] = __byte_perm(x.y, x.w, 0x7632);
-}
-
 // Adds what is not finite among the nodes' values (taken out of the products: a
 // weight of 0 times it would reach rows that do not see it) to the rows that do.
 // Their weights are positive, so that it stays as it is.
@@ -491,8 +444,7 @@ __device__ __forceinline__ void q4_queries(const AttendArgs &a, const AttendUnit
             }
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            if (top > 0.0f && top <= 3.4e38f)
-                e = min(100, 8 - ((int)(__float_as_uint(top) >> 23) - 127));
+            e = q4_row_exponent(top);
             const float f = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
             for (int k = 0; k < D / 32; ++k)
@@ -759,6 +711,8 @@ template <typename T, int D>
 cudaError_t launch_q4_d(const AttendQ4Args &a, cudaStream_t st)
 {
     const int rows = a.a.seq.T * a.a.G;
+    if (rows > 16)
+        return launch_attend_q4_tc(a, std::is_same<T, __half>::value ? SPEC_F16 : SPEC_BF16, st);
     if (rows <= 8)
         return launch_q4<T, D, 1>(a, st);
     return rows <= 16 ? launch_q4<T, D, 2>(a, st) : launch_q4<T, D, 3>(a, st);
@@ -777,7 +731,8 @@ size_t attend_q4_workspace(int T, int Hq, int H, int D)
 {
     (void)T, (void)Hq, (void)H;
     const size_t one = 2 * 3 * kAttendCtas * part_floats<8>(D), many = 2 * 2 * kAttendCtas * part_floats<24>(D);
-    return align256(kPartHead + (one > many ? one : many) * sizeof(float));
+    const size_t few = align256(kPartHead + (one > many ? one : many) * sizeof(float)), tc = attend_q4_tc_workspace(D);
+    return few > tc ? few : tc;
 }
 
 }  // namespace spec

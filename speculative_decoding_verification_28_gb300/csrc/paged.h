@@ -76,6 +76,8 @@ struct AttendQ4Args {
     long long k_block, v_block;  // the layer's first block of keys, of values
 };
 cudaError_t launch_attend_q4(const AttendQ4Args &a, spec_dtype dt, cudaStream_t st);
+cudaError_t launch_attend_q4_tc(const AttendQ4Args &a, spec_dtype dt, cudaStream_t st);
+size_t attend_q4_tc_workspace(int D);
 size_t attend_q4_workspace(int T, int Hq, int H, int D);
 
 }  // namespace spec
