@@ -595,9 +595,10 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NQ>::kCtas) attend_q4_k
             it += tiles;
             // the next warp in turn has the nodes
             if (ok && u.tile_end == u.n_tiles && (it & (kQ4Warps - 1)) == warp) {
-                Q4State<D, NQ> x = st;  // the call keeps only this copy in memory
-                q4_nodes<T, D, NQ>(a, u, x);
-                st = x;
+                Q4State<D, NQ> y = st;  // the call keeps only these copies in memory
+                const AttendUnit v = u;
+                q4_nodes<T, D, NQ>(a, v, y);
+                st = y;
             }
             // the unit's parts of the four warps
 #pragma unroll

@@ -47,6 +47,27 @@ __device__ __forceinline__ void q4_expand(uint32_t w, const Scale2 &s, uint32_t 
     x[3] = hfma2_bits((v & 0x00F000F0u) | 0x54005400u, s.s, s.high);
 }
 
+// The same in bf16, in units of their own: under the bits of 128, 128 + c, times s
+// and -136 s (8 significant bits).
+struct Scale2Bf16 {
+    uint32_t s, low;
+    __device__ __forceinline__ explicit Scale2Bf16(uint32_t byte)
+    {
+        // bits byte << 4 are s * 2^-112
+        const uint32_t raw = byte == kNanScale ? 0x7FC07FC0u : byte * 0x00100010u;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(s) : "r"(raw), "r"(0x77807780u));
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(low) : "r"(s), "r"(0xC308C308u));
+    }
+};
+__device__ __forceinline__ void q4_expand(uint32_t w, const Scale2Bf16 &s, uint32_t *x)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+            : "=r"(x[i])
+            : "r"((w >> (4 * i) & 0x000F000Fu) | 0x43004300u), "r"(s.s), "r"(s.low));
+}
+
 // The eight 16-bit values of a 16-byte word in the order in which a word of
 // codes expands: (0, 4), (1, 5), (2, 6), (3, 7).
 __device__ __forceinline__ void pairs_of(const uint4 &x, uint32_t *p)
