@@ -38,6 +38,7 @@ struct Shape {
     int tile_keys;  // keys of a tile
     int unit_rows;  // query rows of a unit
     int G;          // query rows of a token
+    int idle;       // tiles that a unit's start and end cost, counted behind its own
 };
 __device__ __forceinline__ int round_tiles(const Seq &s, const Shape &sh)
 {
@@ -51,7 +52,7 @@ __device__ __forceinline__ int unit_groups(const Seq &s, const Shape &sh)
 // the host), so that the walk needs no 64-bit division
 __device__ __forceinline__ uint32_t round_weight(const Seq &s, const Shape &sh, int H)
 {
-    return (uint32_t)H * unit_groups(s, sh) * round_tiles(s, sh);
+    return (uint32_t)H * unit_groups(s, sh) * (round_tiles(s, sh) + sh.idle);
 }
 
 // The run of this CTA: filled by the whole CTA, read by every role.
@@ -186,22 +187,27 @@ struct UnitWalk {
     }
     __device__ bool next(AttendUnit &u)
     {
-        if (pos >= run.end)
-            return false;
+        uint32_t tiles, groups, which, t0;
         while (true) {
+            if (pos >= run.end)
+                return false;
             if (loaded != run.b) {
                 cur = load_seq(a->seq, a->cache.N, a->cache.S, run.b);
                 weight = round_weight(cur, sh, a->cache.H);
                 loaded = run.b;
             }
-            if (pos < run.seq_begin + weight)
+            if (pos >= run.seq_begin + weight) {
+                run.seq_begin += weight;
+                ++run.b;  // ends: run.end is at most the tiles of all sequences
+                continue;
+            }
+            tiles = round_tiles(cur, sh), groups = unit_groups(cur, sh);
+            const uint32_t off = pos - run.seq_begin, span = tiles + sh.idle;
+            which = off / span, t0 = off - which * span;
+            if (t0 < tiles)
                 break;
-            run.seq_begin += weight;
-            ++run.b;  // ends: run.end is at most the tiles of all sequences
+            pos += span - t0;  // a run that begins behind a unit's last tile
         }
-        const uint32_t tiles = round_tiles(cur, sh), groups = unit_groups(cur, sh);
-        const uint32_t off = pos - run.seq_begin;
-        const uint32_t which = off / tiles, t0 = off - which * tiles;
         const uint32_t left = run.end - pos;
         u.b = run.b;
         u.h = groups == 1 ? which : which / groups;
@@ -223,6 +229,8 @@ struct UnitWalk {
             u.part = blockIdx.x - first;
         }
         pos += u.tile_end - t0;
+        if (u.tile_end == (int)tiles)
+            pos += sh.idle;
         return true;
     }
 };

@@ -99,21 +99,26 @@ __device__ __forceinline__ void qt_expand(const unsigned char *stage, unsigned c
     constexpr int kEach = D == 128 ? 8 : 16;  // keys of a step
     const int panel = D == 128 ? (lane >> 3 ^ lane >> 2) & 1 : 0, group = 2 * panel + half;
     const int key0 = warp * (kKeys / kQtExpand) + (D == 128 ? lane >> 4 << 2 : lane >> 3 << 2) + k2;
-    const unsigned char *codes = stage + (KEYS ? 0 : Sh::kCodes) + group * 16;
-    const unsigned char *scales = stage + 2 * Sh::kCodes + (KEYS ? 0 : Sh::kScales) + group;
-    unsigned char *dst = to + panel * Sh::kPanel;
+    const unsigned char *codes = stage + (KEYS ? 0 : Sh::kCodes) + key0 * q4_codes(D) + group * 16;
+    const unsigned char *scales = stage + 2 * Sh::kCodes + (KEYS ? 0 : Sh::kScales) + key0 * q4_scales(D) + group;
+    unsigned char *dst = to + panel * Sh::kPanel + key0 * 128;
+    int at[4];  // steps are multiples of eight keys apart, which leaves the swizzle as it is
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        at[k] = ((4 * half + k) ^ (key0 & 7)) << 4;
 #pragma unroll 1
     for (int i = 0; i < kKeys / kQtExpand; i += kEach) {
-        const int key = key0 + i;
-        const uint4 w = *reinterpret_cast<const uint4 *>(codes + key * q4_codes(D));
-        const uint32_t b = key < valid ? scales[key * q4_scales(D)] : 0;
+        const uint4 w = *reinterpret_cast<const uint4 *>(codes + i * q4_codes(D));
+        uint32_t b = scales[i * q4_scales(D)];
+        if (!KEYS && valid < kKeys && key0 + i >= valid)  // products read these rows; keys' scores are hidden
+            b = 0;
         const S s(std::is_same<S, Scale2>::value ? b * 0x00800080u : b);
         const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             uint32_t y[4];
             q4_expand(x[k], s, y);
-            *reinterpret_cast<uint4 *>(dst + swizzled(key, 4 * half + k)) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4 *>(dst + at[k] + i * 128) = make_uint4(y[0], y[1], y[2], y[3]);
         }
     }
 }
@@ -239,7 +244,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) attend_q4_tc_kernel(const __gri
     const AttendArgs &a = x.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int kRows = kQtLanes / COPIES;  // of a unit
-    const Shape sh{kKeys, kRows, a.G};
+    const Shape sh{kKeys, kRows, a.G, 2};
     constexpr int kMmaWarp = kQtSoftmax, kLoadWarp = kMmaWarp + 1, kFirstExpand = kMmaWarp + 4;
     constexpr bool kHalf = std::is_same<T, __half>::value;
 
@@ -502,10 +507,8 @@ __global__ void __launch_bounds__(kQtThreads, 1) attend_q4_tc_kernel(const __gri
                         if (k == 0)
                             tc_wait_ld();
                         tc_pin<32>(x[k]);
-                        // at most 64 nodes, so all in the first two words
-                        const uint32_t w = tl.nodes && col >= 64 ? 0u : seen32(tl.nodes, bits, tl.valid, col / 32 + k);
-                        if (__any_sync(0xFFFFFFFFu, w != ~0u))
-                            hide32(x[k], w);
+                        if (tl.valid < kKeys)  // at most 64 nodes, so all in the first two words
+                            hide32(x[k], tl.nodes && col >= 64 ? 0u : seen32(tl.nodes, bits, tl.valid, col / 32 + k));
                         mx = fmaxf(mx, max32(x[k]));
                     }
                     // the lane's maximum; both threads have read their scores by then,
