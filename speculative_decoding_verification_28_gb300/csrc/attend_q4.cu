@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NQ>::kCtas) attend_q4_k
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&s.full[i], 1);
-            mbar_init(&s.empty[i], 1);
+            mbar_init(&s.empty[i], kQ4Warps);
         }
         mbar_init(&s.never, 1);
         fence_mbar_init();
@@ -574,19 +574,23 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NQ>::kCtas) attend_q4_k
                         st.o[q][j][e] = 0.0f;
             }
             const int tiles = max(0, min(u.tile_end, u.n_tiles - 1) - u.tile);  // of the prefix
-            const int j0 = (warp - (int)it) & (kQ4Warps - 1);
             if (a.starve)
                 ok = __all_sync(0xFFFFFFFFu, ok && wait_phase(&s.never, 0, &s.abort, limit));
-            if (ok && j0 < tiles) {
+            if (tiles > 0) {
                 uint32_t qf[NQ][D / 16][2];
                 float c[NQ][2];
                 q4_queries<T, D, NQ>(a, u, qf, c);
-                for (int j = j0; ok && j < tiles; j += kQ4Warps) {
+                // Every warp waits for every tile and releases it, though it computes
+                // only those whose turn is its own: copies may land out of order, and
+                // to a warp that had not seen a slot's tile before, the parity of the one
+                // before that would look like this one's
+                for (int j = 0; ok && j < tiles; ++j) {
                     const uint32_t i = it + j, sg = i % ST;
                     ok = __all_sync(0xFFFFFFFFu, wait_phase(&s.full[sg], (i / ST) & 1, &s.abort, limit));
                     if (!ok)
                         break;
-                    q4_tile<D, NQ>(st, s.ring[sg], min(kQ4Keys, u.seq.prefix - (u.tile + j) * kQ4Keys), qf, c);
+                    if ((i & (kQ4Warps - 1)) == warp)
+                        q4_tile<D, NQ>(st, s.ring[sg], min(kQ4Keys, u.seq.prefix - (u.tile + j) * kQ4Keys), qf, c);
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(&s.empty[sg]);
