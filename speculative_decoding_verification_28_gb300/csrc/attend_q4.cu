@@ -17,16 +17,15 @@
 // exceeds it by more than 2^4 (tcgen.cuh says why).  The nodes' tile is in the
 // staged type on both sides, weights too.
 //
-// A CTA: four warps, each with its own running statistics and its share of the
-// unit's tiles of 64 keys, joined in shared memory at the unit's end; a fifth
-// copies pages' codes and scales (cp.async.bulk) through a ring.
+// A CTA: four warps, each with its own running statistics and every fourth of the
+// unit's tiles of 64 keys, joined in shared memory at the unit's end; a fifth walks
+// over the units and copies pages' codes and scales (cp.async.bulk) through a ring.
+// A slot of the ring is always the same warp's: to a warp that had not waited for the
+// slot's tile before, that one's parity would look like its own tile's.
 #include <type_traits>
 
-#include "attend_common.cuh"
-#include "bulk_copy.cuh"
-#include "paged.h"
+#include "paged_units.cuh"
 #include "q4_expand.cuh"
-#include "tcgen.cuh"
 
 namespace spec {
 
@@ -39,7 +38,7 @@ template <int D, int NQ>
 struct Q4Shape {
     static constexpr int kRows = 8 * NQ;
     static constexpr int kCtas = NQ == 1 ? 3 : 2;  // of an SM
-    static constexpr int kStages = D == 64 ? 8 : NQ == 2 ? 8 : 6;
+    static constexpr int kStages = 2 * kQ4Warps;
     static constexpr int kCodes = kQ4Keys * q4_codes(D), kScales = kQ4Keys * q4_scales(D);
     static constexpr int kTile = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales
     static constexpr int kStride = D + 4;                 // floats of a row in the join
@@ -48,9 +47,10 @@ template <int D, int NQ>
 struct Q4Shared {
     using Sh = Q4Shape<D, NQ>;
     unsigned char ring[Sh::kStages][Sh::kTile];
-    float o[kQ4Warps][Sh::kRows][Sh::kStride];
-    float m[kQ4Warps][Sh::kRows], l[kQ4Warps][Sh::kRows];
+    float o[Sh::kRows][Sh::kStride];
+    float m[kQ4Warps][Sh::kRows], l[Sh::kRows];
     uint64_t full[Sh::kStages], empty[Sh::kStages], never;
+    PagedRing units;
     uint32_t scan[kQ4Threads / 32 + 1];
     Run run;
     uint32_t asked;  // tiles that were copied in all
@@ -157,38 +157,46 @@ __device__ __forceinline__ void q4_softmax(Q4State<D, NQ> &st, float (&s)[NSUB][
 
 // One tile of 4-bit keys and values; `valid` of its keys count.
 template <int D, int NQ>
-__device__ __forceinline__ void q4_tile(Q4State<D, NQ> &st, const unsigned char *tile, int valid,
+__device__ __forceinline__ void q4_tile(Q4State<D, NQ> &st, unsigned char *tile, int valid,
                                         const uint32_t (&qf)[NQ][D / 16][2], const float (&c)[NQ][2])
 {
     using Sh = Q4Shape<D, NQ>;
     constexpr int NSUB = kQ4Keys / 16, KW = D / 32, VW = D / 64;  // words of a lane: of a key row, of a value row
+    constexpr int kScales = q4_scales(D);
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const unsigned char *kc = tile, *vc = tile + Sh::kCodes, *ks = vc + Sh::kCodes, *vs = ks + Sh::kScales;
+    unsigned char *vs = tile + 2 * Sh::kCodes + Sh::kScales;
+    if (valid < kQ4Keys) {
+        // values behind the last key have no weight, but what lies there may be anything
+        for (int row = valid + lane; row < kQ4Keys; row += 32)
+#pragma unroll
+            for (int i = 0; i < kScales; ++i)
+                vs[row * kScales + i] = 0;
+        __syncwarp();
+    }
+    const unsigned char *kc = tile + g * q4_codes(D) + t * KW * 4;
+    const unsigned char *ks = tile + 2 * Sh::kCodes + g * kScales + t * kScales / 4;
     float s[NSUB][NQ][4];
 #pragma unroll
     for (int i = 0; i < NSUB; ++i) {
-#pragma unroll
-        for (int q = 0; q < NQ; ++q)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                s[i][q][e] = 16 * i < valid ? 0.0f : -INFINITY;
-        if (16 * i >= valid)
-            continue;
         uint32_t w[2][KW];
         uint32_t sc[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const int row = 16 * i + 8 * r + g;
-            const uint32_t *p = reinterpret_cast<const uint32_t *>(kc + row * q4_codes(D)) + t * KW;
+            const int row = 16 * i + 8 * r;
             if constexpr (KW == 4) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(p);
+                const uint4 x = *reinterpret_cast<const uint4 *>(kc + row * q4_codes(D));
                 w[r][0] = x.x, w[r][1] = x.y, w[r][2] = x.z, w[r][3] = x.w;
             } else {
-                const uint2 x = *reinterpret_cast<const uint2 *>(p);
+                const uint2 x = *reinterpret_cast<const uint2 *>(kc + row * q4_codes(D));
                 w[r][0] = x.x, w[r][1] = x.y;
             }
-            sc[r] = (uint32_t)ks[row * q4_scales(D) + t * q4_scales(D) / 4] * 0x00800080u;
+            sc[r] = (uint32_t)ks[row * kScales] * 0x00800080u;
         }
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                s[i][q][e] = 0.0f;
         const Scale2 s0(sc[0]), s1(sc[1]);
 #pragma unroll
         for (int k = 0; k < KW; ++k) {
@@ -203,7 +211,10 @@ __device__ __forceinline__ void q4_tile(Q4State<D, NQ> &st, const unsigned char 
                     mma16816<__half>(s[i][q], a, qf[q][2 * k + h][0], qf[q][2 * k + h][1]);
             }
         }
-        if (valid < 16 * i + 16) {
+    }
+    if (valid < kQ4Keys) {
+#pragma unroll
+        for (int i = 0; i < NSUB; ++i)
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
                 if (16 * i + g >= valid)
@@ -211,60 +222,50 @@ __device__ __forceinline__ void q4_tile(Q4State<D, NQ> &st, const unsigned char 
                 if (16 * i + 8 + g >= valid)
                     s[i][q][2] = s[i][q][3] = -INFINITY;
             }
-        }
     }
     uint32_t pb[NSUB][NQ][2];
     q4_softmax<__half, D, NQ, NSUB>(st, s, c, pb);
+    const unsigned char *vc = tile + Sh::kCodes + 2 * t * q4_codes(D) + g * VW * 4;
+    const unsigned char *vsl = vs + 2 * t * kScales + g * kScales / 8;
 #pragma unroll
     for (int i = 0; i < NSUB; ++i) {
-        if (16 * i >= valid)
-            break;
-        uint32_t a[2][8 * VW][1];  // [pair of keys][dimension]
+        uint32_t a[2][8 * VW];  // [pair of keys][dimension]
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const int row = 16 * i + 8 * r + 2 * t;
+            const int row = 16 * i + 8 * r;
+            const uint32_t *pa = reinterpret_cast<const uint32_t *>(vc + row * q4_codes(D));
+            const uint32_t *pn = reinterpret_cast<const uint32_t *>(vc + (row + 1) * q4_codes(D));
             uint32_t wa[VW], wb[VW];
-            const uint32_t *pa = reinterpret_cast<const uint32_t *>(vc + row * q4_codes(D)) + g * VW;
-            const uint32_t *pn = reinterpret_cast<const uint32_t *>(vc + (row + 1) * q4_codes(D)) + g * VW;
 #pragma unroll
             for (int k = 0; k < VW; ++k) {
                 wa[k] = pa[k];
                 wb[k] = pn[k];
             }
-            uint32_t sa = vs[row * q4_scales(D) + g * q4_scales(D) / 8],
-                     sb = vs[(row + 1) * q4_scales(D) + g * q4_scales(D) / 8];
-            // keys behind the last have no weight, but what lies there may be anything
-            sa = row < valid ? sa : 0;
-            sb = row + 1 < valid ? sb : 0;
-            const Scale2 s2(sa << 7 | sb << 23);
+            const uint32_t sa = vsl[row * kScales], sb = vsl[(row + 1) * kScales];
+            const Scale2 s2((sa | sb << 16) << 7);
 #pragma unroll
             for (int k = 0; k < VW; ++k) {
-                uint32_t x[4];
-                q4_expand(__byte_perm(wa[k], wb[k], 0x5410), s2, x);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    a[r][8 * k + e][0] = x[e];
-                q4_expand(__byte_perm(wa[k], wb[k], 0x7632), s2, x);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    a[r][8 * k + 4 + e][0] = x[e];
+                q4_expand(__byte_perm(wa[k], wb[k], 0x5410), s2, a[r] + 8 * k);
+                q4_expand(__byte_perm(wa[k], wb[k], 0x7632), s2, a[r] + 8 * k + 4);
             }
         }
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
-            const uint32_t v[4] = {a[0][2 * j][0], a[0][2 * j + 1][0], a[1][2 * j][0], a[1][2 * j + 1][0]};
+            const uint32_t v[4] = {a[0][2 * j], a[0][2 * j + 1], a[1][2 * j], a[1][2 * j + 1]};
 #pragma unroll
             for (int q = 0; q < NQ; ++q)
                 mma16816<__half>(st.o[q][j], v, pb[i][q][0], pb[i][q][1]);
         }
     }
+    if (valid < kQ4Keys)  // the zeros above come before the slot's next copy
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // Adds what is not finite among the nodes' values (taken out of the products: a
 // weight of 0 times it would reach rows that do not see it) to the rows that do.
 // Their weights are positive, so that it stays as it is.
 template <typename T, int D, int NQ>
-__device__ __noinline__ void q4_put_back(const AttendArgs &a, const AttendUnit &u, const T *values, float *o)
+__device__ __noinline__ void q4_put_back(const AttendArgs &a, const PagedUnit &u, const T *values, float *o)
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     for (int q = 0; q < NQ; ++q)
@@ -272,9 +273,8 @@ __device__ __noinline__ void q4_put_back(const AttendArgs &a, const AttendUnit &
             const int r = 8 * q + 2 * t + e;
             if (r >= u.n_rows)
                 continue;
-            const int tok = (u.row0 + r) / a.G;
-            const uint64_t bits = a.mask ? a.mask[(size_t)u.b * a.seq.T + tok] : (2ull << tok) - 1;
-            for (int key = 0; key < u.seq.n; ++key)
+            const uint64_t bits = row_nodes(a, u, r);
+            for (int key = 0; key < u.n; ++key)
                 if (bits >> key & 1)
                     for (int d = 0; d < D / 8; ++d) {
                         const float f = Storage<T>::at(values + (size_t)key * D, g * (D / 8) + d);
@@ -286,11 +286,11 @@ __device__ __noinline__ void q4_put_back(const AttendArgs &a, const AttendUnit &
 
 // The nodes' tile: 16-bit keys and values from global memory, masks.
 template <typename T, int D, int NQ>
-__device__ __noinline__ void q4_nodes(const AttendArgs &a, const AttendUnit &u, Q4State<D, NQ> &to)
+__device__ __noinline__ void q4_nodes(const AttendArgs &a, const PagedUnit &u, Q4State<D, NQ> &to)
 {
     Q4State<D, NQ> st = to;
     constexpr int NSUB = SPEC_MAX_NODES / 16, KV = D / 32, VV = D / 64;  // 16-byte words of a lane: key row, value row
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, n = u.seq.n;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, n = u.n;
     const T *keys = reinterpret_cast<const T *>(a.staged) + (a.st_k + (long long)u.b * a.cache.H + u.h) * a.seq.T * D;
     const T *values = reinterpret_cast<const T *>(a.staged) + (a.st_v + (long long)u.b * a.cache.H + u.h) * a.seq.T * D;
     // the nodes' products are in the storage type, and O in its own units
@@ -317,14 +317,8 @@ __device__ __noinline__ void q4_nodes(const AttendArgs &a, const AttendUnit &u, 
         }
         uint64_t bits[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int tok = (u.row0 + 8 * q + 2 * t + e) / a.G;
-            bits[e] = 8 * q + 2 * t + e >= u.n_rows ? 0
-                      : a.mask                      ? a.mask[(size_t)u.b * a.seq.T + tok]
-                                                    : (2ull << tok) - 1;
-            if (n < 64)
-                bits[e] &= (1ull << n) - 1;
-        }
+        for (int e = 0; e < 2; ++e)
+            bits[e] = 8 * q + 2 * t + e < u.n_rows ? row_nodes(a, u, 8 * q + 2 * t + e) : 0;
 #pragma unroll
         for (int i = 0; i < NSUB; ++i) {
 #pragma unroll
@@ -418,7 +412,7 @@ __device__ __noinline__ void q4_nodes(const AttendArgs &a, const AttendUnit &u, 
 // A unit's queries as second operands, fp16, and the factor that takes a raw
 // score to base 2, per column.
 template <typename T, int D, int NQ>
-__device__ __forceinline__ void q4_queries(const AttendArgs &a, const AttendUnit &u, uint32_t (&qf)[NQ][D / 16][2],
+__device__ __forceinline__ void q4_queries(const AttendArgs &a, const PagedUnit &u, uint32_t (&qf)[NQ][D / 16][2],
                                            float (&c)[NQ][2])
 {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -473,95 +467,60 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NQ>::kCtas) attend_q4_k
     Q4Shared<D, NQ> &s = *reinterpret_cast<Q4Shared<D, NQ> *>(base);
     const AttendArgs &a = x.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Shape sh{kQ4Keys, Sh::kRows, a.G};
+    const Shape sh{kQ4Keys, Sh::kRows, a.G, 4};
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&s.full[i], 1);
-            mbar_init(&s.empty[i], kQ4Warps);
+            mbar_init(&s.empty[i], 1);
         }
+        units_init(s.units, kQ4Warps);
         mbar_init(&s.never, 1);
         fence_mbar_init();
         s.abort = 0;
+        s.asked = 0;
         s.run.begin = s.run.end = 0;
     }
     __syncthreads();  // run.begin / end above come before find_run's
     find_run<kQ4Threads, false>(a, sh, s.scan, &s.run);
     __syncthreads();
     const long long limit = a.wait_clocks;
-    UnitWalk units(a, sh, s.run);
-    AttendUnit u{};
-    uint32_t it = 0;  // tiles through the ring
 
     if (warp == kQ4Warps) {
         // ------------------------------------------------------------ loads
-        const int log2 = x.pool.page_log2, piece = min(kQ4Keys, 1 << log2), per = kQ4Keys / piece;
-        const int which = lane & 3, mine = lane >> 2;  // K codes, V codes, K scales, V scales of one piece of a tile
-        const int width = which < 2 ? q4_codes(D) : q4_scales(D);
-        const int at_tile = (which & 1 ? (which < 2 ? Sh::kCodes : Sh::kScales) : 0) + (which < 2 ? 0 : 2 * Sh::kCodes);
-        const long long first = which & 1 ? x.v_block : x.k_block;
+        UnitWalk walk(a, sh, s.run);
+        AttendUnit w{};
+        TileCopies<D, kQ4Keys> copies(x);
+        uint32_t it = 0, n = 0;
         bool ok = true;
-        while (ok && units.next(u)) {
-            const int32_t *row = x.pool.table + (size_t)u.seq.row * x.pool.MP;
-            const int end = min(u.tile_end, u.n_tiles - 1);
-            int have = -1, held = 0;  // table entry of piece `have` + lane of the sequence
-            for (int tile = u.tile; ok && tile < end; ++tile, ++it) {
-                const int sg = it % ST, valid = min(kQ4Keys, u.seq.prefix - tile * kQ4Keys);
-                const int p0 = tile * per;
-                if (have < 0 || p0 + per > have + 32) {
-                    have = p0;
-                    const long long tok = (long long)(p0 + lane) * piece;
-                    held = tok < u.seq.prefix ? __ldg(row + (tok >> log2)) : 0;
-                    held = held >= 0 && held < x.pool.P ? held : 0;  // flagged below
-                }
-                const int page = __shfl_sync(0xFFFFFFFFu, held, p0 - have + (mine < per ? mine : 0));
+        while (ok && walk.next(w)) {
+            ok = units_put(s.units, n++, &w, &s.abort, limit);
+            prefetch_unit<T, D>(a, w);
+            copies.begin();
+            const int end = min(w.tile_end, w.n_tiles - 1);
+            for (int tile = w.tile; ok && tile < end; ++tile, ++it) {
+                const int sg = it % ST, valid = min(kQ4Keys, w.seq.prefix - tile * kQ4Keys);
+                const int page = copies.template page_of<true>(w, tile);
                 ok = __all_sync(0xFFFFFFFFu, wait_phase(&s.empty[sg], ((it / ST) & 1) ^ 1, &s.abort, limit));
                 if (!ok)
                     break;
-                const int pieces = (valid + piece - 1) / piece;
                 if (lane == 0)
-                    mbar_arrive_expect_tx(&s.full[sg], (uint32_t)(pieces * piece * 2 * (q4_codes(D) + q4_scales(D))));
+                    mbar_arrive_expect_tx(&s.full[sg], copies.bytes(valid));
                 __syncwarp();
-                if (mine < pieces) {
-                    const unsigned char *blk = x.pool.pool + (first + (long long)page * x.pool.H + u.h) * x.pool.block;
-                    const int in_page = (tile * kQ4Keys) & ((1 << log2) - 1);  // of a piece as long as the tile
-                    const long long off = which < 2 ? 0 : (long long)q4_codes(D) << log2;
-                    bulk_g2s(s.ring[sg] + at_tile + mine * piece * width, blk + off + (long long)in_page * width,
-                             (uint32_t)(piece * width), &s.full[sg]);
-                }
+                copies.issue(w, tile, page, valid, s.ring[sg], &s.full[sg]);
             }
         }
+        if (ok)
+            units_put(s.units, n, nullptr, &s.abort, limit);
         if (lane == 0)
             s.asked = it;
-        // flags of the sequences whose first tile this CTA had, and by CTA 0 those that have none
-        if (a.flags) {
-            UnitWalk again(a, sh, s.run);
-            while (again.next(u)) {
-                if (u.tile != 0 || u.h != 0 || u.row0 != 0)
-                    continue;
-                const int32_t *row = x.pool.table + (size_t)u.seq.row * x.pool.MP;
-                bool fine = true;
-                for (int i = lane; (long long)i << log2 < u.seq.prefix; i += 32) {
-                    const int page = __ldg(row + i);
-                    fine &= page >= 0 && page < x.pool.P;
-                }
-                fine = __all_sync(0xFFFFFFFFu, fine);
-                if (lane == 0)
-                    a.flags[u.b] = fine ? 0u : SPEC_FLAG_BAD_STATE;
-            }
-            if (blockIdx.x == 0)
-                for (int b = lane; b < a.seq.B; b += 32) {
-                    const Seq q = load_seq(a.seq, a.cache.N, a.cache.S, b);
-                    if (q.n == 0)
-                        a.flags[b] = q.ok ? 0u : SPEC_FLAG_BAD_STATE;
-                }
-            __syncwarp();
-            flag_if_gave_up(a);
-        }
+        paged_flags(x, sh, s.run);
     } else {
         // ---------------------------------------------------------- compute
-        bool ok = true;
         const int g = lane >> 2, t = lane & 3;
-        while (units.next(u)) {
+        uint32_t it = 0;  // tiles through the ring
+        bool ok = !a.starve || __all_sync(0xFFFFFFFFu, wait_phase(&s.never, 0, &s.abort, limit));
+        for (uint32_t n = 0; units_wait(s.units, n, &s.abort, limit); ++n) {
+            const PagedUnit &u = *units_at(s.units, n);  // read as it is wanted: registers are short
             Q4State<D, NQ> st;
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
@@ -574,23 +533,17 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NQ>::kCtas) attend_q4_k
                         st.o[q][j][e] = 0.0f;
             }
             const int tiles = max(0, min(u.tile_end, u.n_tiles - 1) - u.tile);  // of the prefix
-            if (a.starve)
-                ok = __all_sync(0xFFFFFFFFu, ok && wait_phase(&s.never, 0, &s.abort, limit));
-            if (tiles > 0) {
+            const int j0 = (warp - (int)it) & (kQ4Warps - 1);
+            if (ok && j0 < tiles) {
                 uint32_t qf[NQ][D / 16][2];
                 float c[NQ][2];
                 q4_queries<T, D, NQ>(a, u, qf, c);
-                // Every warp waits for every tile and releases it, though it computes
-                // only those whose turn is its own: copies may land out of order, and
-                // to a warp that had not seen a slot's tile before, the parity of the one
-                // before that would look like this one's
-                for (int j = 0; ok && j < tiles; ++j) {
+                for (int j = j0; ok && j < tiles; j += kQ4Warps) {
                     const uint32_t i = it + j, sg = i % ST;
                     ok = __all_sync(0xFFFFFFFFu, wait_phase(&s.full[sg], (i / ST) & 1, &s.abort, limit));
                     if (!ok)
                         break;
-                    if ((i & (kQ4Warps - 1)) == warp)
-                        q4_tile<D, NQ>(st, s.ring[sg], min(kQ4Keys, u.seq.prefix - (u.tile + j) * kQ4Keys), qf, c);
+                    q4_tile<D, NQ>(st, s.ring[sg], min(kQ4Keys, u.prefix - (u.tile + j) * kQ4Keys), qf, c);
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(&s.empty[sg]);
@@ -599,12 +552,12 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NQ>::kCtas) attend_q4_k
             it += tiles;
             // the next warp in turn has the nodes
             if (ok && u.tile_end == u.n_tiles && (it & (kQ4Warps - 1)) == warp) {
-                Q4State<D, NQ> y = st;  // the call keeps only these copies in memory
-                const AttendUnit v = u;
-                q4_nodes<T, D, NQ>(a, v, y);
+                Q4State<D, NQ> y = st;  // the call keeps only this copy in memory
+                q4_nodes<T, D, NQ>(a, u, y);
                 st = y;
             }
-            // the unit's parts of the four warps
+            // The warps' parts, under a common maximum, added up by the first, one
+            // after another: a buffer for each would cost the ring its second slots.
 #pragma unroll
             for (int q = 0; q < NQ; ++q)
 #pragma unroll
@@ -612,80 +565,127 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NQ>::kCtas) attend_q4_k
 #pragma unroll
                     for (int k = 4; k < 32; k <<= 1)
                         st.l[q][e] += __shfl_xor_sync(0xFFFFFFFFu, st.l[q][e], k);
-                    if (g == 0) {
+                    if (g == 0)
                         s.m[warp][8 * q + 2 * t + e] = st.m[q][e];
-                        s.l[warp][8 * q + 2 * t + e] = st.l[q][e];
-                    }
-                    float *row = s.o[warp][8 * q + 2 * t + e] + g * (D / 8);
-#pragma unroll
-                    for (int j = 0; j < D / 16; ++j)
-                        *reinterpret_cast<float2 *>(row + 2 * j) = make_float2(st.o[q][j][e], st.o[q][j][e + 2]);
                 }
             q4_sync();
+#pragma unroll
+            for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * q + 2 * t + e;
+                    float m = s.m[0][r];
+#pragma unroll
+                    for (int w = 1; w < kQ4Warps; ++w)
+                        m = fmaxf(m, s.m[w][r]);
+                    const float f = exp2f(st.m[q][e] - (m == -INFINITY ? 0.0f : m));
+                    st.m[q][e] = m;
+                    st.l[q][e] *= f;
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        st.o[q][j][e] *= f * kQ4Units;
+                        st.o[q][j][e + 2] *= f * kQ4Units;
+                    }
+                }
+#pragma unroll 1
+            for (int w = 1; w < kQ4Warps; ++w) {
+                if (warp == w) {
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float *row = s.o[8 * q + 2 * t + e] + g * (D / 8);
+#pragma unroll
+                            for (int j = 0; j < D / 16; j += 2)
+                                *reinterpret_cast<float4 *>(row + 2 * j) = make_float4(
+                                    st.o[q][j][e], st.o[q][j][e + 2], st.o[q][j + 1][e], st.o[q][j + 1][e + 2]);
+                            if (g == 0)
+                                s.l[8 * q + 2 * t + e] = st.l[q][e];
+                        }
+                }
+                q4_sync();
+                if (warp == 0) {
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float *row = s.o[8 * q + 2 * t + e] + g * (D / 8);
+#pragma unroll
+                            for (int j = 0; j < D / 16; j += 2) {
+                                const float4 z = *reinterpret_cast<const float4 *>(row + 2 * j);
+                                st.o[q][j][e] += z.x;
+                                st.o[q][j][e + 2] += z.y;
+                                st.o[q][j + 1][e] += z.z;
+                                st.o[q][j + 1][e + 2] += z.w;
+                            }
+                            st.l[q][e] += s.l[8 * q + 2 * t + e];
+                        }
+                }
+                q4_sync();
+            }
             const bool whole = u.n_parts == 1;
-            float *slot = whole ? nullptr : part_slot<Sh::kRows>(a, blockIdx.x, u.part);
-            for (int i = tid; i < u.n_rows * (D / 8); i += 32 * kQ4Warps) {
-                const int r = i / (D / 8), d = i % (D / 8) * 8;
-                float m = -INFINITY, l = 0.0f, y[8] = {}, f[kQ4Warps];
+            if (warp == 0) {
+                float *slot = whole ? nullptr : part_slot<Sh::kRows>(a, blockIdx.x, u.part);
 #pragma unroll
-                for (int w = 0; w < kQ4Warps; ++w)
-                    m = fmaxf(m, s.m[w][r]);
-                const float m0 = m == -INFINITY ? 0.0f : m;
+                for (int q = 0; q < NQ; ++q)
 #pragma unroll
-                for (int w = 0; w < kQ4Warps; ++w) {
-                    f[w] = exp2f(s.m[w][r] - m0);
-                    l = fmaf(f[w], s.l[w][r], l);
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = 8 * q + 2 * t + e;
+                        if (r >= u.n_rows)
+                            continue;
+                        const float l = st.l[q][e], to = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+                        T *dst = reinterpret_cast<T *>(a.out) + row_place(a, u, r) + g * (D / 8);
 #pragma unroll
-                    for (int k = 0; k < 8; k += 4) {
-                        const float4 z = *reinterpret_cast<const float4 *>(&s.o[w][r][d + k]);
-                        y[k] = fmaf(f[w], z.x, y[k]);
-                        y[k + 1] = fmaf(f[w], z.y, y[k + 1]);
-                        y[k + 2] = fmaf(f[w], z.z, y[k + 2]);
-                        y[k + 3] = fmaf(f[w], z.w, y[k + 3]);
+                        for (int j = 0; j < D / 16; j += 4) {
+                            const float y[8] = {st.o[q][j][e],     st.o[q][j][e + 2],     st.o[q][j + 1][e], st.o[q][j + 1][e + 2],
+                                                st.o[q][j + 2][e], st.o[q][j + 2][e + 2], st.o[q][j + 3][e], st.o[q][j + 3][e + 2]};
+                            if (whole) {
+                                uint4 v;
+                                v.x = TcType<T>::pack(y[0] * to, y[1] * to);
+                                v.y = TcType<T>::pack(y[2] * to, y[3] * to);
+                                v.z = TcType<T>::pack(y[4] * to, y[5] * to);
+                                v.w = TcType<T>::pack(y[6] * to, y[7] * to);
+                                *reinterpret_cast<uint4 *>(dst + 2 * j) = v;
+                            } else {
+                                const int d = (g * (D / 8) + 2 * j) / 4;
+                                __stcg(reinterpret_cast<float4 *>(slot + part_quad<Sh::kRows>(d, r)),
+                                       make_float4(y[0], y[1], y[2], y[3]));
+                                __stcg(reinterpret_cast<float4 *>(slot + part_quad<Sh::kRows>(d + 1, r)),
+                                       make_float4(y[4], y[5], y[6], y[7]));
+                            }
+                        }
+                        if (!whole && g == 0) {
+                            __stcg(slot + (size_t)Sh::kRows * D + r, st.m[q][e]);
+                            __stcg(slot + (size_t)Sh::kRows * D + Sh::kRows + r, l);
+                        }
                     }
-                }
-                const float to = whole ? (l > 0.0f || l != l ? 128.0f / l : 0.0f) : 128.0f;
-                if (whole) {
-                    uint4 v;
-                    v.x = TcType<T>::pack(y[0] * to, y[1] * to);
-                    v.y = TcType<T>::pack(y[2] * to, y[3] * to);
-                    v.z = TcType<T>::pack(y[4] * to, y[5] * to);
-                    v.w = TcType<T>::pack(y[6] * to, y[7] * to);
-                    *reinterpret_cast<uint4 *>(reinterpret_cast<T *>(a.out) + row_place(a, u, r) + d) = v;
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; k += 4)
-                        __stcg(reinterpret_cast<float4 *>(slot + part_quad<Sh::kRows>((d + k) / 4, r)),
-                               make_float4(y[k] * to, y[k + 1] * to, y[k + 2] * to, y[k + 3] * to));
-                    if (d == 0) {
-                        __stcg(slot + (size_t)Sh::kRows * D + r, m);
-                        __stcg(slot + (size_t)Sh::kRows * D + Sh::kRows + r, l);
-                    }
-                }
             }
             if (!whole) {
-                __threadfence();
-                q4_sync();
-                if (tid == 0) {
-                    s.last = 0;
-                    if (!*reinterpret_cast<volatile int *>(&s.abort)) {
-                        int *cnt = part_counter(a, u.first_cta);
-                        s.last = atomicAdd(cnt, 1) == u.n_parts - 1;
-                        if (s.last)
-                            *cnt = 0;
+                if (warp == 0) {
+                    __threadfence();
+                    __syncwarp();
+                    if (lane == 0) {
+                        s.last = 0;
+                        if (!*reinterpret_cast<volatile int *>(&s.abort)) {
+                            int *cnt = part_counter(a, u.first_cta);
+                            s.last = atomicAdd(cnt, 1) == u.n_parts - 1;
+                            if (s.last)
+                                *cnt = 0;
+                        }
                     }
                 }
                 q4_sync();
                 if (s.last) {
                     __threadfence();
-                    join_parts<T, Sh::kRows>(a, u, tid, 32 * kQ4Warps, [] {
+                    join_parts<T, Sh::kRows>(a, join_unit(a, u), tid, 32 * kQ4Warps, [] {
                         __threadfence();
                         q4_sync();
                         return true;
                     });
                 }
+                q4_sync();  // `last` has been read
             }
-            q4_sync();  // the next unit's parts come after these were read
+            units_done(s.units, n);
         }
     }
     __syncthreads();
@@ -718,9 +718,7 @@ cudaError_t launch_q4_d(const AttendQ4Args &a, cudaStream_t st)
     const int rows = a.a.seq.T * a.a.G;
     if (rows > 16)
         return launch_attend_q4_tc(a, std::is_same<T, __half>::value ? SPEC_F16 : SPEC_BF16, st);
-    if (rows <= 8)
-        return launch_q4<T, D, 1>(a, st);
-    return rows <= 16 ? launch_q4<T, D, 2>(a, st) : launch_q4<T, D, 3>(a, st);
+    return rows <= 8 ? launch_q4<T, D, 1>(a, st) : launch_q4<T, D, 2>(a, st);
 }
 
 }  // namespace
@@ -735,7 +733,7 @@ cudaError_t launch_attend_q4(const AttendQ4Args &a, spec_dtype dt, cudaStream_t 
 size_t attend_q4_workspace(int T, int Hq, int H, int D)
 {
     (void)T, (void)Hq, (void)H;
-    const size_t one = 2 * 3 * kAttendCtas * part_floats<8>(D), many = 2 * 2 * kAttendCtas * part_floats<24>(D);
+    const size_t one = 2 * 3 * kAttendCtas * part_floats<8>(D), many = 2 * 2 * kAttendCtas * part_floats<16>(D);
     const size_t few = align256(kPartHead + (one > many ? one : many) * sizeof(float)), tc = attend_q4_tc_workspace(D);
     return few > tc ? few : tc;
 }

@@ -213,24 +213,6 @@ __device__ __noinline__ void qt_put_back32(const AttendArgs &a, const PagedUnit 
             }
 }
 
-// A unit's queries and nodes on their way to L2, by the walking warp: the expand
-// warps read them when the unit's turn comes, with nothing else to do meanwhile.
-template <typename T, int D>
-__device__ __forceinline__ void prefetch_unit(const AttendArgs &a, const AttendUnit &u)
-{
-    const int lane = threadIdx.x & 31;
-    auto fetch = [](const T *p, long long elements) {
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"((uint32_t)(elements * 2)) : "memory");
-    };
-    const int t0 = u.row0 / a.G, t1 = (u.row0 + u.n_rows - 1) / a.G;
-    for (int t = t0 + lane; t <= t1; t += 32)
-        fetch(reinterpret_cast<const T *>(a.q) + ((u.seq.tok0 + t) * a.Hq + (long long)u.h * a.G) * D, (long long)a.G * D);
-    if (u.tile_end == u.n_tiles && lane < 2)
-        fetch(reinterpret_cast<const T *>(a.staged) +
-                  ((lane ? a.st_v : a.st_k) + (long long)u.b * a.cache.H + u.h) * a.seq.T * D,
-              (long long)u.seq.n * D);
-}
-
 template <typename T, int D, int COPIES>
 __global__ void __launch_bounds__(kQtThreads, 1) attend_q4_tc_kernel(const __grid_constant__ AttendQ4Args x)
 {

@@ -7,6 +7,7 @@
 
 #include "attend_common.cuh"
 #include "paged.h"
+#include "q4.cuh"
 #include "tcgen.cuh"
 
 namespace spec {
@@ -70,6 +71,13 @@ __device__ __forceinline__ bool units_get(PagedRing &r, uint32_t n, PagedUnit &u
         return false;
     u = r.unit[i];
     return u.n_rows != 0;
+}
+// The same, where it lies: a unit stays there until units_done.
+__device__ __forceinline__ const PagedUnit *units_at(const PagedRing &r, uint32_t n) { return &r.unit[n % kUnitRing]; }
+__device__ __forceinline__ bool units_wait(PagedRing &r, uint32_t n, int *abort, long long limit)
+{
+    return __all_sync(0xFFFFFFFFu, wait_phase(&r.full[n % kUnitRing], (n / kUnitRing) & 1, abort, limit)) &&
+           units_at(r, n)->n_rows != 0;
 }
 // ... which is done with it
 __device__ __forceinline__ void units_done(PagedRing &r, uint32_t n)
@@ -158,6 +166,24 @@ struct TileCopies {
         bulk_g2s(to + at + mine * piece * width, blk + off + (long long)in_page * width, (uint32_t)(piece * width), bar);
     }
 };
+
+// A unit's queries and nodes on their way to L2, by the walking warp: they
+// are read when the unit's turn comes, with nothing else to do meanwhile.
+template <typename T, int D>
+__device__ __forceinline__ void prefetch_unit(const AttendArgs &a, const AttendUnit &u)
+{
+    const int lane = threadIdx.x & 31;
+    auto fetch = [](const T *p, long long elements) {
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"((uint32_t)(elements * 2)) : "memory");
+    };
+    const int t0 = u.row0 / a.G, t1 = (u.row0 + u.n_rows - 1) / a.G;
+    for (int t = t0 + lane; t <= t1; t += 32)
+        fetch(reinterpret_cast<const T *>(a.q) + ((u.seq.tok0 + t) * a.Hq + (long long)u.h * a.G) * D, (long long)a.G * D);
+    if (u.tile_end == u.n_tiles && lane < 2)
+        fetch(reinterpret_cast<const T *>(a.staged) +
+                  ((lane ? a.st_v : a.st_k) + (long long)u.b * a.cache.H + u.h) * a.seq.T * D,
+              (long long)u.seq.n * D);
+}
 
 // By the walking warp at its end: flags of the sequences whose first tile this
 // CTA had, and by CTA 0 of those that have none.

@@ -27,6 +27,14 @@ __device__ __forceinline__ uint32_t hmul2_bits(uint32_t a, uint32_t b)
     return r;
 }
 
+// (a & b) | c in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
 // s' and its products, of a pair of scales: halves with bits byte << 7
 struct Scale2 {
     uint32_t s, low, high;
@@ -41,10 +49,10 @@ struct Scale2 {
 __device__ __forceinline__ void q4_expand(uint32_t w, const Scale2 &s, uint32_t *x)
 {
     const uint32_t v = w >> 8;
-    x[0] = hfma2_bits((w & 0x000F000Fu) | 0x64006400u, s.s, s.low);
-    x[1] = hfma2_bits((w & 0x00F000F0u) | 0x54005400u, s.s, s.high);
-    x[2] = hfma2_bits((v & 0x000F000Fu) | 0x64006400u, s.s, s.low);
-    x[3] = hfma2_bits((v & 0x00F000F0u) | 0x54005400u, s.s, s.high);
+    x[0] = hfma2_bits(and_or(w, 0x000F000Fu, 0x64006400u), s.s, s.low);
+    x[1] = hfma2_bits(and_or(w, 0x00F000F0u, 0x54005400u), s.s, s.high);
+    x[2] = hfma2_bits(and_or(v, 0x000F000Fu, 0x64006400u), s.s, s.low);
+    x[3] = hfma2_bits(and_or(v, 0x00F000F0u, 0x54005400u), s.s, s.high);
 }
 
 // The same in bf16, in units of their own: under the bits of 128, 128 + c, times s
@@ -65,7 +73,7 @@ __device__ __forceinline__ void q4_expand(uint32_t w, const Scale2Bf16 &s, uint3
     for (int i = 0; i < 4; ++i)
         asm("fma.rn.bf16x2 %0, %1, %2, %3;"
             : "=r"(x[i])
-            : "r"((w >> (4 * i) & 0x000F000Fu) | 0x43004300u), "r"(s.s), "r"(s.low));
+            : "r"(and_or(w >> (4 * i), 0x000F000Fu, 0x43004300u)), "r"(s.s), "r"(s.low));
 }
 
 // The eight 16-bit values of a 16-byte word in the order in which a word of
