@@ -26,7 +26,7 @@ int page_log2(int page)
 int check_pool(int L, int P, int H, int page, int D, int R, int MP)
 {
     if (L < 1 || P < 1 || P > kMostPages || H < 1 || H > 65535 || page_log2(page) < 0 || R < 1 || MP < 1 ||
-        MP > kMostPages || (long long)MP * page > INT_MAX || D < kGroup || D > SPEC_MAX_HEAD_DIM || D % kGroup != 0)
+        MP > kMostPages || (long long)MP * page > INT_MAX - 8192 || D < kGroup || D > SPEC_MAX_HEAD_DIM || D % kGroup != 0)
         return SPEC_EINVAL;
     // rows of blocks: thread indices over a layer's pages and heads stay in 63 bits
     return (long long)L * 2 * H <= INT_MAX ? SPEC_OK : SPEC_EINVAL;

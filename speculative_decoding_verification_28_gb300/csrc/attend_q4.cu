@@ -495,18 +495,14 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NQ>::kCtas) attend_q4_k
         while (ok && walk.next(w)) {
             ok = units_put(s.units, n++, &w, &s.abort, limit);
             prefetch_unit<T, D>(a, w);
-            copies.begin();
+            copies.begin(w);
             const int end = min(w.tile_end, w.n_tiles - 1);
             for (int tile = w.tile; ok && tile < end; ++tile, ++it) {
-                const int sg = it % ST, valid = min(kQ4Keys, w.seq.prefix - tile * kQ4Keys);
-                const int page = copies.template page_of<true>(w, tile);
+                const int sg = it % ST, page = copies.template page_of<true>(tile);
                 ok = __all_sync(0xFFFFFFFFu, wait_phase(&s.empty[sg], ((it / ST) & 1) ^ 1, &s.abort, limit));
                 if (!ok)
                     break;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&s.full[sg], copies.bytes(valid));
-                __syncwarp();
-                copies.issue(w, tile, page, valid, s.ring[sg], &s.full[sg]);
+                copies.issue(tile, page, s.ring[sg], &s.full[sg]);
             }
         }
         if (ok)

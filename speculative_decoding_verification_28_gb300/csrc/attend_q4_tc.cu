@@ -291,17 +291,13 @@ __global__ void __launch_bounds__(kQtThreads, 1) attend_q4_tc_kernel(const __gri
         while (ok && walk.next(w)) {
             ok = units_put(s.units, n++, &w, &s.abort, limit);
             prefetch_unit<T, D>(a, w);
-            copies.begin();
+            copies.begin(w);
             for (int tile = min(w.tile_end, w.n_tiles - 1) - 1; ok && tile >= w.tile; --tile, ++it) {
-                const int sg = it % ST, valid = min(kKeys, w.seq.prefix - tile * kKeys);
-                const int page = copies.template page_of<false>(w, tile);
+                const int sg = it % ST, page = copies.template page_of<false>(tile);
                 ok = wait(&s.st_empty[sg], ((it / ST) & 1) ^ 1);
                 if (!ok)
                     break;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(&s.st_full[sg], copies.bytes(valid));
-                __syncwarp();
-                copies.issue(w, tile, page, valid, stage_p + sg * Sh::kStage, &s.st_full[sg]);
+                copies.issue(tile, page, stage_p + sg * Sh::kStage, &s.st_full[sg]);
             }
         }
         if (ok)

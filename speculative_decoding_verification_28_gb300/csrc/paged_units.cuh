@@ -116,54 +116,66 @@ __device__ __forceinline__ AttendUnit join_unit(const AttendArgs &a, const Paged
 }
 
 // The copies of a tile of KEYS keys of a unit, by the whole walking warp: codes
-// and scales of its keys and values, a copy a lane, as K codes, V codes, K
-// scales, V scales one after another.
+// and scales of its keys and values, a copy a lane (page of 16: 32 lanes), as K codes,
+// V codes, K scales, V scales one after another.  What does not change from tile to tile is
+// worked out once a unit: this warp's time a tile is what the others wait for.
 template <int D, int KEYS>
 struct TileCopies {
     static constexpr int kCodes = KEYS * q4_codes(D), kScales = KEYS * q4_scales(D);
-    const PoolView &pool;
-    long long k_block, v_block;
-    int piece, per;       // tokens that lie side by side in a page, up to a tile; pieces of a tile
-    int have, held;       // this lane's table entry: that of piece have + lane of the sequence
+    const int32_t *table, *row;
+    const unsigned char *first;  // this lane's part of page 0, of key head 0
+    const unsigned char *base;   // ... of the unit's key head
+    long long block, page_bytes;
+    int MP, P, log2, log2_piece, per;  // a piece: tokens that lie side by side in a page, up to a tile; pieces of a tile
+    int width, bytes, to, mine;        // of this lane's part of a piece: a token's bytes, all, place in the tile; its piece
+    int prefix, have, held;            // this lane's table entry: that of piece have + lane of the sequence
     __device__ __forceinline__ TileCopies(const AttendQ4Args &x)
-        : pool(x.pool), k_block(x.k_block), v_block(x.v_block), piece(min(KEYS, 1 << x.pool.page_log2)),
-          per(KEYS / piece), have(0), held(0)
     {
+        const int which = threadIdx.x & 3;
+        table = x.pool.table;
+        MP = x.pool.MP;
+        P = x.pool.P;
+        log2 = x.pool.page_log2;
+        log2_piece = min(31 - __clz(KEYS), log2);
+        per = KEYS >> log2_piece;
+        mine = (threadIdx.x & 31) >> 2;
+        block = x.pool.block;
+        page_bytes = x.pool.H * block;
+        width = which < 2 ? q4_codes(D) : q4_scales(D);
+        bytes = width << log2_piece;
+        to = (which & 1 ? (which < 2 ? kCodes : kScales) : 0) + (which < 2 ? 0 : 2 * kCodes) + mine * bytes;
+        first = x.pool.pool + (which & 1 ? x.v_block : x.k_block) * block + (which < 2 ? 0 : (long long)q4_codes(D) << log2);
     }
-    // before the first tile of a unit; the tiles go up or down from `tile`
-    __device__ __forceinline__ void begin() { have = -1; }
-    // bytes of a tile with `valid` keys
-    __device__ __forceinline__ uint32_t bytes(int valid) const
+    __device__ __forceinline__ void begin(const AttendUnit &u)
     {
-        return (uint32_t)((valid + piece - 1) / piece * piece * 2 * (q4_codes(D) + q4_scales(D)));
+        row = table + (size_t)u.seq.row * MP;
+        base = first + u.h * block;
+        prefix = u.seq.prefix;
+        have = -1;
     }
     // page of this lane's piece of the tile; UP: whether tiles go up
     template <bool UP>
-    __device__ __forceinline__ int page_of(const AttendUnit &u, int tile)
+    __device__ __forceinline__ int page_of(int tile)
     {
-        const int lane = threadIdx.x & 31, mine = lane >> 2, p0 = tile * per;
+        const int p0 = tile * per;
         if (have < 0 || (UP ? p0 + per > have + 32 : p0 < have)) {
             have = UP ? p0 : max(0, p0 + per - 32);
-            const long long tok = (long long)(have + lane) * piece;
-            held = tok < u.seq.prefix ? __ldg(pool.table + (size_t)u.seq.row * pool.MP + (tok >> pool.page_log2)) : 0;
-            held = held >= 0 && held < pool.P ? held : 0;  // flagged at the walk's end
+            const int tok = (have + (threadIdx.x & 31)) << log2_piece;  // fewer than 2^31 and a few pages: no overflow
+            held = tok >= 0 && tok < prefix ? __ldg(row + (tok >> log2)) : 0;
+            held = (unsigned)held < (unsigned)P ? held : 0;  // flagged at the walk's end
         }
         return __shfl_sync(0xFFFFFFFFu, held, p0 - have + (mine < per ? mine : 0));
     }
-    // after lane 0 announced the bytes
-    __device__ __forceinline__ void issue(const AttendUnit &u, int tile, int page, int valid, unsigned char *to,
-                                          uint64_t *bar) const
+    __device__ __forceinline__ void issue(int tile, int page, unsigned char *slot, uint64_t *bar) const
     {
-        const int lane = threadIdx.x & 31, which = lane & 3, mine = lane >> 2, log2 = pool.page_log2;
-        if (mine >= (valid + piece - 1) / piece)
-            return;
-        const int width = which < 2 ? q4_codes(D) : q4_scales(D);
-        const int at = (which & 1 ? (which < 2 ? kCodes : kScales) : 0) + (which < 2 ? 0 : 2 * kCodes);
-        const unsigned char *blk =
-            pool.pool + ((which & 1 ? v_block : k_block) + (long long)page * pool.H + u.h) * pool.block;
-        const long long off = which < 2 ? 0 : (long long)q4_codes(D) << log2;
-        const int in_page = (tile * KEYS) & ((1 << log2) - 1);  // of a piece as long as the tile
-        bulk_g2s(to + at + mine * piece * width, blk + off + (long long)in_page * width, (uint32_t)(piece * width), bar);
+        const int valid = min(KEYS, prefix - tile * KEYS), pieces = (valid + (1 << log2_piece) - 1) >> log2_piece;
+        if ((threadIdx.x & 31) == 0)
+            mbar_arrive_expect_tx(bar, (uint32_t)((pieces << log2_piece) * 2 * (q4_codes(D) + q4_scales(D))));
+        __syncwarp();
+        if (mine < pieces) {
+            const int in_page = (tile * KEYS) & ((1 << log2) - 1);  // not 0 only where a piece is as long as the tile
+            bulk_g2s(slot + to, base + page * page_bytes + in_page * width, (uint32_t)bytes, bar);
+        }
     }
 };
 
@@ -199,11 +211,11 @@ __device__ __noinline__ inline void paged_flags(const AttendQ4Args &x, const Sha
         if (u.tile != 0 || u.h != 0 || u.row0 != 0)
             continue;
         const int32_t *row = x.pool.table + (size_t)u.seq.row * x.pool.MP;
+        const int pages = (int)(((long long)u.seq.prefix + (1 << x.pool.page_log2) - 1) >> x.pool.page_log2);
         bool fine = true;
-        for (int i = lane; (long long)i << x.pool.page_log2 < u.seq.prefix; i += 32) {
-            const int page = __ldg(row + i);
-            fine &= page >= 0 && page < x.pool.P;
-        }
+#pragma unroll 8
+        for (int i = lane; i < pages; i += 32)
+            fine &= (unsigned)__ldg(row + i) < (unsigned)x.pool.P;
         fine = __all_sync(0xFFFFFFFFu, fine);
         if (lane == 0)
             a.flags[u.b] = fine ? 0u : SPEC_FLAG_BAD_STATE;
