@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NQ>::kCtas) attend_q4_k
     Q4Shared<D, NQ> &s = *reinterpret_cast<Q4Shared<D, NQ> *>(base);
     const AttendArgs &a = x.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const Shape sh{kQ4Keys, Sh::kRows, a.G, 4};
+    const Shape sh{kQ4Keys, Sh::kRows, a.G, 8};
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&s.full[i], 1);
