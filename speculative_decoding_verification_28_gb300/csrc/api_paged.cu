@@ -42,6 +42,7 @@ PoolView pool_view(void *pool, int L, int P, int H, int page, int D, const int32
     v.D = D;
     v.page_log2 = page_log2(page);
     v.block = q4_block(page, D);
+    v.page_bytes = v.block * H;
     v.table = table;
     v.R = R;
     v.MP = MP;

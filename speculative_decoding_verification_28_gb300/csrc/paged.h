@@ -14,7 +14,7 @@ struct PoolView {
     unsigned char *pool;
     int L, P, H, D;
     int page_log2;
-    long long block;  // bytes of a head's tokens of a page
+    long long block, page_bytes;  // bytes of a head's tokens of a page, and of all heads'
     const int32_t *table;
     int R, MP;
 };

@@ -140,7 +140,7 @@ struct TileCopies {
         per = KEYS >> log2_piece;
         mine = (threadIdx.x & 31) >> 2;
         block = x.pool.block;
-        page_bytes = x.pool.H * block;
+        page_bytes = x.pool.page_bytes;
         width = which < 2 ? q4_codes(D) : q4_scales(D);
         bytes = width << log2_piece;
         to = (which & 1 ? (which < 2 ? kCodes : kScales) : 0) + (which < 2 ? 0 : 2 * kCodes) + mine * bytes;

@@ -23,11 +23,13 @@ __host__ __device__ inline long long q4_block(int page, int D)
 }
 
 // max |x| of a group -> the byte of max |x| / 7, rounded to even.  The quotient's
-// fp32 rounding does not change the result: a tie is exact in fp32, and max |x|
-// (11 bits at most) is otherwise at least 2^-12 of its value away from one.
+// fp32 rounding (a product corrected by its remainder) does not change the result: a tie
+// is exact in fp32, and max |x| (11 bits at most) is otherwise at least 2^-12 of its value
+// away from one.
 __device__ __forceinline__ int q4_scale_byte(float amax)
 {
-    const float f = __fdiv_rn(amax, 7.0f);
+    float f = amax * (1.0f / 7.0f);
+    f = fmaf(fmaf(f, -7.0f, amax), 1.0f / 7.0f, f);
     int b;
     if (f < 6.103515625e-05f) {  // 2^-14: steps of 2^-17
         b = __float2int_rn(f * 131072.0f);
@@ -39,15 +41,28 @@ __device__ __forceinline__ int q4_scale_byte(float amax)
 }
 __device__ __forceinline__ float q4_scale(int byte) { return __half2float(__ushort_as_half((unsigned short)(byte << 7))); }
 
-// x / s to the nearest code, ties to even.  q is the quotient rounded once
-// (a product with the reciprocal r, corrected by its remainder), which is exact
-// at ties; adding 1.5 * 2^23 + 8 rounds it to an integer in the low bits.
-__device__ __forceinline__ uint32_t q4_code(float x, float s, float r)
+// About 1 / s, off by less than 2^-22 of it.
+__device__ __forceinline__ float q4_reciprocal(float s)
 {
-    float q = x * r;
-    q = fmaf(fmaf(-q, s, x), r, q);
-    q = fminf(fmaxf(q, -7.0f), 7.0f);
-    return __float_as_uint(q + 12582920.0f) & 15u;
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    return r;
+}
+// x / s to the nearest integer, ties to even, as a float; r about 1 / s.  A
+// quotient below 8 is within 2^-19 of x r, and half way between integers or at least
+// 2^-12 away from that (x has 11 bits at most, s four): 768 + x r, whose last bit is 2^-14,
+// is exact where it is half way, and on the right side where it is not.  Adding 1.5 *
+// 2^23 less 768 then rounds to integers.
+__device__ __forceinline__ float q4_level(float x, float r)
+{
+    return __fsub_rn(__fadd_rn(fmaf(x, r, 768.0f), 12582912.0f - 768.0f), 12582912.0f);
+}
+// Four levels within -7 .. 7 as codes, in the low 16 bits: summed in fp32 with their
+// place values, which is exact, and 2^23 + 0x8888 more, so that the integer pipe has
+// one instruction for four.
+__device__ __forceinline__ uint32_t q4_pack4(float a, float b, float c, float d)
+{
+    return __float_as_uint(__fadd_rn(fmaf(d, 4096.0f, fmaf(c, 256.0f, fmaf(b, 16.0f, a))), 8388608.0f + 34952.0f));
 }
 
 }  // namespace spec

@@ -86,6 +86,13 @@ __device__ __forceinline__ void pairs_of(const uint4 &x, uint32_t *p)
     p[3] = __byte_perm(x.y, x.w, 0x7632);
 }
 
+// A word's values as they come out -> in order.
+__device__ __forceinline__ uint4 in_order(const uint32_t *x)
+{
+    return make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[0], x[1], 0x7632),
+                      __byte_perm(x[2], x[3], 0x7632));
+}
+
 // exponent e of the power of two that a bf16 row with largest magnitude `top`
 // is held times in fp16: top goes to 2^8 .. 2^9.  What falls under fp16's steps
 // is then less than 2^-32 of it, less than fp32 sums keep.
