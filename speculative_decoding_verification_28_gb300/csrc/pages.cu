@@ -24,7 +24,7 @@ __device__ __forceinline__ bool in_pool(const PagesArgs &p, int page) { return p
 
 size_t page_workspace(int B, int MP, int P)
 {
-    const size_t fork = (size_t)B * ((size_t)MP + 1), reserve = 5 * (size_t)B + (size_t)P, compact = 3 * (size_t)P + 1;
+    const size_t fork = (size_t)B * ((size_t)MP + 1), reserve = 6 * (size_t)B + 3 * (size_t)P, compact = 3 * (size_t)P + 1;
     const size_t most = fork > reserve ? fork : reserve;
     return align256((most > compact ? most : compact) * 4);
 }
@@ -149,106 +149,109 @@ __device__ __forceinline__ uint32_t page_bits(const PagesArgs &p, int p0)
 // ---------------------------------------------------------------------------
 // reserve
 // ---------------------------------------------------------------------------
-// What a sequence wants: pages lo .. hi - 1 of its own are written, it ends
-// with n pages and had h.
-struct Wish {
-    int row, lo, hi, n, h;
-    bool ok;
+constexpr int kWishes = 1024;     // sequences whose wishes fit in shared memory
+constexpr int kWishLanes = 8;     // threads of a sequence
+
+// What the sequences want, by sequence: of row's h pages those at places lo .. hi - 1 are
+// written, and it ends with n; h < 0: refused.  at: first the pages it needs, then the place
+// of the first of them among all.
+struct Wishes {
+    int *row, *lo, *hi, *n, *h, *at;
+    __device__ Wishes(int *p, int B) : row(p), lo(p + B), hi(lo + B), n(hi + B), h(n + B), at(h + B) {}
 };
-__device__ __forceinline__ Wish wish_of(const ReserveArgs &a, int b)
-{
-    const PagesArgs &p = a.p;
-    Wish w{};
-    w.row = a.idx ? a.idx[b] : b;
-    const long long first = a.first[b], total = a.total[b], n = pages_for(total, p.page_log2);
-    w.ok = w.row >= 0 && w.row < p.N && first >= 0 && total >= 0 && n <= p.MP;
-    if (!w.ok)
-        return w;
-    w.h = p.held[w.row];
-    w.ok = w.h >= 0 && w.h <= p.MP;
-    w.n = (int)n;
-    const int keep = w.h < w.n ? w.h : w.n;
-    w.lo = first < total ? (int)(first >> p.page_log2) : keep;
-    w.lo = w.lo < keep ? w.lo : keep;
-    w.hi = keep;
-    return w;
-}
 
 // An entry that will be replaced holds ~page until it is.
-__device__ __forceinline__ int entry(const PagesArgs &p, int row, int i)
-{
-    const int e = __ldcg(p.table + (size_t)row * p.MP + i);
-    return e < 0 ? ~e : e;
-}
-
 __global__ void __launch_bounds__(kBookThreads) reserve_kernel(const ReserveArgs a)
 {
     __shared__ int s_words[32];
+    __shared__ int s_wishes[6 * kWishes];
     const PagesArgs &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int *s_ok = p.ws, *lo = p.ws + p.B, *hi = lo + p.B, *rows = hi + p.B, *want = rows + p.B, *grant = want + p.B;
+    // eight threads a sequence: their lane among them, their bits in the warp
+    const int k = lane & (kWishLanes - 1), shift = lane & ~(kWishLanes - 1);
+    const unsigned us = ((1u << kWishLanes) - 1) << shift;
+    constexpr int kGroups = kBookThreads / kWishLanes;
+    const int first_b = tid / kWishLanes;
+    int *grant = p.ws, *writers = grant + p.P, *last = writers + p.P;
+    const Wishes w(p.B <= kWishes ? s_wishes : last + p.P, p.B);
 
-    // check, and let go of pages behind the new end
+    // rows named twice
     for (int b = warp; b < p.B; b += kBookWarps) {
-        const Wish w = wish_of(a, b);
-        bool ok = w.ok;
-        const bool twice = repeated_row(a.idx, p.B, w.row);
-        ok = ok && !twice;
-        if (ok)
-            for (int i = w.lo + lane; i < w.h; i += 32)
-                ok &= in_pool(p, p.table[(size_t)w.row * p.MP + i]);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (ok)
-            for (int i = w.n + lane; i < w.h; i += 32) {
-                int32_t *e = p.table + (size_t)w.row * p.MP + i;
-                atomicSub(p.refs + *e, 1);
-                *e = -1;
-            }
+        const int row = a.idx ? a.idx[b] : b;
+        const bool twice = repeated_row(a.idx, p.B, row);
         if (lane == 0) {
-            s_ok[b] = ok;
-            lo[b] = w.lo;
-            hi[b] = ok ? w.hi : w.lo;
-            rows[b] = w.row;
+            w.row[b] = row;
+            w.h[b] = twice ? -1 : 0;
+        }
+    }
+    __syncthreads();
+    // check, and let go of pages behind the new end
+    for (int b = first_b; b < p.B; b += kGroups) {
+        const int row = w.row[b];
+        const long long first = a.first[b], total = a.total[b], n = pages_for(total, p.page_log2);
+        bool ok = w.h[b] == 0 && row >= 0 && row < p.N && first >= 0 && total >= 0 && n <= p.MP;
+        const int h = ok ? p.held[row] : 0;
+        ok = ok && h >= 0 && h <= p.MP;
+        const int keep = (int)(h < n ? h : n);
+        const long long from = first < total ? first >> p.page_log2 : keep;
+        const int lo = from < keep ? (int)from : keep;
+        int32_t *entries = p.table + (size_t)(ok ? row : 0) * p.MP;
+        if (ok)
+#pragma unroll 4
+            for (int i = lo + k; i < h; i += kWishLanes)
+                ok &= in_pool(p, entries[i]);
+        ok = __all_sync(us, ok);
+        if (ok) {
+            for (int i = lo + k; i < keep; i += kWishLanes) {
+                writers[entries[i]] = 0;
+                last[entries[i]] = -1;
+            }
+#pragma unroll 4
+            for (int i = (int)n + k; i < h; i += kWishLanes) {
+                atomicSub(p.refs + entries[i], 1);
+                entries[i] = -1;
+            }
+        }
+        __syncwarp(us);
+        if (k == 0) {
+            w.lo[b] = lo;
+            w.hi[b] = ok ? keep : lo;
+            w.n[b] = ok ? (int)n : 0;
+            w.h[b] = ok ? h : -1;
             if (p.flags)
                 p.flags[b] = ok ? 0u : SPEC_FLAG_BAD_STATE;
-            if (a.copies) {
-                a.copies[2 * b] = -1;
-                a.copies[2 * b + 1] = -1;
-            }
+            a.copies[2 * b] = -1;
+            a.copies[2 * b + 1] = -1;
         }
     }
     __threadfence();
     __syncthreads();
-
-    // Of the sequences that will write a shared page each takes another, but
-    // the last of them where nobody else names it.  A page is shared at the
-    // same place of every table that names it (fork copies rows).
-    for (int b = warp; b < p.B; b += kBookWarps) {
-        int swaps = 0;
-        for (int c = lo[b]; c < hi[b]; c += 32) {
-            const int i = c + lane;
-            const int page = i < hi[b] ? entry(p, rows[b], i) : 0;
-            const int refs = i < hi[b] ? __ldcg(p.refs + page) : 0;
-            unsigned shared = __ballot_sync(0xFFFFFFFFu, refs > 1);
-            while (shared) {
-                const int l = __ffs(shared) - 1, at = c + l;
-                shared &= shared - 1;
-                const int which = __shfl_sync(0xFFFFFFFFu, page, l);
-                int before = 0;
-                for (int o = lane; o < b; o += 32)
-                    before += lo[o] <= at && at < hi[o] && entry(p, rows[o], at) == which;
-                before = __reduce_add_sync(0xFFFFFFFFu, before);
-                if (before < __shfl_sync(0xFFFFFFFFu, refs, l) - 1) {
-                    if (lane == 0)
-                        __stcg(p.table + (size_t)rows[b] * p.MP + at, ~which);
-                    ++swaps;
-                }
+    // how many will write a page that several name, and which is the last of them
+    for (int b = first_b; b < p.B; b += kGroups)
+        for (int i = w.lo[b] + k; i < w.hi[b]; i += kWishLanes) {
+            const int page = p.table[(size_t)w.row[b] * p.MP + i];
+            if (__ldcg(p.refs + page) > 1) {
+                atomicAdd(writers + page, 1);
+                atomicMax(last + page, b);
             }
         }
-        if (lane == 0) {
-            const Wish w = wish_of(a, b);
-            want[b] = s_ok[b] ? swaps + max(0, w.n - w.h) : 0;
+    __threadfence();
+    __syncthreads();
+    // Each of them takes another page, but the last where nobody else names it.
+    for (int b = first_b; b < p.B; b += kGroups) {
+        int need = 0;
+        for (int i = w.lo[b] + k; i < w.hi[b]; i += kWishLanes) {
+            int32_t *e = p.table + (size_t)w.row[b] * p.MP + i;
+            const int page = *e, refs = __ldcg(p.refs + page);
+            if (refs > 1 && !(__ldcg(writers + page) == refs && __ldcg(last + page) == b)) {
+                *e = ~page;
+                ++need;
+            }
         }
+        need = __reduce_add_sync(us, need);
+        if (k == 0)
+            w.at[b] = w.h[b] < 0 ? 0 : need + max(0, w.n[b] - w.h[b]);
+        __syncwarp(us);
     }
     __threadfence();
     __syncthreads();
@@ -256,11 +259,11 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(const ReserveArgs
     // places of the sequences' wishes, in order
     int total = 0;
     for (int c = 0; c < p.B; c += kBookThreads) {
-        const int b = c + tid, v = b < p.B ? want[b] : 0;
+        const int b = c + tid, v = b < p.B ? w.at[b] : 0;
         int sum;
         const int before = block_before(v, s_words, &sum);
         if (b < p.B)
-            want[b] = total + before;
+            w.at[b] = total + before;
         total += sum;
         if (total > p.P)
             total = p.P + 1;  // more than there can be: enough to know
@@ -277,32 +280,31 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(const ReserveArgs
         found += sum;
     }
     const bool enough = found >= total;
-    if (tid == 0 && a.missing)
+    if (tid == 0)
         *a.missing = enough ? 0 : total - found;
     __threadfence();
     __syncthreads();
 
-    for (int b = warp; b < p.B; b += kBookWarps) {
-        if (!s_ok[b])
+    for (int b = first_b; b < p.B; b += kGroups) {
+        if (w.h[b] < 0)
             continue;
-        const Wish w = wish_of(a, b);
-        int at = want[b];
-        for (int c = w.lo; c < w.n; c += 32) {
-            const int i = c + lane;
-            int32_t *e = p.table + (size_t)w.row * p.MP + (i < w.n ? i : 0);
-            const int old = i < w.hi ? *e : 0;
-            const bool fresh = i < w.n && (i < w.hi ? old < 0 : enough);
-            const unsigned all = __ballot_sync(0xFFFFFFFFu, fresh && enough);
+        const int row = w.row[b], hi = w.hi[b], n = w.n[b], first = a.first[b];
+        int at = w.at[b];
+        for (int c = w.lo[b]; c < n; c += kWishLanes) {
+            const int i = c + k;
+            int32_t *e = p.table + (size_t)row * p.MP + (i < n ? i : 0);
+            const int old = i < hi ? *e : 0;
+            const bool fresh = i < n && (i < hi ? old < 0 : enough);
+            const unsigned all = __ballot_sync(us, fresh && enough) >> shift;
             if (fresh && !enough)
                 *e = ~old;  // as it was
             if (fresh && enough) {
-                const int page = grant[at + __popc(all & ((1u << lane) - 1))];
+                const int page = grant[at + __popc(all & ((1u << k) - 1))];
                 *e = page;
                 p.refs[page] = 1;
-                if (i < w.hi) {
+                if (i < hi) {
                     atomicSub(p.refs + ~old, 1);
-                    const int first = a.first[b];
-                    if (a.copies && i == first >> p.page_log2 && (first & ((1 << p.page_log2) - 1))) {
+                    if (i == first >> p.page_log2 && (first & ((1 << p.page_log2) - 1))) {
                         a.copies[2 * b] = ~old;
                         a.copies[2 * b + 1] = page;
                     }
@@ -310,8 +312,8 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(const ReserveArgs
             }
             at += __popc(all);
         }
-        if (lane == 0)
-            p.held[w.row] = enough ? w.n : w.hi;
+        if (k == 0)
+            p.held[row] = enough ? n : hi;
     }
 }
 
@@ -399,13 +401,15 @@ cudaError_t launch_page_compact(const CompactArgs &a, cudaStream_t st)
 // copies
 // ---------------------------------------------------------------------------
 constexpr int kCopyThreads = 256;
-constexpr int kCopyEach = 4;  // 16-byte words of a thread in flight
+constexpr int kCopyEach = 8;  // 16-byte words of a thread in flight
 constexpr int kCopyChunk = kCopyThreads * kCopyEach * 16;
 
-__global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const PageCopyArgs a)
+// CTA (x, y): chunk x of a page, the chunks of all slabs numbered through, of every
+// gridDim.y-th pair.
+__global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const PageCopyArgs a, int chunks, int chunk_bytes)
 {
     const int n = a.n_pairs ? max(0, min(*a.n_pairs, a.M)) : a.M;
-    if (blockIdx.x == 0 && a.err) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && a.err) {
         int bad = 0;
         for (int c = 0; c < n; c += kCopyThreads) {
             const int i = c + threadIdx.x;
@@ -415,19 +419,26 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const PageCopyA
         if (threadIdx.x == 0)
             *a.err = bad;
     }
-    const int chunks = (int)((a.bytes + kCopyChunk - 1) / kCopyChunk);
-    const long long items = (long long)n * a.slabs * chunks;
-    for (long long w = blockIdx.x; w < items; w += gridDim.x) {
-        const int i = (int)(w / ((long long)a.slabs * chunks));
-        const int rest = (int)(w - (long long)i * a.slabs * chunks), slab = rest / chunks, chunk = rest - slab * chunks;
-        const int from = a.pairs[2 * i], to = a.pairs[2 * i + 1];
+    if (chunks == 0)
+        return;
+    const int slab = blockIdx.x / chunks, chunk = blockIdx.x - slab * chunks;
+    const long long off = (long long)chunk * chunk_bytes;
+    unsigned char *base = a.pool + (long long)slab * a.P * a.bytes + off;
+    const int words = (int)(min((long long)chunk_bytes, a.bytes - off) / 16);
+    const int2 *pairs = reinterpret_cast<const int2 *>(a.pairs);
+    int i = blockIdx.y;
+    const bool wide = reinterpret_cast<uintptr_t>(a.pairs) % 8 == 0;
+    auto pair_at = [&](int j) {
+        return j >= n ? make_int2(-1, -1) : wide ? __ldg(pairs + j) : make_int2(a.pairs[2 * j], a.pairs[2 * j + 1]);
+    };
+    int2 next = pair_at(i);
+    for (; i < n; i += gridDim.y) {
+        const int from = next.x, to = next.y;
+        next = pair_at(i + gridDim.y);
         if (from < 0 || from >= a.P || to < 0 || to >= a.P)
             continue;
-        unsigned char *base = a.pool + (long long)slab * a.P * a.bytes;
-        const long long off = (long long)chunk * kCopyChunk;
-        const uint4 *src = reinterpret_cast<const uint4 *>(base + from * a.bytes + off);
-        uint4 *dst = reinterpret_cast<uint4 *>(base + to * a.bytes + off);
-        const int words = (int)(min((long long)kCopyChunk, a.bytes - off) / 16);
+        const uint4 *src = reinterpret_cast<const uint4 *>(base + from * a.bytes);
+        uint4 *dst = reinterpret_cast<uint4 *>(base + to * a.bytes);
         uint4 x[kCopyEach];
 #pragma unroll
         for (int k = 0; k < kCopyEach; ++k)
@@ -442,9 +453,13 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const PageCopyA
 
 cudaError_t launch_page_copy(const PageCopyArgs &a, cudaStream_t st)
 {
-    const long long items = (long long)a.M * a.slabs * ((a.bytes + kCopyChunk - 1) / kCopyChunk);
-    const long long most = 152 * 8;
-    page_copy_kernel<<<(unsigned)(items < 1 ? 1 : items < most ? items : most), kCopyThreads, 0, st>>>(a);
+    // chunks of a page, as even as 16-byte words allow
+    const int chunks = (int)((a.bytes + kCopyChunk - 1) / kCopyChunk);
+    const long long words = a.bytes / 16, each = (words + chunks - 1) / chunks;
+    const long long x = (long long)a.slabs * chunks, most = 152 * 8;  // eight CTAs an SM
+    const long long y = x < 1 ? 1 : most / x < 1 ? 1 : most / x < a.M ? most / x : a.M > 0 ? a.M : 1;
+    page_copy_kernel<<<dim3((unsigned)(x < 1 ? 1 : x), (unsigned)y), kCopyThreads, 0, st>>>(a, x < 1 ? 0 : chunks,
+                                                                                           (int)(each * 16));
     return cudaGetLastError();
 }
 
