@@ -23,25 +23,33 @@ def q4_block_bytes(page, D):
     return page * 17 * D // 32
 
 
-def _pool(pool, H, D, layer, layers):
+_page_of = {}  # tokens of a page by (bytes of a block, head size)
+
+
+def _pool(pool, dev, H, D, layer, layers):
     """Checked pool -> (address, L, P, page)."""
-    if pool.dim() != 5 or pool.shape[1] != 2 or pool.shape[3] != H:
+    shape = pool.shape
+    if len(shape) != 5 or shape[1] != 2 or shape[3] != H:
         raise ValueError(f"pool must be [L, 2, P, {H}, block]")
-    if not pool.is_cuda or pool.dtype is not torch.uint8 or not pool.is_contiguous():
-        _need(pool, torch.uint8, "pool")
-    page = pool.shape[4] * 32 // (17 * D) if D else 0
-    if q4_block_bytes(page, D) != pool.shape[4]:
-        raise ValueError(f"a block of {pool.shape[4]} bytes holds no whole number of tokens of heads of {D}")
-    if not 0 <= layer <= pool.shape[0] - layers:
-        raise ValueError(f"layers {layer} .. {layer + layers - 1} of {pool.shape[0]}")
-    return pool.data_ptr(), pool.shape[0], pool.shape[2], page
+    at = _at(pool, torch.uint8, "pool", dev, shape)
+    L, _, P, _, block = shape
+    page = _page_of.get((block, D))
+    if page is None:
+        page = block * 32 // (17 * D) if D else 0
+        if q4_block_bytes(page, D) != block:
+            raise ValueError(f"a block of {block} bytes holds no whole number of tokens of heads of {D}")
+        _page_of[block, D] = page
+    if not 0 <= layer <= L - layers:
+        raise ValueError(f"layers {layer} .. {layer + layers - 1} of {L}")
+    return at, L, P, page
 
 
 def _table(table, dev):
     """Checked table [R, MP] -> (address, R, MP)."""
-    if table.dim() != 2:
+    shape = table.shape
+    if len(shape) != 2:
         raise ValueError("table must be [R, MP]")
-    return _at(table, _I32, "table", dev, table.shape), *table.shape
+    return _at(table, _I32, "table", dev, shape), shape[0], shape[1]
 
 
 def _rows_of(given, B, most, dev, name):
@@ -54,17 +62,25 @@ def spec_page_workspace_bytes(B, MP, P):
     return int(_lib.load().spec_page_workspace_bytes(int(B), int(MP), int(P)))
 
 
+_book_bytes = {}  # spec_page_workspace_bytes by its arguments
+
+
 def _book(table, held, refs, B, workspace):
     """Checked table, held and refs -> (device, sizes, addresses, workspace)."""
     dev = table.device
-    _need(table, _I32, "table", dev)
+    if not table.is_cuda:
+        _need(table, None, "table")
     at, N, MP = _table(table, dev)
     P = refs.numel()
     held_at, refs_at = _at(held, _I32, "held", dev, (N,)), _at(refs, _I32, "refs", dev, (P,))
-    if B > 65535:
-        raise ValueError(f"{B} sequences in a call")
-    ws = _ws(workspace, "pages", spec_page_workspace_bytes(B, MP, P), dev, 0)
-    return dev, (N, MP, P), (at, held_at, refs_at), ws
+    need = _book_bytes.get((B, MP, P))
+    if need is None:
+        if B > 65535:
+            raise ValueError(f"{B} sequences in a call")
+        if len(_book_bytes) >= 4096:  # whoever has ever new sizes
+            _book_bytes.clear()
+        need = _book_bytes[B, MP, P] = spec_page_workspace_bytes(B, MP, P)
+    return dev, (N, MP, P), (at, held_at, refs_at), _ws(workspace, "pages", need, dev, 0)
 
 
 @_streamed
@@ -119,30 +135,33 @@ def spec_page_copy(pool, pairs, n_pairs=None, err=None):
     """Copies whole pages of pool [L, 2, P, ...] (any contiguous tensor) by
     pairs [M, 2] (from, to; -1: none), the first n_pairs[0] of them.
     -> err [1]: pairs outside the pool."""
-    if pool.dim() < 4 or not pool.is_cuda or not pool.is_contiguous():
+    shape = pool.shape
+    if not pool.is_cuda or not pool.is_contiguous():
         _need(pool, None, "pool")
+    if len(shape) < 4:
         raise ValueError("pool must be [L, 2, P, ...]")
-    dev, (L, two, P) = pool.device, pool.shape[:3]
+    dev, L, two, P = pool.device, shape[0], shape[1], shape[2]
     if pairs.dim() != 2:
         raise ValueError("pairs must be [M, 2]")
     M = pairs.shape[0]
     pairs_at = _at(pairs, _I32, "pairs", dev, (M, 2))
     if err is None:
         err = torch.empty(1, dtype=_I32, device=dev)
-    size = pool[0, 0, 0].numel() * pool.element_size() if L * two * P else 0
-    _call(_lib.load().spec_page_copy, dev, pool.data_ptr(), L * two, P, size, pairs_at, M,
+    blocks = L * two * P
+    _call(_lib.load().spec_page_copy, dev, pool.data_ptr(), L * two, P, pool.nbytes // blocks if blocks else 0, pairs_at, M,
           _at(n_pairs, _I32, "n_pairs", dev, (1,)), _at(err, _I32, "err", dev, (1,)))
     return err
 
 
 def _rows16(t, name):
-    if t.dim() != 6 or t.shape[1] != 2:
+    shape = t.shape
+    if len(shape) != 6 or shape[1] != 2:
         raise ValueError(f"{name} must be [L, 2, N, H, S, D]")
     if not t.is_cuda or not t.is_contiguous():
         _need(t, None, name)
     if t.dtype not in _HALVES:
         raise ValueError(f"unsupported {name} dtype {t.dtype}: bf16 or fp16")
-    L, _, N, H, S, D = t.shape
+    L, _, N, H, S, D = shape
     return t.device, L, N, H, S, D
 
 
@@ -152,14 +171,14 @@ def spec_store_pages(src, pool, table, pos, count, layer=0, slot=None, idx=None,
     D] row idx[b] -> positions pos[b] + j of table row row[b], layers layer ..
     of pool.  -> flags [B]."""
     dev, L, N, H, S, D = _rows16(src, "src")
-    pool_at, Lp, P, page = _pool(pool, H, D, layer, L)
+    pool_at, Lp, P, page = _pool(pool, dev, H, D, layer, L)
     table_at, R, MP = _table(table, dev)
     B = pos.shape[0]
     rows = B,
     T = S if path is None else path.shape[1]
     pos_at = _at(pos, _I32, "pos", dev, rows)
     flags = _out(flags, rows, _I32, dev, "flags", pos)
-    _call(_lib.load().spec_store_pages, dev, src.data_ptr(), _DT[src.dtype], L, N, H, S, D, _on(pool_at, pool, dev), Lp, P,
+    _call(_lib.load().spec_store_pages, dev, src.data_ptr(), _DT[src.dtype], L, N, H, S, D, pool_at, Lp, P,
           page, layer, table_at, R, MP, B, T, pos_at, _at(count, _I32, "count", dev, rows),
           _at(slot, _I32, "slot", dev, rows), _rows_of(idx, B, N, dev, "idx"), _rows_of(row, B, R, dev, "row"),
           _at(path, _I32, "path", dev, (B, T)), flags.data_ptr())
@@ -171,23 +190,17 @@ def spec_load_pages(pool, dst, table, pos, count, layer=0, slot=None, idx=None, 
     """Positions pos[b] + j, j < count[b], of table row row[b] -> rows slot[b] +
     j of dst [L, 2, N, H, S, D] row idx[b].  -> flags [B]."""
     dev, L, N, H, S, D = _rows16(dst, "dst")
-    pool_at, Lp, P, page = _pool(pool, H, D, layer, L)
+    pool_at, Lp, P, page = _pool(pool, dev, H, D, layer, L)
     table_at, R, MP = _table(table, dev)
     B = pos.shape[0]
     rows = B,
     pos_at = _at(pos, _I32, "pos", dev, rows)
     flags = _out(flags, rows, _I32, dev, "flags", pos)
-    _call(_lib.load().spec_load_pages, dev, _on(pool_at, pool, dev), Lp, P, page, layer, dst.data_ptr(), _DT[dst.dtype], L, N,
+    _call(_lib.load().spec_load_pages, dev, pool_at, Lp, P, page, layer, dst.data_ptr(), _DT[dst.dtype], L, N,
           H, S, D, table_at, R, MP, B, S, pos_at, _at(count, _I32, "count", dev, rows),
           _at(slot, _I32, "slot", dev, rows), _rows_of(idx, B, N, dev, "idx"), _rows_of(row, B, R, dev, "row"),
           flags.data_ptr())
     return flags
-
-
-def _on(at, t, dev):
-    if t.device != dev:
-        _need(t, None, "pool", dev)
-    return at
 
 
 _attend_bytes = {}  # spec_attend_pages_workspace_bytes by its arguments
@@ -199,7 +212,7 @@ def spec_attend_pages_workspace_bytes(T, Hq, H, D):
 
 @_streamed
 def spec_attend_pages(q, pool, layer, table, length, staged, tree_mask=None, n_nodes=None, idx=None, scale=None,
-                         out=None, flags=None, workspace=None):
+                      out=None, flags=None, workspace=None):
     """Attention of a round's queries q [B, T, Hq, D] over the prefix in pages
     (positions 0 .. length - 2 of table row idx[b]; None: b) and the nodes in
     staged [L, 2, B, H, T, D] that each may see.  -> (out [B, T, Hq, D], flags [B])."""
@@ -212,7 +225,7 @@ def spec_attend_pages(q, pool, layer, table, length, staged, tree_mask=None, n_n
         _need(q, None, "q")
     if dt not in _HALVES:
         raise ValueError(f"unsupported q dtype {dt}: bf16 or fp16")
-    pool_at, L, P, page = _pool(pool, H, D, layer, 1)
+    pool_at, L, P, page = _pool(pool, dev, H, D, layer, 1)
     table_at, R, MP = _table(table, dev)
     rows = B,
     length_at = _at(length, _I32, "length", dev, rows)
@@ -223,7 +236,7 @@ def spec_attend_pages(q, pool, layer, table, length, staged, tree_mask=None, n_n
     if need is None:
         need = _attend_bytes[T, Hq, H, D] = lib.spec_attend_pages_workspace_bytes(T, Hq, H, D)
     ws = _ws(workspace, "attend", need, dev, ATTEND_ZERO)
-    _call(lib.spec_attend_pages, dev, q.data_ptr(), _DT[dt], B, T, Hq, _on(pool_at, pool, dev), L, P, H, page, D, layer,
+    _call(lib.spec_attend_pages, dev, q.data_ptr(), _DT[dt], B, T, Hq, pool_at, L, P, H, page, D, layer,
           table_at, R, MP, length_at, _rows_of(idx, B, R, dev, "idx"), _at(n_nodes, _I32, "n_nodes", dev, rows),
           _at(tree_mask, torch.int64, "tree_mask", dev, (B, T)), _at(staged, dt, "staged", dev, (L, 2, B, H, T, D)),
           D ** -0.5 if scale is None else scale, out.data_ptr(), flags.data_ptr(), ws.data_ptr(), ws.numel())
