@@ -59,7 +59,19 @@ struct Q4Shared {
 
 // among the warps that compute
 __device__ __forceinline__ void q4_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-static_assert(32 * kQ4Warps == 128, "q4_sync");
+// ... and whether all of them say so.  They go on to a unit together or not at
+// all: after a wait that gave up, one that left alone would be waited for above.
+__device__ __forceinline__ bool q4_all(bool yes)
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.and.pred q, 2, 128, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)yes)
+                 : "memory");
+    return r != 0;
+}
+static_assert(32 * kQ4Warps == 128, "q4_sync, q4_all");
 static_assert(3 * kAttendCtas <= kGaveUpWord, "one counter per CTA");
 
 template <typename T>
@@ -515,7 +527,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NQ>::kCtas) attend_q4_k
         const int g = lane >> 2, t = lane & 3;
         uint32_t it = 0;  // tiles through the ring
         bool ok = !a.starve || __all_sync(0xFFFFFFFFu, wait_phase(&s.never, 0, &s.abort, limit));
-        for (uint32_t n = 0; units_wait(s.units, n, &s.abort, limit); ++n) {
+        for (uint32_t n = 0; q4_all(units_wait(s.units, n, &s.abort, limit)); ++n) {
             const PagedUnit &u = *units_at(s.units, n);  // read as it is wanted: registers are short
             Q4State<D, NQ> st;
 #pragma unroll
