@@ -448,7 +448,9 @@ SPEC_API int spec_tree_plan(int B, int T, const int32_t *parent, const int32_t *
  * q_out [B, T, Hq, D] gets the queries.  Keys and values go to `staged`
  * [L, 2, B, H, T, D] at node i, or with staged NULL to cache slot
  * pad + len - 1 + i.  Flagged: len < 1, pad < 0, a slot past S, an index
- * outside [0, N); and, where the cache is written, a repeated index.
+ * outside [0, N); and, where the cache is written, a repeated index.  With a
+ * staged block kv may be NULL (the prefix is in pages): N and S are then the
+ * pages' table rows and the most tokens that one may have.
  * qkv, q_out and the layer or staged block written must not overlap.
  */
 SPEC_API int spec_append_round(const void *qkv, spec_dtype dt, int B, int T, int Hq, void *kv, int L, int N, int H,

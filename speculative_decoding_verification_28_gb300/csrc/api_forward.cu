@@ -159,7 +159,8 @@ int spec_append_round(const void *qkv, spec_dtype dt, int B, int T, int Hq, void
         return rc;
     const Append p = {qkv, dt, Hq, q_weight, k_weight, eps, inv_freq, R, interleaved != 0, q_out};
     const int e = dtype_bytes(dt);
-    rc = check_append(p, kv, H, D, (long long)B * T, layer_span(kv, N, H, S, D, layer, e),
+    // keys and values that go to the staged block need no cache
+    rc = check_append(p, kv ? kv : staged, H, D, (long long)B * T, layer_span(kv, N, H, S, D, layer, e),
                       layer_span(staged, B, H, T, D, layer, e));
     if (rc != SPEC_OK)
         return rc;

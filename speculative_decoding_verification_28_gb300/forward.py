@@ -109,13 +109,13 @@ def _ws(given, kind, nbytes, device, head):
     return buf
 
 
-def _cache(kv, layer):
+def _cache(kv, layer, name="kv"):
     if kv.dim() != 6 or kv.shape[1] != 2:
-        raise ValueError("kv must be [L, 2, N, H, S, D]")
+        raise ValueError(f"{name} must be [L, 2, N, H, S, D]")
     if not kv.is_cuda or not kv.is_contiguous():
-        _need(kv, None, "kv")
+        _need(kv, None, name)
     if kv.dtype not in _DT:
-        raise ValueError(f"unsupported kv dtype {kv.dtype}")
+        raise ValueError(f"unsupported {name} dtype {kv.dtype}")
     L, _, N, H, S, D = kv.shape
     if not 0 <= layer < L:
         raise ValueError(f"layer {layer} of {L}")
@@ -147,8 +147,8 @@ def spec_tree_plan(parent, n_nodes=None, mask=None, depth=None, flags=None):
     return mask, depth, flags
 
 
-def _append_common(qkv, kv, layer, inv_freq, q_weight, k_weight, lead):
-    dev, L, N, H, S, D = _cache(kv, layer)
+def _append_common(qkv, kv, layer, inv_freq, q_weight, k_weight, lead, name="kv"):
+    dev, L, N, H, S, D = _cache(kv, layer, name)
     dt = kv.dtype
     shape = qkv.shape
     if len(shape) != lead + 2 or shape[-1] != D or shape[-2] <= 2 * H:
@@ -168,15 +168,20 @@ def spec_append_round(qkv, kv, layer, length, pad, inv_freq, q_weight=None, k_we
                       interleaved=False, depth=None, n_nodes=None, idx=None, staged=None, q_out=None, flags=None):
     """qkv [B, T, Hq + 2H, D] of a round's nodes: per-head RMS norm of queries
     and keys, rotation, keys and values to the cache kv [L, 2, N, H, S, D] (or
-    to staged [L, 2, B, H, T, D]).  pad None: 0.
+    to staged [L, 2, B, H, T, D], where kv may be None: a prefix in pages, whose
+    rows idx names).  pad None: 0.
     -> (q_out [B, T, Hq, D], flags [B] int32)."""
-    dev, dt, (L, N, H, S, D), Hq, x, qw, kw, inv, R = _append_common(qkv, kv, layer, inv_freq, q_weight, k_weight, 2)
+    paged = kv is None and staged is not None
+    at, name = (staged, "staged") if paged else (kv, "kv")
+    dev, dt, (L, N, H, S, D), Hq, x, qw, kw, inv, R = _append_common(qkv, at, layer, inv_freq, q_weight, k_weight, 2, name)
     B, T = qkv.shape[:2]
+    if paged:  # the table's rows and lengths, which this call does not see: what it may count
+        N, S = (2 ** 30 - 1) // H, 2 ** 31 - 257
     rows = B,
     length_at = _at(length, _I32, "length", dev, rows)
     q_out = _out(q_out, (B, T, Hq, D), dt, dev, "q_out")
     flags = _out(flags, rows, _I32, dev, "flags", length)
-    _call(_lib.load().spec_append_round, dev, x, _DT[dt], B, T, Hq, kv.data_ptr(), L, N, H, S, D, layer,
+    _call(_lib.load().spec_append_round, dev, x, _DT[dt], B, T, Hq, None if paged else kv.data_ptr(), L, N, H, S, D, layer,
           length_at, _at(pad, _I32, "pad", dev, rows), _rows(idx, B, N, dev),
           _at(n_nodes, _I32, "n_nodes", dev, rows), _at(depth, _I32, "depth", dev, (B, T)),
           _at(staged, dt, "staged", dev, (L, 2, B, H, T, D)), qw, kw, eps, inv, R, 1 if interleaved else 0,

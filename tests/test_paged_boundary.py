@@ -161,3 +161,15 @@ def test_host_tensors_are_refused():
     for call in calls:
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_nodes_without_a_cache(lib):
+    from test_forward_boundary import ODD as odd
+    from test_forward_boundary import ST, append_round
+
+    # the checks of the cache are the staged block's then
+    assert append_round(lib, kv=None) == -1
+    for kw in (dict(q=None), dict(N=1), dict(S=0), dict(qkv=ST), dict(q=ST)):
+        assert append_round(lib, kv=None, staged=ST, **kw) == -1, kw
+    assert append_round(lib, kv=None, staged=odd) == -5
+    assert append_round(lib, kv=None, staged=ST, B=0) == 0
