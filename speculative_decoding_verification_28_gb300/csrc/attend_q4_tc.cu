@@ -50,8 +50,8 @@ struct QtShape {
     static constexpr int kCodes = kKeys * q4_codes(D), kScales = kKeys * q4_scales(D);
     static constexpr int kStage = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales
     static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kJoinStride = D / 2 + 4;           // floats of a row of O's half in the copies' join
-    static constexpr int kJoin = 2 * 64 * kJoinStride * 4;  // bytes
+    static constexpr int kJoinStride = D / 4 + 4;               // floats of a row of O's quarter in the copies' join
+    static constexpr int kJoin = 2 * 2 * 64 * kJoinStride * 4;  // bytes
     // two expanded tiles of keys, and of values
     static constexpr int kSmem = 4 * kTile + kStages * kStage + kJoin + 1024;
 };
@@ -71,6 +71,19 @@ struct QtShared {
     float m[kQtLanes], l[2][kQtLanes];
     int odd[kUnitRing][kQtExpand];      // whether a value of the nodes is not finite
 };
+
+// whether a phase has ended, at once
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(smem_addr(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
 
 // A part's tiles in the order in which they are taken: the last, the nodes', first.
 __device__ __forceinline__ Tile qt_tile(const PagedUnit &u, int tile)
@@ -186,10 +199,11 @@ __device__ __forceinline__ void qt_queries(const AttendArgs &a, const PagedUnit 
 }
 
 // Columns in the order of the expanded words -> as they are.
-__device__ __forceinline__ void in_order32(uint32_t *o)
+template <int W>
+__device__ __forceinline__ void put_in_order(uint32_t *o)
 {
 #pragma unroll
-    for (int w = 0; w < 32; w += 8) {
+    for (int w = 0; w < W; w += 8) {
         const uint32_t x[8] = {o[w], o[w + 2], o[w + 4], o[w + 6], o[w + 1], o[w + 3], o[w + 5], o[w + 7]};
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -197,16 +211,46 @@ __device__ __forceinline__ void in_order32(uint32_t *o)
     }
 }
 
-// Adds what is not finite among the nodes' values to columns col .. col + 31
+// W columns of a row's half of O
+template <int W>
+__device__ __forceinline__ void load_row(uint32_t addr, uint32_t *o)
+{
+    if constexpr (W == 32) {
+        tc_load(addr, o);
+    } else {
+        tc_ld16(addr, o);
+        tc_wait_ld();
+        tc_pin<16>(o);
+    }
+}
+// ... times f, rounded, to dst
+template <typename T, int W>
+__device__ __forceinline__ void store_row(T *dst, const uint32_t *o, float f)
+{
+    if constexpr (W == 32) {
+        store_row32<T>(dst, o, f);
+    } else {
+#pragma unroll
+        for (int e = 0; e < W; e += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = TcType<T>::pack(__uint_as_float(o[e + 2 * i]) * f, __uint_as_float(o[e + 2 * i + 1]) * f);
+            *reinterpret_cast<uint4 *>(dst + e) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// Adds what is not finite among the nodes' values to columns col .. col + W - 1
 // of a row that sees it; its weights are positive, so that it stays as it is.
-template <typename T, int D>
-__device__ __noinline__ void qt_put_back32(const AttendArgs &a, const PagedUnit &u, int row, int col, uint32_t *o)
+template <typename T, int D, int W>
+__device__ __noinline__ void qt_put_back(const AttendArgs &a, const PagedUnit &u, int row, int col, uint32_t *o)
 {
     const T *values = reinterpret_cast<const T *>(a.staged) + (a.st_v + (long long)u.b * a.cache.H + u.h) * a.seq.T * D;
     const uint64_t bits = row_nodes(a, u, row);
     for (int key = 0; key < u.n; ++key)
         if (bits >> key & 1)
-            for (int e = 0; e < 32; ++e) {
+            for (int e = 0; e < W; ++e) {
                 const float f = Storage<T>::at(values + (size_t)key * D, col + e);
                 if (!(fabsf(f) <= 3.4e38f))
                     o[e] = __float_as_uint(__uint_as_float(o[e]) + f);
@@ -320,7 +364,8 @@ __global__ void __launch_bounds__(kQtThreads, 1) attend_q4_tc_kernel(const __gri
         bool have = get(0, w);
         int wt = w.tile_end - 1;
         bool ok = true;
-        auto ready = [&](uint64_t *bar, uint32_t parity) -> bool { return __all_sync(0xFFFFFFFFu, mbar_poll(bar, parity)); };
+        // (a try_wait would sleep on one barrier while the other's phase ends: 349 us for 256 chains, against 343)
+        auto ready = [&](uint64_t *bar, uint32_t parity) -> bool { return __all_sync(0xFFFFFFFFu, mbar_test(bar, parity)); };
         auto score_next = [&]() {
             const int b = is & 1;
             const Tile tl = qt_tile(w, wt);
@@ -593,21 +638,24 @@ __global__ void __launch_bounds__(kQtThreads, 1) attend_q4_tc_kernel(const __gri
                     m = top;
                     f *= f0;
                 }
-                float *mine = join_p + (side * 64 + r) * Sh::kJoinStride;
+                // Each copy puts out half of this side's columns and gives the other half away.
+                constexpr int kOut = D / 2 / COPIES;
+                const int out0 = copy * kOut;
+                const float *theirs = join_p + ((side * 2 + copy) * 64 + r) * Sh::kJoinStride;
                 if (COPIES == 2) {
-                    if (copy == 1)
+                    float *mine = join_p + ((side * 2 + (copy ^ 1)) * 64 + r) * Sh::kJoinStride;
 #pragma unroll 1
-                        for (int k = 0; k < D / 2; k += 16) {
-                            uint32_t o[16];
-                            tc_ld16(tm_o + k, o);
-                            tc_wait_ld();
-                            tc_pin<16>(o);
+                    for (int k = 0; k < kOut; k += 16) {
+                        uint32_t o[16];
+                        tc_ld16(tm_o + (out0 ^ kOut) + k, o);
+                        tc_wait_ld();
+                        tc_pin<16>(o);
 #pragma unroll
-                            for (int e = 0; e < 16; e += 4)
-                                *reinterpret_cast<float4 *>(mine + k + e) =
-                                    make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f,
-                                                __uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
-                        }
+                        for (int e = 0; e < 16; e += 4)
+                            *reinterpret_cast<float4 *>(mine + k + e) =
+                                make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f,
+                                            __uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
+                    }
                     ok = meet(&s.copies[quad & 1], meets);
                     if (!ok)
                         break;
@@ -618,45 +666,46 @@ __global__ void __launch_bounds__(kQtThreads, 1) attend_q4_tc_kernel(const __gri
                     for (int k = 0; k < kQtExpand; ++k)
                         any_odd |= *reinterpret_cast<const volatile int *>(&s.odd[n % kUnitRing][k]) != 0;
                 const float inv = !whole ? 1.0f : l > 0.0f || l != l ? 1.0f / l : 0.0f;
-                T *dst = real ? reinterpret_cast<T *>(a.out) + row_place(a, u, r) + side * (D / 2) : nullptr;
-                if (copy == 0)
+                constexpr int W = kOut < 32 ? kOut : 32;
+                const int d0 = side * (D / 2) + out0;
+                T *dst = real ? reinterpret_cast<T *>(a.out) + row_place(a, u, r) + d0 : nullptr;
 #pragma unroll 1
-                    for (int k = 0; k < D / 2; k += 32) {
-                        uint32_t o[32];
-                        tc_load(tm_o + k, o);
+                for (int k = 0; k < kOut; k += W) {
+                    uint32_t o[W];
+                    load_row<W>(tm_o + out0 + k, o);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            float4 y = make_float4(0, 0, 0, 0);
-                            if (COPIES == 2)
-                                y = *reinterpret_cast<const float4 *>(mine + k + e);
-                            o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), f, y.x));
-                            o[e + 1] = __float_as_uint(fmaf(__uint_as_float(o[e + 1]), f, y.y));
-                            o[e + 2] = __float_as_uint(fmaf(__uint_as_float(o[e + 2]), f, y.z));
-                            o[e + 3] = __float_as_uint(fmaf(__uint_as_float(o[e + 3]), f, y.w));
-                        }
-                        in_order32(o);
-                        if (any_odd && real) {
-                            uint32_t y[32];  // rare; the call keeps only these copies in memory
-                            const PagedUnit v = u;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                y[e] = o[e];
-                            qt_put_back32<T, D>(a, v, r, side * (D / 2) + k, y);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = y[e];
-                        }
-                        if (!real)
-                            continue;
-                        if (whole) {
-                            store_row32<T>(dst + k, o, inv);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4)
-                                __stcg(reinterpret_cast<uint4 *>(slot + part_quad<kRows>((side * (D / 2) + k + e) / 4, r)),
-                                       make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
-                        }
+                    for (int e = 0; e < W; e += 4) {
+                        float4 y = make_float4(0, 0, 0, 0);
+                        if (COPIES == 2)
+                            y = *reinterpret_cast<const float4 *>(theirs + k + e);
+                        o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), f, y.x));
+                        o[e + 1] = __float_as_uint(fmaf(__uint_as_float(o[e + 1]), f, y.y));
+                        o[e + 2] = __float_as_uint(fmaf(__uint_as_float(o[e + 2]), f, y.z));
+                        o[e + 3] = __float_as_uint(fmaf(__uint_as_float(o[e + 3]), f, y.w));
                     }
+                    put_in_order<W>(o);
+                    if (any_odd && real) {
+                        uint32_t y[W];  // rare; the call keeps only these copies in memory
+                        const PagedUnit v = u;
+#pragma unroll
+                        for (int e = 0; e < W; ++e)
+                            y[e] = o[e];
+                        qt_put_back<T, D, W>(a, v, r, d0 + k, y);
+#pragma unroll
+                        for (int e = 0; e < W; ++e)
+                            o[e] = y[e];
+                    }
+                    if (!real)
+                        continue;
+                    if (whole) {
+                        store_row<T, W>(dst + k, o, inv);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < W; e += 4)
+                            __stcg(reinterpret_cast<uint4 *>(slot + part_quad<kRows>((d0 + k + e) / 4, r)),
+                                   make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+                    }
+                }
                 if (real && !whole && side == 0 && copy == 0) {
                     __stcg(slot + (size_t)kRows * D + r, m);
                     __stcg(slot + (size_t)kRows * D + kRows + r, l);
