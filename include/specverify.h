@@ -616,8 +616,8 @@ SPEC_API int spec_page_fork(int32_t *table, int32_t *held, int32_t *refs, int N,
  * page also holds tokens before first[b], copies[b] is the pair (old, new) that
  * spec_page_copy has to copy before anything is written, else (-1, -1).  The
  * lowest free pages are taken, by sequences in order, by places in order within
- * one.  Where there are too few, missing[0] says by how many; then pages have
- * been let go, but no row has got any, and what is held is that.  Else it is 0.
+ * one.  Where there are too few, missing[0] says by how many (2^29 wanted pages
+ * at most are counted); then pages have been let go, but no row has got any, and what is held is that.  Else it is 0.
  * Flagged, and left as it is: a row outside [0, N) or repeated, first < 0,
  * total < 0 or of more than MP pages, entries outside the pool.
  */

@@ -6,6 +6,8 @@
 // makes "the lowest free page first" a prefix sum and every result independent
 // of the order in which threads run.  Only sums into refs are atomic, and
 // those commute.  The copies are bound by HBM.
+#include <limits.h>
+
 #include "paged.h"
 #include "spec_common.cuh"
 
@@ -102,16 +104,19 @@ cudaError_t launch_page_fork(const ForkArgs &a, cudaStream_t st)
 // walking the pool in order
 // ---------------------------------------------------------------------------
 // exclusive prefix of v over the block and its total; `s`: a word per warp.
-// Every thread calls; barriers on both sides.
+// Every thread calls; barriers on both sides.  MOST: where sums stop, for values
+// up to it (what lies behind one that stopped is then no prefix any more).
+template <int MOST = INT_MAX>
 __device__ __forceinline__ int block_before(int v, int *s, int *total)
 {
+    static_assert(MOST == INT_MAX || MOST <= INT_MAX / 2, "two sums in 31 bits");
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     int x = v;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
         const int o = __shfl_up_sync(0xFFFFFFFFu, x, m);
         if (lane >= m)
-            x += o;
+            x = min(x + o, MOST);
     }
     __syncthreads();
     if (lane == 31)
@@ -122,7 +127,7 @@ __device__ __forceinline__ int block_before(int v, int *s, int *total)
     for (int m = 1; m < 32; m <<= 1) {
         const int o = __shfl_up_sync(0xFFFFFFFFu, y, m);
         if (lane >= m)
-            y += o;
+            y = min(y + o, MOST);
     }
     *total = __shfl_sync(0xFFFFFFFFu, y, 31);
     const int warps = __shfl_sync(0xFFFFFFFFu, y, w) - s[w];
@@ -149,6 +154,7 @@ __device__ __forceinline__ uint32_t page_bits(const PagesArgs &p, int p0)
 // ---------------------------------------------------------------------------
 // reserve
 // ---------------------------------------------------------------------------
+constexpr int kMostWishes = 1 << 29;  // that are counted
 constexpr int kWishes = 1024;     // sequences whose wishes fit in shared memory
 constexpr int kWishLanes = 8;     // threads of a sequence
 
@@ -261,12 +267,10 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(const ReserveArgs
     for (int c = 0; c < p.B; c += kBookThreads) {
         const int b = c + tid, v = b < p.B ? w.at[b] : 0;
         int sum;
-        const int before = block_before(v, s_words, &sum);
+        const int before = block_before<kMostWishes>(v, s_words, &sum);
         if (b < p.B)
             w.at[b] = total + before;
-        total += sum;
-        if (total > p.P)
-            total = p.P + 1;  // more than there can be: enough to know
+        total = min(total + sum, kMostWishes);  // far more than there can be
     }
     // the lowest free pages
     int found = 0;
@@ -290,7 +294,7 @@ __global__ void __launch_bounds__(kBookThreads) reserve_kernel(const ReserveArgs
             continue;
         const int row = w.row[b], hi = w.hi[b], n = w.n[b], first = a.first[b];
         int at = w.at[b];
-        for (int c = w.lo[b]; c < n; c += kWishLanes) {
+        for (int c = w.lo[b]; c < (enough ? n : hi); c += kWishLanes) {
             const int i = c + k;
             int32_t *e = p.table + (size_t)row * p.MP + (i < n ? i : 0);
             const int old = i < hi ? *e : 0;

@@ -235,3 +235,22 @@ def test_a_captured_round_and_other_streams():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(held, expect)) and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("N,MP,P,want", [(3, 40, 9, 25), (40, 300, 33, 300), (2000, 70, 100, 70)])
+def test_more_wanted_than_the_pool_has(N, MP, P, want):
+    """missing is by how many, also where more are wanted than there are pages; nobody got any."""
+    b = Both(N, MP, P, 16)
+    b.reserve([0], [5 * 16], [1])
+    b.reserve([0] * N, [want * 16] * N)
+    b.reserve([3 * 16, 0], [4 * 16, min(P - 4, MP) * 16], [1, 0])  # and what is left can be had
+
+
+def test_more_wanted_than_31_bits_count():
+    """128 sequences want 2^24 pages each, 2^31 in all: sums stop at 2^29, and nothing is handed out."""
+    N, MP, P = 128, 1 << 24, 50
+    table = torch.full((N, MP), -1, dtype=torch.int32, device="cuda")
+    held, refs = i32(np.zeros(N)), i32(np.zeros(P))
+    copies, missing, f = sv.spec_page_reserve(table, held, refs, i32(np.zeros(N)), i32(np.full(N, 1 << 28)), 16)
+    assert int(missing) == (1 << 29) - P and not f.any() and (copies == -1).all()
+    assert (table == -1).all() and not held.any() and not refs.any()
