@@ -238,8 +238,9 @@ int spec_attend_pages(const void *q, spec_dtype dt, int B, int T, int Hq, const 
     if (!q || !pool || !table || !len || !staged || !out || (!idx && B > R) || !(scale > 0.0f) ||
         !isfinite(scale * 1.44269504088896340736f) || (long long)B * T * Hq > INT_MAX)
         return SPEC_EINVAL;
-    // tiles of 64 keys for 8 query rows each: the kernels count them in 31 bits
-    const long long groups = ((long long)T * (Hq / H) + 7) / 8, tiles = ((long long)MP * page + 63) / 64 + 1;
+    // tiles of 64 keys for 8 query rows each, and eight more a unit for its start and end: the
+    // kernels count them in 31 bits
+    const long long groups = ((long long)T * (Hq / H) + 7) / 8, tiles = ((long long)MP * page + 63) / 64 + 1 + 8;
     if ((double)B * H * groups * tiles > (double)INT_MAX)
         return SPEC_EINVAL;
     const Span to = span(out, 0, (double)B * T * Hq * D, 2);

@@ -175,7 +175,7 @@ def spec_store_pages(src, pool, table, pos, count, layer=0, slot=None, idx=None,
     table_at, R, MP = _table(table, dev)
     B = pos.shape[0]
     rows = B,
-    T = S if path is None else path.shape[1]
+    T = S if path is None else path.shape[-1]
     pos_at = _at(pos, _I32, "pos", dev, rows)
     flags = _out(flags, rows, _I32, dev, "flags", pos)
     _call(_lib.load().spec_store_pages, dev, src.data_ptr(), _DT[src.dtype], L, N, H, S, D, pool_at, Lp, P,

@@ -173,3 +173,10 @@ def test_nodes_without_a_cache(lib):
         assert append_round(lib, kv=None, staged=ST, **kw) == -1, kw
     assert append_round(lib, kv=None, staged=odd) == -5
     assert append_round(lib, kv=None, staged=ST, B=0) == 0
+
+
+def test_units_are_counted_with_their_starts(lib):
+    # 288 million units of two tiles: ten tiles each are counted
+    far = dict(q=at(1 << 44), out=at(1 << 45), staged=at(1 << 46))
+    assert attend(lib, B=60000, R=60000, H=4800, Hq=4800, T=1, MP=1, page=16, L=1, layer=0, **far) == -1
+    assert attend(lib, B=60000, R=60000, H=1200, Hq=1200, T=1, MP=1, page=16, L=1, layer=0, wsb=16, **far) == -3
