@@ -302,3 +302,38 @@ def test_a_wait_that_gives_up_is_reported():
     ws[:sv.ATTEND_ZERO].zero_()
     o, flags = run(c, workspace=ws)
     assert not flags.any() and torch.equal(o, good)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("T,G,D", [(3, 2, 64), (4, 4, 128), (7, 3, 64), (9, 7, 128), (9, 8, 64), (20, 7, 128)])
+def test_values_that_are_not_finite_in_every_form(dt, T, G, D):
+    """Rows that see a node whose value is not finite have it, the others what they would have without."""
+    c = make(19, dt, 3, T, G, 2, D, 16, [130, 1, 17], tree=True, full=True)
+    d = dict(c, staged=c["staged"].clone())
+    at = [(b, h, b + 1 if b + 1 < T else 0, d) for b, h, d in ((0, 1, D - 3), (1, 0, 0), (2, 1, D // 2 - 1), (0, 0, D // 4))]
+    for k, (b, h, node, dim) in enumerate(at):
+        d["staged"][1, 1, b, h, node, dim] = (float("inf"), NAN, -float("inf"), float("inf"))[k]
+    plain = dict(d, staged=d["staged"].nan_to_num(0.0, 0.0, 0.0))
+    want, tol = ref.attend(plain["q"], plain["pool"], 1, plain["table"], plain["length"], plain["staged"], c["mask"], c["n"])
+    o = run(d)[0].cpu().double()
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    for b, h, node, dim in at:
+        for i in range(T):
+            hit[b, i, h * G:(h + 1) * G, dim] = bool(int(c["mask"][b, i]) >> node & 1)
+    assert torch.equal(torch.isfinite(o), ~hit)
+    assert float(((o - want).abs() - tol)[~hit].max()) <= 0
+
+
+@pytest.mark.parametrize("T,G,D", [(4, 4, 128), (9, 4, 64), (20, 5, 128)])
+def test_a_wait_that_gives_up_in_every_form(T, G, D):
+    """Sequences whose units are cut over many CTAs; the call after it on a clean workspace is as if nothing had been."""
+    from speculative_decoding_verification_28_gb300 import _lib
+
+    c = make(21, "f16", 5, T, G, 2, D, 64, [1500, 17, 64, 3000, 1])
+    ws = torch.zeros(sv.spec_attend_pages_workspace_bytes(T, 2 * G, 2, D), dtype=torch.uint8, device="cuda")
+    good = run(c, workspace=ws)[0]
+    assert _lib.load().spec_attend_starve_next(100000) == 0
+    assert (run(c, workspace=ws)[1] & sv.FLAG_TIMEOUT).all()
+    ws[:sv.ATTEND_ZERO].zero_()
+    o, flags = run(c, workspace=ws)
+    assert not flags.any() and torch.equal(o, good)

@@ -254,3 +254,14 @@ def test_more_wanted_than_31_bits_count():
     copies, missing, f = sv.spec_page_reserve(table, held, refs, i32(np.zeros(N)), i32(np.full(N, 1 << 28)), 16)
     assert int(missing) == (1 << 29) - P and not f.any() and (copies == -1).all()
     assert (table == -1).all() and not held.any() and not refs.any()
+
+
+def test_pages_copied_past_32_bits():
+    """The ends of slabs of 5 GB."""
+    P, page = 150000, 34816
+    pool = torch.zeros((2, 1, P, page), dtype=torch.uint8, device="cuda")
+    pool[:, :, 3] = torch.arange(page, device="cuda").to(torch.uint8)
+    pool[1, 0, 3, 7] = 99
+    assert int(sv.spec_page_copy(pool, i32([[3, P - 1], [-1, -1], [P - 2, 0]]))) == 0
+    assert torch.equal(pool[:, :, P - 1], pool[:, :, 3]) and int(pool[1, 0, P - 1, 7]) == 99
+    assert int(pool[0, 0, 4:P - 1].max()) == 0
