@@ -17,6 +17,9 @@
 // exceeds it by more than 2^4 (tcgen.cuh says why).  The nodes' tile is in the
 // staged type on both sides, weights too.
 //
+// What it takes: decoding over 70000 keys (6 sequences, 64 / 8 heads of 128) 106 us, HBM's floor
+// 68.  1190 instructions a tile of 64 keys, half of them to expand, at half of the issue slots.
+//
 // A CTA: four warps, each with its own running statistics and every fourth of the
 // unit's tiles of 64 keys, joined in shared memory at the unit's end; a fifth walks
 // over the units and copies pages' codes and scales (cp.async.bulk) through a ring.
@@ -479,6 +482,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NQ>::kCtas) attend_q4_k
     Q4Shared<D, NQ> &s = *reinterpret_cast<Q4Shared<D, NQ> *>(base);
     const AttendArgs &a = x.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // a unit's start and end cost about eight tiles (128 sequences 97 us; counted as none 117)
     const Shape sh{kQ4Keys, Sh::kRows, a.G, 8};
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
@@ -723,6 +727,10 @@ cudaError_t launch_q4(const AttendQ4Args &a, cudaStream_t st)
 template <typename T, int D>
 cudaError_t launch_q4_d(const AttendQ4Args &a, cudaStream_t st)
 {
+    // Query rows of a key head decide.  Measured on both sides (500 .. 4000 keys, 8 key heads of 128, us):
+    //   1 .. 8 rows   one query tile here 97 (128 sequences of 4 rows), two 153, tcgen05 180
+    //   9 .. 16       two tiles 91 (64 of 12), one (two units) 96, tcgen05 99; heads of 64 (16 rows) 58, 67, 83
+    //   17 and more   tcgen05 101 (64 of 20), units of 16 rows here 160
     const int rows = a.a.seq.T * a.a.G;
     if (rows > 16)
         return launch_attend_q4_tc(a, std::is_same<T, __half>::value ? SPEC_F16 : SPEC_BF16, st);

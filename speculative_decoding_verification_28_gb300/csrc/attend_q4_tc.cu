@@ -28,10 +28,15 @@
 // which one has the keys 0 .. 63 of every tile and the other the rest: four warps
 // would else be idle, and the softmax is the longest chain.  The two
 // are joined as parts of a unit are, in shared memory.
+//
+// What it takes: 256 chains of 9 over 256 .. 4000 keys, 32 / 8 heads of 128, 335 us (96 for
+// HBM, 41 of products): a tile of 128 keys 2500 clocks, of which the products of 128 lanes take 1000 and
+// shared memory's traffic (64 kB written expanded, 64 read by the products) as much. No pipe is full
+// (tensor 32%, ALU 46%, issue 55%): each warp's chain of dependent steps is, expansion first.
 #include <type_traits>
 
-#include "q4_expand.cuh"
 #include "paged_units.cuh"
+#include "q4_expand.cuh"
 
 namespace spec {
 
@@ -49,11 +54,17 @@ struct QtShape {
     static constexpr int kTile = kPanels * kPanel;  // bytes of an expanded tile
     static constexpr int kCodes = kKeys * q4_codes(D), kScales = kKeys * q4_scales(D);
     static constexpr int kStage = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales
-    static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kJoinStride = D / 4 + 4;               // floats of a row of O's quarter in the copies' join
-    static constexpr int kJoin = 2 * 2 * 64 * kJoinStride * 4;  // bytes
+};
+// COPIES: of a row, see above
+template <int D, int COPIES>
+struct QtLayout {
+    using Sh = QtShape<D>;
+    static constexpr int kStages = D == 64 ? 8 : COPIES == 2 ? 4 : 5;  // what fits (256 chains: 2 366 us, 3 340)
+    static constexpr int kOut = COPIES == 2 ? 16 : 32;                 // columns of O that a thread puts out at a time
+    static constexpr int kJoinStride = kOut + 4;                       // floats of a row of them in the copies' join
+    static constexpr int kJoin = COPIES == 2 ? 2 * 2 * 64 * kJoinStride * 4 : 0;  // bytes
     // two expanded tiles of keys, and of values
-    static constexpr int kSmem = 4 * kTile + kStages * kStage + kJoin + 1024;
+    static constexpr int kSmem = 4 * Sh::kTile + kStages * Sh::kStage + kJoin + 1024;
 };
 template <int STAGES>
 struct QtShared {
@@ -100,7 +111,7 @@ __device__ __forceinline__ int swizzled(int row, int chunk) { return row * 128 +
 
 // A tile's keys or values (KEYS), expanded by one warp of kQtExpand, in a short
 // loop: every role's code competes for the instruction cache (unrolled four times
-// 560 us for 256 chains, against 437).
+// 369 us for 256 chains and 140 for 32 trees of 64, against 340 and 114).
 template <typename T, int D, bool KEYS>
 __device__ __forceinline__ void qt_expand(const unsigned char *stage, unsigned char *to, int warp, int valid)
 {
@@ -261,7 +272,8 @@ template <typename T, int D, int COPIES>
 __global__ void __launch_bounds__(kQtThreads, 1) attend_q4_tc_kernel(const __grid_constant__ AttendQ4Args x)
 {
     using Sh = QtShape<D>;
-    constexpr int ST = Sh::kStages;
+    using Lay = QtLayout<D, COPIES>;
+    constexpr int ST = Lay::kStages;
     extern __shared__ unsigned char dyn[];
     __shared__ QtShared<ST> s;
     unsigned char *base = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
@@ -270,6 +282,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) attend_q4_tc_kernel(const __gri
     const AttendArgs &a = x.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int kRows = kQtLanes / COPIES;  // of a unit
+    // a unit's start and end cost about two tiles (256 chains 340 us; counted as none 377, one 355, four 348)
     const Shape sh{kKeys, kRows, a.G, 2};
     constexpr int kMmaWarp = kQtSoftmax, kLoadWarp = kMmaWarp + 1, kFirstExpand = kMmaWarp + 4;
     constexpr bool kHalf = std::is_same<T, __half>::value;
@@ -323,7 +336,8 @@ __global__ void __launch_bounds__(kQtThreads, 1) attend_q4_tc_kernel(const __gri
     PagedUnit u;
 
     // 640 threads launch with 96 registers each (61440); the softmax keeps 120, the
-    // others 80 (256 * 120 + 384 * 80 = 61440; with 136, 64 and 72 440 us for 256 chains, 407)
+    // others 80 (256 * 120 + 384 * 80 = 61440; 256 chains 340 us, with 104 and 88 350, with 136
+    // and 64 for the expansion 365)
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
@@ -638,46 +652,41 @@ __global__ void __launch_bounds__(kQtThreads, 1) attend_q4_tc_kernel(const __gri
                     m = top;
                     f *= f0;
                 }
-                // Each copy puts out half of this side's columns and gives the other half away.
-                constexpr int kOut = D / 2 / COPIES;
-                const int out0 = copy * kOut;
-                const float *theirs = join_p + ((side * 2 + copy) * 64 + r) * Sh::kJoinStride;
-                if (COPIES == 2) {
-                    float *mine = join_p + ((side * 2 + (copy ^ 1)) * 64 + r) * Sh::kJoinStride;
-#pragma unroll 1
-                    for (int k = 0; k < kOut; k += 16) {
-                        uint32_t o[16];
-                        tc_ld16(tm_o + (out0 ^ kOut) + k, o);
-                        tc_wait_ld();
-                        tc_pin<16>(o);
-#pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            *reinterpret_cast<float4 *>(mine + k + e) =
-                                make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f,
-                                            __uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
-                    }
-                    ok = meet(&s.copies[quad & 1], meets);
-                    if (!ok)
-                        break;
-                }
                 bool any_odd = false;
                 if (u.tile_end == u.n_tiles)
 #pragma unroll
                     for (int k = 0; k < kQtExpand; ++k)
                         any_odd |= *reinterpret_cast<const volatile int *>(&s.odd[n % kUnitRing][k]) != 0;
                 const float inv = !whole ? 1.0f : l > 0.0f || l != l ? 1.0f / l : 0.0f;
-                constexpr int W = kOut < 32 ? kOut : 32;
-                const int d0 = side * (D / 2) + out0;
+                // Each copy puts out half of this side's columns and gives the other half
+                // away, a few at a time: the ring needs the room.
+                constexpr int kMine = D / 2 / COPIES, W = Lay::kOut;
+                const int out0 = copy * kMine, d0 = side * (D / 2) + out0;
+                float *give = join_p + ((side * 2 + (copy ^ 1)) * 64 + r) * Lay::kJoinStride;
+                const float *take = join_p + ((side * 2 + copy) * 64 + r) * Lay::kJoinStride;
                 T *dst = real ? reinterpret_cast<T *>(a.out) + row_place(a, u, r) + d0 : nullptr;
 #pragma unroll 1
-                for (int k = 0; k < kOut; k += W) {
+                for (int k = 0; k < kMine; k += W) {
                     uint32_t o[W];
+                    if (COPIES == 2) {
+                        load_row<W>(tm_o + (out0 ^ kMine) + k, o);
+                        if (k > 0)  // what was given before has been read
+                            ok = meet(&s.copies[quad & 1], meets);
+#pragma unroll
+                        for (int e = 0; e < W; e += 4)
+                            *reinterpret_cast<float4 *>(give + e) =
+                                make_float4(__uint_as_float(o[e]) * f, __uint_as_float(o[e + 1]) * f,
+                                            __uint_as_float(o[e + 2]) * f, __uint_as_float(o[e + 3]) * f);
+                        ok = ok && meet(&s.copies[quad & 1], meets);
+                        if (!ok)
+                            break;
+                    }
                     load_row<W>(tm_o + out0 + k, o);
 #pragma unroll
                     for (int e = 0; e < W; e += 4) {
                         float4 y = make_float4(0, 0, 0, 0);
                         if (COPIES == 2)
-                            y = *reinterpret_cast<const float4 *>(theirs + k + e);
+                            y = *reinterpret_cast<const float4 *>(take + e);
                         o[e] = __float_as_uint(fmaf(__uint_as_float(o[e]), f, y.x));
                         o[e + 1] = __float_as_uint(fmaf(__uint_as_float(o[e + 1]), f, y.y));
                         o[e + 2] = __float_as_uint(fmaf(__uint_as_float(o[e + 2]), f, y.z));
@@ -695,17 +704,18 @@ __global__ void __launch_bounds__(kQtThreads, 1) attend_q4_tc_kernel(const __gri
                         for (int e = 0; e < W; ++e)
                             o[e] = y[e];
                     }
-                    if (!real)
-                        continue;
-                    if (whole) {
+                    if (real && whole) {
                         store_row<T, W>(dst + k, o, inv);
-                    } else {
+                    } else if (real) {
 #pragma unroll
                         for (int e = 0; e < W; e += 4)
                             __stcg(reinterpret_cast<uint4 *>(slot + part_quad<kRows>((d0 + k + e) / 4, r)),
                                    make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
                     }
+                    __syncwarp();
                 }
+                if (!ok)
+                    break;
                 if (real && !whole && side == 0 && copy == 0) {
                     __stcg(slot + (size_t)kRows * D + r, m);
                     __stcg(slot + (size_t)kRows * D + kRows + r, l);
@@ -762,17 +772,19 @@ namespace {
 template <typename T, int D, int COPIES>
 cudaError_t launch_qt(const AttendQ4Args &a, cudaStream_t st)
 {
-    const cudaError_t e = cudaFuncSetAttribute(attend_q4_tc_kernel<T, D, COPIES>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, QtShape<D>::kSmem);
+    constexpr int smem = QtLayout<D, COPIES>::kSmem;
+    const cudaError_t e =
+        cudaFuncSetAttribute(attend_q4_tc_kernel<T, D, COPIES>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
         return e;
-    attend_q4_tc_kernel<T, D, COPIES><<<kAttendCtas, kQtThreads, QtShape<D>::kSmem, st>>>(a);
+    attend_q4_tc_kernel<T, D, COPIES><<<kAttendCtas, kQtThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_qt_t(const AttendQ4Args &a, cudaStream_t st)
 {
+    // (64 chains of 20 rows 101 us, with one copy 119; 256 of 36 340, 403)
     const bool few = a.a.seq.T * a.a.G <= kQtLanes / 2;
     if (a.pool.D == 64)
         return few ? launch_qt<T, 64, 2>(a, st) : launch_qt<T, 64, 1>(a, st);
