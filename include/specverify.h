@@ -582,9 +582,9 @@ SPEC_API int spec_commit_tree(const void *staged, void *kv, spec_dtype dt, int L
  *
  * A round: spec_append_round (staged) -> spec_attend_pages -> spec_verify_tree
  * -> spec_page_reserve (first = len - 1, total = len - 1 + n_emit) and
- * spec_page_copy of its copies -> spec_store_pages of the path.  Prompts run
- * through a 16-bit cache of one layer (spec_append_prompt, spec_attend_prompt),
- * which spec_store_pages then stores; pieces of prompts have their prefix back by
+ * spec_page_copy of its copies -> spec_store_pages_reserved of the path.  Prompts
+ * run through a 16-bit cache of one layer (spec_append_prompt, spec_attend_prompt),
+ * which the same call then stores; pieces of prompts have their prefix back by
  * spec_load_pages.  Pools and 16-bit blocks begin on 16 bytes.
  * ---------------------------------------------------------------------------
  */
@@ -617,7 +617,10 @@ SPEC_API int spec_page_fork(int32_t *table, int32_t *held, int32_t *refs, int N,
  * spec_page_copy has to copy before anything is written, else (-1, -1).  The
  * lowest free pages are taken, by sequences in order, by places in order within
  * one.  Where there are too few, missing[0] says by how many (2^29 wanted pages
- * at most are counted); then pages have been let go, but no row has got any, and what is held is that.  Else it is 0.
+ * at most are counted); then pages have been let go, but no row has got any, and
+ * what is held is that: rows may still share the pages that they were to write, so
+ * nothing may be stored and no length advanced (spec_store_pages_reserved looks at
+ * missing on the device; rows that are good stay unflagged here).  Else it is 0.
  * Flagged, and left as it is: a row outside [0, N) or repeated, first < 0,
  * total < 0 or of more than MP pages, entries outside the pool.
  */
@@ -660,6 +663,18 @@ SPEC_API int spec_store_pages(const void *src, spec_dtype dt, int L, int N, int 
                   int P, int page, int layer, const int32_t *table, int R, int MP, int B, int T,
                   const int32_t *pos, const int32_t *count, const int32_t *slot, const int32_t *idx,
                   const int32_t *row, const int32_t *path, uint32_t *flags, void *cuda_stream);
+
+/*
+ * The same behind a reservation, for rounds that run without a look at the device:
+ * missing [1] int32 is what spec_page_reserve wrote.  Where it is not 0 nothing is
+ * stored, and every sequence is flagged.  (NULL: as spec_store_pages, whose callers
+ * answer for it that no page that is written is another row's too.)
+ */
+SPEC_API int spec_store_pages_reserved(const void *src, spec_dtype dt, int L, int N, int H, int S, int D, void *pool,
+                  int L_pool, int P, int page, int layer, const int32_t *table, int R, int MP, int B, int T,
+                  const int32_t *pos, const int32_t *count, const int32_t *slot, const int32_t *idx,
+                  const int32_t *row, const int32_t *path, const int32_t *missing, uint32_t *flags,
+                  void *cuda_stream);
 
 /*
  * The reverse: positions pos[b] .. pos[b] + count[b] - 1 to rows slot[b] .. of

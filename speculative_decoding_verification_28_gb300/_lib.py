@@ -76,6 +76,8 @@ SIGNATURES["spec_page_compact"] = ([_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _
 SIGNATURES["spec_page_copy"] = ([_vp, _i32, _i32, _sz, _vp, _i32, _vp, _vp, _vp], _i32)
 SIGNATURES["spec_store_pages"] = ([_vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _i32,
                                 _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32)
+SIGNATURES["spec_store_pages_reserved"] = ([_vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _vp,
+                                            _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32)
 SIGNATURES["spec_load_pages"] = ([_vp, _i32, _i32, _i32, _i32, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i32, _i32,
                                _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp], _i32)
 SIGNATURES["spec_attend_pages_workspace_bytes"] = ([_i32, _i32, _i32, _i32], _sz)

@@ -58,8 +58,8 @@ Span pool_span(const void *pool, int P, int H, int page, int D, int layer, int l
 
 int rows_q4(bool store, void *rows, int dt, int L, int N, int H, int S, int D, void *pool, int L_pool, int P, int page,
             int layer, const int32_t *table, int R, int MP, int B, int T, const int32_t *pos, const int32_t *count,
-            const int32_t *slot, const int32_t *idx, const int32_t *row, const int32_t *path, uint32_t *flags,
-            void *cuda_stream)
+            const int32_t *slot, const int32_t *idx, const int32_t *row, const int32_t *path, const int32_t *missing,
+            uint32_t *flags, void *cuda_stream)
 {
     if (B < 0 || B > 65535 || T < 1 || L < 1 || N < 1 || S < 1 || S > INT_MAX - 256 || T > INT_MAX - 256 || layer < 0)
         return SPEC_EINVAL;
@@ -76,7 +76,7 @@ int rows_q4(bool store, void *rows, int dt, int L, int N, int H, int S, int D, v
         overlap(span(rows, 0, 2.0 * L * N * H * (double)S * D, 2), pool_span(pool, P, H, page, D, layer, L)))
         return SPEC_EINVAL;
     if (!aligned(rows, 16) || !aligned(pool, 16) || !int_arrays_ok(table, pos, count, slot, idx) ||
-        !int_arrays_ok(row, path, flags, nullptr, nullptr))
+        !int_arrays_ok(row, path, missing, flags, nullptr))
         return SPEC_EALIGN;
     Q4RowsArgs a{};
     a.pool = pool_view(pool, L_pool, P, H, page, D, table, R, MP);
@@ -94,6 +94,7 @@ int rows_q4(bool store, void *rows, int dt, int L, int N, int H, int S, int D, v
     a.idx = idx;
     a.row = row;
     a.path = path;
+    a.missing = missing;
     a.flags = flags;
     const cudaStream_t st = (cudaStream_t)cuda_stream;
     return launched(store ? launch_store_q4(a, (spec_dtype)dt, st) : launch_load_q4(a, (spec_dtype)dt, st));
@@ -131,7 +132,16 @@ int spec_store_pages(const void *src, spec_dtype dt, int L, int N, int H, int S,
                   const int32_t *path, uint32_t *flags, void *cuda_stream)
 {
     return rows_q4(true, const_cast<void *>(src), dt, L, N, H, S, D, pool, L_pool, P, page, layer, table, R, MP, B, T, pos,
-                   count, slot, idx, row, path, flags, cuda_stream);
+                   count, slot, idx, row, path, nullptr, flags, cuda_stream);
+}
+
+int spec_store_pages_reserved(const void *src, spec_dtype dt, int L, int N, int H, int S, int D, void *pool, int L_pool,
+                  int P, int page, int layer, const int32_t *table, int R, int MP, int B, int T, const int32_t *pos,
+                  const int32_t *count, const int32_t *slot, const int32_t *idx, const int32_t *row,
+                  const int32_t *path, const int32_t *missing, uint32_t *flags, void *cuda_stream)
+{
+    return rows_q4(true, const_cast<void *>(src), dt, L, N, H, S, D, pool, L_pool, P, page, layer, table, R, MP, B, T, pos,
+                   count, slot, idx, row, path, missing, flags, cuda_stream);
 }
 
 int spec_load_pages(const void *pool, int L_pool, int P, int page, int layer, void *dst, spec_dtype dt, int L, int N, int H,
@@ -140,7 +150,7 @@ int spec_load_pages(const void *pool, int L_pool, int P, int page, int layer, vo
                  void *cuda_stream)
 {
     return rows_q4(false, dst, dt, L, N, H, S, D, const_cast<void *>(pool), L_pool, P, page, layer, table, R, MP, B, T, pos,
-                   count, slot, idx, row, nullptr, flags, cuda_stream);
+                   count, slot, idx, row, nullptr, nullptr, flags, cuda_stream);
 }
 
 size_t spec_page_workspace_bytes(int B, int MP, int P)

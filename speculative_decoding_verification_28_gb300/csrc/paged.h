@@ -27,6 +27,7 @@ struct Q4RowsArgs {
     void *dst;  // one of the two
     int L, N, S, B, T;
     const int32_t *pos, *count, *slot, *idx, *row, *path;
+    const int32_t *missing;  // null, or: not 0 stores nothing
     uint32_t *flags;
 };
 cudaError_t launch_store_q4(const Q4RowsArgs &a, spec_dtype dt, cudaStream_t st);

@@ -36,6 +36,8 @@ __device__ bool row_tile(const Q4RowsArgs &a, RowTile &s)
     bool ok = n >= 0 && n <= a.T && pos >= 0 && (long long)pos + n <= (long long)v.MP * page && slot >= 0 && from >= 0 &&
               from < a.N && trow >= 0 && trow < v.R;
     ok = ok && (a.path || (long long)slot + n <= a.S);
+    // after a reservation that came short, rows may share the pages that they were to write
+    ok = ok && !(STORE && a.missing && *a.missing != 0);
     // sequences that write the same rows
     const bool twice = STORE ? repeated_row(a.row, a.B, trow) : repeated_row(a.idx, a.B, from);
     bool fits = true;

@@ -102,7 +102,8 @@ def spec_page_fork(table, held, refs, src, page, dst=None, length=None, flags=No
 def spec_page_reserve(table, held, refs, first, total, page, idx=None, copies=None, missing=None, flags=None,
                       workspace=None):
     """Pages for total[b] tokens in row idx[b] (None: b), of which those from
-    first[b] on will be written and so are named by no other row.
+    first[b] on will be written and so are named by no other row.  missing: the
+    pages that the pool lacked, where no row has got any (see spec_store_pages).
     -> (copies [B, 2] for spec_page_copy, missing [1], flags [B])."""
     B = first.shape[0]
     dev, (N, MP, P), book, ws = _book(table, held, refs, B, workspace)
@@ -166,10 +167,12 @@ def _rows16(t, name):
 
 
 @_streamed
-def spec_store_pages(src, pool, table, pos, count, layer=0, slot=None, idx=None, row=None, path=None, flags=None):
+def spec_store_pages(src, pool, table, pos, count, layer=0, slot=None, idx=None, row=None, path=None, flags=None,
+                     missing=None):
     """Rows slot[b] + j (or + path[b, j]), j < count[b], of src [L, 2, N, H, S,
     D] row idx[b] -> positions pos[b] + j of table row row[b], layers layer ..
-    of pool.  -> flags [B]."""
+    of pool.  missing [1] of the reservation before it: where that is not 0,
+    nothing is stored and all are flagged.  -> flags [B]."""
     dev, L, N, H, S, D = _rows16(src, "src")
     pool_at, Lp, P, page = _pool(pool, dev, H, D, layer, L)
     table_at, R, MP = _table(table, dev)
@@ -178,10 +181,10 @@ def spec_store_pages(src, pool, table, pos, count, layer=0, slot=None, idx=None,
     T = S if path is None else path.shape[-1]
     pos_at = _at(pos, _I32, "pos", dev, rows)
     flags = _out(flags, rows, _I32, dev, "flags", pos)
-    _call(_lib.load().spec_store_pages, dev, src.data_ptr(), _DT[src.dtype], L, N, H, S, D, pool_at, Lp, P,
+    _call(_lib.load().spec_store_pages_reserved, dev, src.data_ptr(), _DT[src.dtype], L, N, H, S, D, pool_at, Lp, P,
           page, layer, table_at, R, MP, B, T, pos_at, _at(count, _I32, "count", dev, rows),
           _at(slot, _I32, "slot", dev, rows), _rows_of(idx, B, N, dev, "idx"), _rows_of(row, B, R, dev, "row"),
-          _at(path, _I32, "path", dev, (B, T)), flags.data_ptr())
+          _at(path, _I32, "path", dev, (B, T)), _at(missing, _I32, "missing", dev, (1,)), flags.data_ptr())
     return flags
 
 

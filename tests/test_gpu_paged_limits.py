@@ -1,0 +1,115 @@
+"""The paged cache where it runs out: pools with too few pages for a round, calls
+without sequences, values at the ends of their ranges."""
+import numpy as np
+import pytest
+import torch
+
+import paged_ref as ref
+import speculative_decoding_verification_28_gb300 as sv
+
+pytestmark = pytest.mark.gpu
+I32 = torch.int32
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=I32).cuda()
+
+
+class Pool:
+    """Rows 0, 1 and 2 of `page`: two forks with a part-full page between them, and one of their own."""
+
+    def __init__(self, page, D, spare, dt=torch.bfloat16):
+        self.page, self.D, self.L, self.H = page, D, 2, 2
+        self.g = torch.Generator().manual_seed(page + D)
+        self.own = 3  # pages of row 2
+        self.P = 2 + self.own + spare
+        self.book = ref.Book(3, 5, self.P, page)
+        self.t = [x.cuda() for x in self.book.tensors()]
+        self.pool = torch.zeros((self.L, 2, self.P, self.H, sv.q4_block_bytes(page, D)), dtype=torch.uint8, device="cuda")
+        self.first = page + page // 2 + 1  # tokens of rows 0 and 1
+        self.last = self.own * page
+        rows = i32([0, 2])
+        total = i32([self.first, self.last])
+        prompt = torch.randn((self.L, 2, 2, self.H, self.last, D), generator=self.g).to(dt).cuda()
+        zero = torch.zeros_like(total)
+        _, missing, f = sv.spec_page_reserve(*self.t, zero, total, page, idx=rows)
+        assert int(missing) == 0 and not f.any()
+        assert not sv.spec_store_pages(prompt, self.pool, self.t[0], zero, total, row=rows, missing=missing).any()
+        assert not sv.spec_page_fork(*self.t, i32([0]), page, dst=i32([1])).any()
+        self.book.reserve([0, 0], [self.first, self.last], [0, 2])
+        self.book.fork([0], [1])
+        self.length = i32([self.first + 1, self.first + 1, self.last + 1])
+        self.T = 3
+        self.staged = torch.randn((self.L, 2, 3, self.H, self.T, D), generator=self.g).to(dt).cuda()
+        self.path = torch.arange(self.T, dtype=I32, device="cuda").repeat(3, 1)
+        self.missing, self.copies = i32([77]), torch.full((3, 2), 7, dtype=I32, device="cuda")
+        self.flags = torch.full((3,), 7, dtype=I32, device="cuda")
+
+    def check_book(self):
+        for got, want, name in zip(self.t, self.book.tensors(), ("table", "held", "refs")):
+            assert torch.equal(got.cpu(), want), name
+
+    def end_of_round(self, n_emit, stream=None):
+        """as a program without a look at the device runs it"""
+        before = self.length - 1
+        sv.spec_page_reserve(*self.t, before, before + n_emit, self.page, copies=self.copies, missing=self.missing)
+        sv.spec_page_copy(self.pool, self.copies)
+        sv.spec_store_pages(self.staged, self.pool, self.t[0], before, n_emit, path=self.path, flags=self.flags,
+                            missing=self.missing)
+        self.length += n_emit * (self.missing == 0)
+
+    def row(self, r, n, pos=0):
+        return ref.get(self.pool.cpu(), self.page, self.D, self.t[0][r].cpu(), n, pos)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("page,D,spare,short", [(16, 64, 0, 2), (32, 128, 1, 1), (64, 96, 0, 2)])
+def test_a_round_with_too_few_pages_stores_nothing(page, D, spare, short, captured):
+    """Rows 0 and 1 both write their shared page, row 2 wants one more: 2 pages for them, where there
+    are fewer.  Nothing may change but `missing` and the flags; with row 2 freed the same round runs."""
+    s = Pool(page, D, spare)
+    n_emit = i32([2, 3, 1])
+    if captured:
+        keep = [x.clone() for x in (*s.t, s.pool, s.length)]
+        graph = sv.RoundGraph(lambda: s.end_of_round(n_emit))
+        for x, y in zip((*s.t, s.pool, s.length), keep):
+            x.copy_(y)
+        run = graph.replay
+    else:
+        run = lambda: s.end_of_round(n_emit)  # noqa: E731
+    pool, length = s.pool.clone(), s.length.clone()
+    run()
+    torch.cuda.synchronize()
+    copies, missing = s.book.reserve([s.first, s.first, s.last], [s.first + 2, s.first + 3, s.last + 1])
+    assert int(s.missing) == missing == short and (s.copies == -1).all()
+    assert (s.flags == sv.FLAG_BAD_STATE).all()
+    s.check_book()
+    assert int(s.t[2].max()) == 2 and torch.equal(s.pool, pool) and torch.equal(s.length, length)
+    # row 2 ends; its part of the round is left out
+    sv.spec_page_fork(*s.t, i32([-1]), page, dst=i32([2]))
+    s.book.fork([-1], [2])
+    n_emit[2] = 0
+    s.length[2] = 1
+    before = [s.row(r, s.first) for r in (0, 1)]
+    run()
+    torch.cuda.synchronize()
+    copies, missing = s.book.reserve([s.first, s.first, 0], [s.first + 2, s.first + 3, 0])
+    assert int(s.missing) == missing == 0 and not s.flags.any()
+    assert s.copies.cpu().tolist() == [list(x) for x in copies] and copies[0][0] >= 0
+    s.check_book()
+    assert s.length.tolist() == [s.first + 3, s.first + 4, 1]
+    for r, n in ((0, 2), (1, 3)):
+        assert torch.equal(s.row(r, s.first), before[r])
+        want = ref.unpack(*ref.pack(s.staged[:, :, r, :, :n].cpu()))
+        assert torch.equal(s.row(r, n, s.first), want)
+
+
+def test_a_store_without_a_reservation_is_as_before():
+    s = Pool(16, 64, 3)
+    pos, count = i32([5, 1, 0]), i32([0, 0, 2])
+    f = sv.spec_store_pages(s.staged, s.pool, s.t[0], pos, count)
+    assert not f.any()
+    want = ref.unpack(*ref.pack(s.staged[:, :, 2, :, :2].cpu()))
+    assert torch.equal(s.row(2, 2), want)
+    with pytest.raises(ValueError, match="missing"):
+        sv.spec_store_pages(s.staged, s.pool, s.t[0], pos, count, missing=i32([0, 0]))
