@@ -453,6 +453,15 @@ __device__ __forceinline__ void q4_queries(const AttendArgs &a, const PagedUnit 
             }
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            const bool small = top < 1.0f / kSmallRow;
+            if (small) {
+                top *= kSmallRow;
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        x[k][i] *= kSmallRow;
+            }
             e = q4_row_exponent(top);
             const float f = __uint_as_float((uint32_t)(127 + e) << 23);
 #pragma unroll
@@ -460,16 +469,19 @@ __device__ __forceinline__ void q4_queries(const AttendArgs &a, const PagedUnit 
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     w[k][i] = TcType<__half>::pack(x[k][i] * f, x[k][i + 4] * f);
+            e += small ? 64 : 0;
         }
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
             qf[q][2 * k][0] = w[k][0], qf[q][2 * k][1] = w[k][1];
             qf[q][2 * k + 1][0] = w[k][2], qf[q][2 * k + 1][1] = w[k][3];
         }
-        // a column's factor comes from a lane that has its row
+        // a column's factor comes from a lane that has its row; never 0, which would make
+        // hidden scores NaN (raw ones are below 2^25, so that nothing else sees the limit)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            c[q][i] = a.scale_log2 * exp2f((float)(7 - __shfl_sync(0xFFFFFFFFu, e, (2 * t + i) * 4)));
+            c[q][i] = fmaxf(a.scale_log2 * exp2f((float)(7 - __shfl_sync(0xFFFFFFFFu, e, (2 * t + i) * 4))),
+                            1.17549435e-38f);
     }
 }
 

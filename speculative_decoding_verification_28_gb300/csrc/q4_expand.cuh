@@ -93,12 +93,15 @@ __device__ __forceinline__ uint4 in_order(const uint32_t *x)
                       __byte_perm(x[2], x[3], 0x7632));
 }
 
-// exponent e of the power of two that a bf16 row with largest magnitude `top`
-// is held times in fp16: top goes to 2^8 .. 2^9.  What falls under fp16's steps
-// is then less than 2^-32 of it, less than fp32 sums keep.
+// exponent e of the power of two that a bf16 row with largest magnitude `top`,
+// 2^-64 at least, is held times in fp16: top goes to 2^8 .. 2^9.  What falls under
+// fp16's steps is then less than 2^-32 of it, less than fp32 sums keep.  Smaller rows
+// (subnormal ones among them) come times 2^64 first, kSmallRow: 2^e alone would be
+// past fp32's range for them.
+constexpr float kSmallRow = 18446744073709551616.0f;
 __device__ __forceinline__ int q4_row_exponent(float top)
 {
-    return top > 0.0f && top <= 3.4e38f ? min(100, 8 - ((int)(__float_as_uint(top) >> 23) - 127)) : 0;
+    return top > 0.0f && top <= 3.4e38f ? 8 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
 }
 
 }  // namespace spec

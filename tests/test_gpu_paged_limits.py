@@ -113,3 +113,31 @@ def test_a_store_without_a_reservation_is_as_before():
     assert torch.equal(s.row(2, 2), want)
     with pytest.raises(ValueError, match="missing"):
         sv.spec_store_pages(s.staged, s.pool, s.t[0], pos, count, missing=i32([0, 0]))
+
+
+@pytest.mark.parametrize("T,G", [(1, 4), (3, 4), (9, 4)])
+@pytest.mark.parametrize("power", [-64, -92, -95, -110, -120])
+def test_queries_of_any_size(power, T, G):
+    """Rows of queries down to the smallest normal numbers, with a scale to match, in every form: as exact as
+    rows of ordinary size.  (All products are normal numbers in fp32: values are 2^-9 .. 2^3 and zeros.)"""
+    from test_gpu_attend_q4 import check, make
+
+    c = make(31, "bf16", 4, T, G, 2, 128, 32, [300, 65, 20, 1])
+    f = 2.0 ** power
+    check(dict(c, q=(c["q"].float() * f).to(torch.bfloat16)), scale=128 ** -0.5 / f)
+    # rows of a unit that differ: the smaller ones' weights are nearly even
+    g = torch.exp2(-3.0 * (torch.arange(c["q"].shape[2]) % 3))[:, None]
+    check(dict(c, q=(c["q"].float() * g * f).to(torch.bfloat16)), scale=128 ** -0.5 / f)
+
+
+@pytest.mark.parametrize("T,G", [(1, 4), (3, 4), (9, 4)])
+@pytest.mark.parametrize("scale", [1.0, 1e-4, 1e-30, 1e-37])
+def test_queries_of_next_to_nothing(scale, T, G):
+    """Subnormal rows and rows of zeros, whose weights are even, in tiles with hidden keys."""
+    from test_gpu_attend_q4 import check, make
+
+    c = make(32, "bf16", 4, T, G, 2, 64, 16, [300, 65, 20, 1])
+    q = (c["q"].float() * 2.0 ** -130).to(torch.bfloat16)
+    q[:, :, ::3] = 0.0
+    assert q.any()
+    check(dict(c, q=q), scale=scale)
