@@ -694,6 +694,7 @@ SPEC_API size_t spec_attend_pages_workspace_bytes(int T, int Hq, int H, int D);
  * spec_attend_round with the prefix (positions 0 .. len - 2) in pages of the
  * pool's layer `layer`, by table row idx[b] (NULL: b), and the nodes in staged
  * [L, 2, B, H, T, D]; q, staged and out in bf16 or fp16, heads of 64 or 128.
+ * With fp16 scale is at most 1.8e36.
  * What lies in pages behind the prefix may be anything.  Flagged: len < 1 or
  * past MP pages, a row outside [0, R), n_nodes outside [0, T]; and pages of
  * the prefix outside the pool, where the outputs of the sequence are undefined.

@@ -6,7 +6,7 @@
 
 #include "host_checks.h"
 #include "paged.h"
-#include "q4.cuh"
+#include "q4_expand.cuh"
 
 using namespace spec;
 
@@ -245,8 +245,10 @@ int spec_attend_pages(const void *q, spec_dtype dt, int B, int T, int Hq, const 
         return SPEC_EDTYPE;
     if (B == 0)
         return SPEC_OK;
-    if (!q || !pool || !table || !len || !staged || !out || (!idx && B > R) || !(scale > 0.0f) ||
-        !isfinite(scale * 1.44269504088896340736f) || (long long)B * T * Hq > INT_MAX)
+    if (!q || !pool || !table || !len || !staged || !out || (!idx && B > R) || (long long)B * T * Hq > INT_MAX)
+        return SPEC_EINVAL;
+    // fp16 scores are 128 times too small (q4_expand.cuh), which their factor to base 2 makes good
+    if (!(scale > 0.0f) || !isfinite(scale * 1.44269504088896340736f * (dt == SPEC_F16 ? kQ4Units : 1.0f)))
         return SPEC_EINVAL;
     // tiles of 64 keys for 8 query rows each, and eight more a unit for its start and end: the
     // kernels count them in 31 bits

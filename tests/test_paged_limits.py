@@ -2,7 +2,7 @@
 every call returns before any CUDA call."""
 import pytest
 
-from test_paged_boundary import A, ODD, POOL, Q, at, lib, store  # noqa: F401
+from test_paged_boundary import A, ODD, POOL, Q, at, attend, lib, store  # noqa: F401
 
 
 def store_reserved(lib, src=Q, dt=1, L=1, N=2, H=2, S=64, D=64, pool=POOL, Lp=2, P=9, page=16, layer=1, table=A, R=2, MP=4,
@@ -20,3 +20,10 @@ def test_a_store_behind_a_reservation_refuses_what_a_store_refuses(lib, missing)
                dict(pos=ODD), dict(path=ODD), dict(flags=ODD), dict(B=0)):
         assert store_reserved(lib, missing=missing, **kw) == store(lib, **kw), kw
     assert store_reserved(lib, missing=ODD) == -5
+
+
+def test_scales_that_fp16_scores_cannot_be_taken_to_base_2_with(lib):  # noqa: F811
+    # 128 * 1.4427 times the scale has to be finite for fp16, the scale's 1.4427-fold for bf16
+    assert attend(lib, dt=2, scale=1.9e36) == -1 and attend(lib, dt=2, scale=3e38) == -1
+    assert attend(lib, dt=2, scale=1.8e36, wsb=16) == -3
+    assert attend(lib, dt=1, scale=2e38, wsb=16) == -3 and attend(lib, dt=1, scale=3e38) == -1
