@@ -490,7 +490,8 @@ SPEC_API size_t spec_attend_workspace_bytes(int T, int Hq, int H, int D);
  * (len 1, mask 0) gives zeros.  Slots no query of the sequence sees may hold
  * anything, and a value that is not finite reaches only the queries that see
  * it.  T = 1 is plain decoding.  An index may be repeated.  scale > 0, and
- * scale * |q.k| within fp32's range.  Statistics and sums are fp32; the same
+ * scale * |q.k| below 2^23: past that a step of an fp32 score is more than fp16
+ * weights have room for, and results need not be finite.  Statistics and sums are fp32; the same
  * inputs give the same bits.  out must not overlap q, the layer or staged.
  */
 SPEC_API int spec_attend_round(const void *q, spec_dtype dt, int B, int T, int Hq, const void *kv, int L, int N,

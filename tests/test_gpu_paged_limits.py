@@ -141,3 +141,58 @@ def test_queries_of_next_to_nothing(scale, T, G):
     q[:, :, ::3] = 0.0
     assert q.any()
     check(dict(c, q=q), scale=scale)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("T,G", [(1, 4), (3, 4), (9, 4)])
+def test_the_largest_scales_and_scores(dt, T, G):
+    """Rows of zeros keep even weights under any scale; scores up to 2^23 give finite results, and the
+    value of the largest score's key where that leads by 64 and more."""
+    from test_gpu_attend_q4 import DT, check, make, run
+
+    c = make(33, dt, 3, T, G, 2, 128, 64, [300, 65, 1])
+    check(dict(c, q=torch.zeros_like(c["q"])), scale={"bf16": 2e38, "f16": 1.8e36}[dt])
+    eps = torch.finfo(DT[dt]).eps
+    for q in (c["q"], c["q"] * 2.0 ** -10, torch.zeros_like(c["q"])):
+        if not q.any():
+            q[..., 77] = 2.0 ** -24  # scores from a single product
+        keys, values = [], []
+        for b in range(3):
+            pre = ref.get(c["pool"][1:2], 64, 128, c["table"][b], int(c["length"][b]) - 1)[0]
+            keys.append([torch.cat([pre[0], c["staged"][1, 0, b, :, :i + 1].double()], 1) for i in range(T)])
+            values.append([torch.cat([pre[1], c["staged"][1, 1, b, :, :i + 1].double()], 1) for i in range(T)])
+        raw = [[torch.einsum("hgd,hnd->hgn", q[b, i].double().view(2, G, 128), keys[b][i]) for i in range(T)] for b in range(3)]
+        top = max(float(x.abs().max()) for r in raw for x in r)
+        scale = 2.0 ** 23 / top * (1 - 2.0 ** -10)
+        out = run(dict(c, q=q), scale=scale)[0].cpu().double()
+        assert torch.isfinite(out).all()
+        led = 0
+        for b in range(3):
+            for i in range(T):
+                s, o = raw[b][i] * scale, out[b, i].view(2, G, 128)
+                best = s.max(-1, keepdim=True)[0]
+                near = s >= best - 64
+                # a score's error is 136 * 2^-24 * 2^23 at most, so that what is not within 136 has no weight
+                clear = near.sum(-1) == 1
+                clear &= (s >= best - 64 - 136).sum(-1) == 1
+                want = torch.einsum("hgn,hnd->hgd", near.double(), values[b][i])
+                off = ((o - want).abs() - eps * want.abs() - 2.0 ** -25)[clear]
+                assert off.numel() == 0 or float(off.max()) <= 0, (b, i, float(off.max()))
+                led += int(clear.sum())
+        assert led > 0
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,D", [(1, 128), (9, 128), (40, 64), (3, 96)])
+def test_the_largest_scores_over_a_16_bit_cache(dt, T, D):
+    """The same bound over a contiguous cache."""
+    dtype = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}[dt]
+    g = torch.Generator().manual_seed(34)
+    B, H, G, S = 2, 2, 4, 400
+    q = torch.randn((B, T, G * H, D), generator=g).to(dtype)
+    kv = torch.randn((1, 2, B, H, S, D), generator=g).to(dtype)
+    top = torch.einsum("bthgd,bhsd->bthgs", q.double().view(B, T, H, G, D), kv[0, 0].double()).abs().max()
+    mask = (2 << torch.arange(T, device="cuda")).sub(1).repeat(B, 1)
+    o, flags = sv.spec_attend_round(q.cuda(), kv.cuda(), 0, i32([300, 65]), None, mask, scale=float(2.0 ** 23 / top * 0.999))
+    assert not flags.any() and torch.isfinite(o).all()
+    assert float(o.abs().max()) <= float(kv.abs().max()) * (1 + torch.finfo(dtype).eps)
