@@ -622,6 +622,7 @@ SPEC_API int spec_page_fork(int32_t *table, int32_t *held, int32_t *refs, int N,
  * what is held is that: rows may still share the pages that they were to write, so
  * nothing may be stored and no length advanced (spec_store_pages_reserved looks at
  * missing on the device; rows that are good stay unflagged here).  Else it is 0.
+ * With B = 0 nothing is written, missing neither.
  * Flagged, and left as it is: a row outside [0, N) or repeated, first < 0,
  * total < 0 or of more than MP pages, entries outside the pool.
  */

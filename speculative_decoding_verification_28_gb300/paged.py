@@ -111,8 +111,10 @@ def spec_page_reserve(table, held, refs, first, total, page, idx=None, copies=No
     first_at, total_at = _at(first, _I32, "first", dev, rows), _at(total, _I32, "total", dev, rows)
     copies = _out(copies, (B, 2), _I32, dev, "copies")
     if missing is None:
-        missing = torch.zeros(1, dtype=_I32, device=dev) if B == 0 else torch.empty(1, dtype=_I32, device=dev)
+        missing = torch.empty(1, dtype=_I32, device=dev)
     missing_at = _at(missing, _I32, "missing", dev, (1,))
+    if B == 0:  # for which the C call does nothing
+        missing.zero_()
     flags = _out(flags, rows, _I32, dev, "flags", first)
     _call(_lib.load().spec_page_reserve, dev, *book, N, MP, P, int(page), B, first_at, total_at,
           _rows_of(idx, B, N, dev, "idx"), copies.data_ptr(), missing_at, flags.data_ptr(), ws.data_ptr(), ws.numel())

@@ -196,3 +196,22 @@ def test_the_largest_scores_over_a_16_bit_cache(dt, T, D):
     o, flags = sv.spec_attend_round(q.cuda(), kv.cuda(), 0, i32([300, 65]), None, mask, scale=float(2.0 ** 23 / top * 0.999))
     assert not flags.any() and torch.isfinite(o).all()
     assert float(o.abs().max()) <= float(kv.abs().max()) * (1 + torch.finfo(dtype).eps)
+
+
+def test_a_reservation_for_no_sequences_lacks_nothing():
+    """A batch that became empty, with the `missing` word of a call that came short: a store behind it may go on."""
+    book = [x.cuda() for x in ref.Book(2, 3, 2, 16).tensors()]
+    missing = i32([0])
+    sv.spec_page_reserve(*book, i32([0]), i32([48]), 16, missing=missing)
+    assert int(missing) == 1
+    none = i32([])
+    copies, m, flags = sv.spec_page_reserve(*book, none, none, 16, missing=missing)
+    assert m is missing and int(missing) == 0 and copies.shape == (0, 2) and flags.shape == (0,)
+    assert int(sv.spec_page_reserve(*book, none, none, 16)[1]) == 0
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    missing.fill_(5)
+    other.wait_stream(torch.cuda.current_stream())
+    sv.spec_page_reserve(*book, none, none, 16, missing=missing, stream=other)
+    other.synchronize()
+    assert int(missing) == 0
