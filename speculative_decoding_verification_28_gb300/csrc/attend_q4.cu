@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NQ>::kCtas) attend_q4_k
     const AttendArgs &a = x.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // a unit's start and end cost about eight tiles (128 sequences 97 us; counted as none 117)
-    const Shape sh{kQ4Keys, Sh::kRows, a.G, 8};
+    const UnitShape<8> sh{kQ4Keys, Sh::kRows, a.G};
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&s.full[i], 1);
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NQ>::kCtas) attend_q4_k
 
     if (warp == kQ4Warps) {
         // ------------------------------------------------------------ loads
-        UnitWalk walk(a, sh, s.run);
+        UnitWalk<UnitShape<8>> walk(a, sh, s.run);
         AttendUnit w{};
         TileCopies<D, kQ4Keys> copies(x);
         uint32_t it = 0, n = 0;

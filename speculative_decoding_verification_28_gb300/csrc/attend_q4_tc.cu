@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) attend_q4_tc_kernel(const __gri
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int kRows = kQtLanes / COPIES;  // of a unit
     // a unit's start and end cost about two tiles (256 chains 340 us; counted as none 377, one 355, four 348)
-    const Shape sh{kKeys, kRows, a.G, 2};
+    const UnitShape<2> sh{kKeys, kRows, a.G};
     constexpr int kMmaWarp = kQtSoftmax, kLoadWarp = kMmaWarp + 1, kFirstExpand = kMmaWarp + 4;
     constexpr bool kHalf = std::is_same<T, __half>::value;
 
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(kQtThreads, 1) attend_q4_tc_kernel(const __gri
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------ loads
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        UnitWalk walk(a, sh, s.run);
+        UnitWalk<UnitShape<2>> walk(a, sh, s.run);
         AttendUnit w{};
         TileCopies<D, kKeys> copies(x);
         uint32_t it = 0, n = 0;

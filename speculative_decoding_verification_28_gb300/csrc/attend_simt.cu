@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(kSimtThreads, CB <= 2 ? 2 : 1) attend_simt_ker
         find_run<kSimtThreads>(a, sh, s_scan, &s_run);
         __syncthreads();
     }
-    UnitWalk walk(a, sh, PROMPT ? Run{} : s_run);
+    UnitWalk<> walk(a, sh, PROMPT ? Run{} : s_run);
     if constexpr (!PROMPT)
         have = walk.next(u);
     const long long slab = (long long)a.cache.S * D;

@@ -199,13 +199,14 @@ __device__ __forceinline__ void prefetch_unit(const AttendArgs &a, const AttendU
 
 // By the walking warp at its end: flags of the sequences whose first tile this
 // CTA had, and by CTA 0 of those that have none.
-__device__ __noinline__ inline void paged_flags(const AttendQ4Args &x, const Shape &sh, const Run &run)
+template <typename SH>
+__device__ __noinline__ void paged_flags(const AttendQ4Args &x, const SH &sh, const Run &run)
 {
     const AttendArgs &a = x.a;
     if (!a.flags)
         return;
     const int lane = threadIdx.x & 31;
-    UnitWalk again(a, sh, run);
+    UnitWalk<SH> again(a, sh, run);
     AttendUnit u{};
     while (again.next(u)) {
         if (u.tile != 0 || u.h != 0 || u.row0 != 0)

@@ -388,7 +388,7 @@ __device__ __noinline__ void put_back32(const AttendArgs &a, const AttendUnit &u
 // Walks the units of a CTA: a prompt's one, or a round's run.
 template <bool PROMPT>
 struct Units {
-    UnitWalk walk;
+    UnitWalk<> walk;
     AttendUnit one;
     bool fresh;
     // some: whether the prompt has one for this CTA
