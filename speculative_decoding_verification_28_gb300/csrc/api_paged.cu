@@ -208,8 +208,8 @@ int spec_page_copy(void *pool, int slabs, int P, size_t page_bytes, const int32_
     if (slabs < 0 || P < 1 || P > kMostPages || M < 0 || M > kMostPages || page_bytes < 16 || page_bytes % 16 != 0 ||
         page_bytes > (size_t)1 << 31 || (double)slabs * page_bytes > 1e12)
         return SPEC_EINVAL;
-    // chunks of 16 kB of a page in all slabs are counted in 31 bits
-    if ((double)slabs * (page_bytes / 16384 + 1) > (double)INT_MAX)
+    // the chunks of a page in all slabs are a grid's first dimension
+    if (slabs * copy_chunks((long long)page_bytes) > INT_MAX)
         return SPEC_EINVAL;
     if (M == 0 && !err)
         return SPEC_OK;

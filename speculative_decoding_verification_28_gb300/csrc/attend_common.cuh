@@ -20,7 +20,7 @@
 
 namespace spec {
 
-constexpr int kAttendCtas = 152;  // CTAs of a round's launch: one per SM
+constexpr int kAttendCtas = kSms;  // CTAs of a round's launch: one per SM
 constexpr int kMinTiles = 2;      // smallest run worth a CTA of its own
 
 struct AttendUnit {

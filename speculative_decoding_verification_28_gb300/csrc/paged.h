@@ -59,6 +59,8 @@ cudaError_t launch_page_fork(const ForkArgs &a, cudaStream_t st);
 cudaError_t launch_page_reserve(const ReserveArgs &a, cudaStream_t st);
 cudaError_t launch_page_compact(const CompactArgs &a, cudaStream_t st);
 
+constexpr int kCopyChunk = 32768;  // bytes of a page in a slab that a CTA copies at a time
+inline long long copy_chunks(long long page_bytes) { return (page_bytes + kCopyChunk - 1) / kCopyChunk; }
 struct PageCopyArgs {
     unsigned char *pool;
     int slabs, P;         // pages of a slab

@@ -444,7 +444,7 @@ cudaError_t launch_page_compact(const CompactArgs &a, cudaStream_t st)
 // ---------------------------------------------------------------------------
 constexpr int kCopyThreads = 256;
 constexpr int kCopyEach = 8;  // 16-byte words of a thread in flight
-constexpr int kCopyChunk = kCopyThreads * kCopyEach * 16;
+static_assert(kCopyChunk == kCopyThreads * kCopyEach * 16, "what the host counts a page's chunks by");
 
 // CTA (x, y): chunk x of a page, the chunks of all slabs numbered through, of every
 // gridDim.y-th pair.
@@ -496,9 +496,9 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const PageCopyA
 cudaError_t launch_page_copy(const PageCopyArgs &a, cudaStream_t st)
 {
     // chunks of a page, as even as 16-byte words allow
-    const int chunks = (int)((a.bytes + kCopyChunk - 1) / kCopyChunk);
+    const int chunks = (int)copy_chunks(a.bytes);
     const long long words = a.bytes / 16, each = (words + chunks - 1) / chunks;
-    const long long x = (long long)a.slabs * chunks, most = 152 * 8;  // eight CTAs an SM
+    const long long x = (long long)a.slabs * chunks, most = 8 * kSms;  // eight CTAs an SM
     const long long y = x < 1 ? 1 : most / x < 1 ? 1 : most / x < a.M ? most / x : a.M > 0 ? a.M : 1;
     page_copy_kernel<<<dim3((unsigned)(x < 1 ? 1 : x), (unsigned)y), kCopyThreads, 0, st>>>(a, x < 1 ? 0 : chunks,
                                                                                            (int)(each * 16));

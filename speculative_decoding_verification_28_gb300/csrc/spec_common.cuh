@@ -15,6 +15,7 @@ namespace spec {
 // ---------------------------------------------------------------------------
 // sizes
 // ---------------------------------------------------------------------------
+constexpr int kSms = 152;              // of a GB300
 constexpr int kThreads = 256;          // threads of the row-streaming kernels
 constexpr int kMinChunk = 4096;        // smallest vocabulary chunk of a verify work unit
 #ifndef SPEC_TARGET_UNITS

@@ -27,3 +27,16 @@ def test_scales_that_fp16_scores_cannot_be_taken_to_base_2_with(lib):  # noqa: F
     assert attend(lib, dt=2, scale=1.9e36) == -1 and attend(lib, dt=2, scale=3e38) == -1
     assert attend(lib, dt=2, scale=1.8e36, wsb=16) == -3
     assert attend(lib, dt=1, scale=2e38, wsb=16) == -3 and attend(lib, dt=1, scale=3e38) == -1
+
+
+def test_pages_copied_are_counted_by_the_chunks_of_a_launch(lib):  # noqa: F811
+    """The last sizes within the limits get as far as the check of addresses, the next ones do not."""
+    def copy(**kw):
+        a = dict(pool=at(0x100000004), slabs=4, P=9, size=1088, M=3)
+        a.update(kw)
+        return lib.spec_page_copy(a["pool"], a["slabs"], a["P"], a["size"], A, a["M"], None, None, None)
+
+    most = (1 << 31) - 1
+    assert copy(slabs=most, size=464) == -5 and copy(slabs=most, size=480) == -1  # 10^12 bytes of a page
+    assert copy(slabs=465, size=1 << 31) == -5 and copy(slabs=466, size=1 << 31) == -1
+    assert copy(size=(1 << 31) + 16) == -1 and copy(P=1 << 24) == -5 and copy(M=1 << 24) == -5 and copy(M=(1 << 24) + 1) == -1
