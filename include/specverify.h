@@ -491,8 +491,10 @@ SPEC_API size_t spec_attend_workspace_bytes(int T, int Hq, int H, int D);
  * anything, and a value that is not finite reaches only the queries that see
  * it.  T = 1 is plain decoding.  An index may be repeated.  scale > 0, and
  * scale * |q.k| below 2^23: past that a step of an fp32 score is more than fp16
- * weights have room for, and results need not be finite.  Statistics and sums are fp32; the same
- * inputs give the same bits.  out must not overlap q, the layer or staged.
+ * weights have room for, and results need not be finite.  Statistics and sums are
+ * fp32, weights of 16-bit inputs fp16 or bf16 (what is lost by that is less than a
+ * result's own rounding); the same inputs give the same bits.  out must not overlap
+ * q, the layer or staged.
  */
 SPEC_API int spec_attend_round(const void *q, spec_dtype dt, int B, int T, int Hq, const void *kv, int L, int N,
                       int H, int S, int D, int layer, const int32_t *len, const int32_t *pad,
@@ -577,8 +579,9 @@ SPEC_API int spec_commit_tree(const void *staged, void *kv, spec_dtype dt, int L
  *
  * The pages of sequences are in table [N, MP] int32: row r's token i is in page
  * table[r, i / page].  held [N] says how many pages a row has, the entries
- * behind are -1; refs [P] how many entries name a page (0: free).  A table of
- * -1 and zeros elsewhere is an empty pool.  The three are changed only by the
+ * behind are -1; refs [P] how many entries name a page (0: free).  P and MP are at
+ * most 2^24, and MP * page is below 2^31 - 8192.  A table of -1 and zeros elsewhere is
+ * an empty pool.  The three are changed only by the
  * spec_page_* calls; the calls on keys and values read the table alone.
  *
  * A round: spec_append_round (staged) -> spec_attend_pages -> spec_verify_tree
@@ -601,8 +604,8 @@ SPEC_API size_t spec_page_workspace_bytes(int B, int MP, int P);
  * forked into one another, and src = dst shortens a row.  Pages are shared, not
  * copied; spec_page_reserve gives a row its own before they are written.
  * Flagged, and left as it is: a row outside [0, N) (src: [-1, N)) or a repeated
- * dst, a negative length or one longer than the source's pages, entries outside the
- * pool.
+ * dst, a negative length or one longer than the source's pages (with src -1 it is
+ * not looked at), entries of the two rows outside the pool.
  */
 SPEC_API int spec_page_fork(int32_t *table, int32_t *held, int32_t *refs, int N, int MP, int P, int page, int B,
                    const int32_t *src, const int32_t *dst, const int32_t *length, uint32_t *flags,
@@ -624,7 +627,8 @@ SPEC_API int spec_page_fork(int32_t *table, int32_t *held, int32_t *refs, int N,
  * missing on the device; rows that are good stay unflagged here).  Else it is 0.
  * With B = 0 nothing is written, missing neither.
  * Flagged, and left as it is: a row outside [0, N) or repeated, first < 0,
- * total < 0 or of more than MP pages, entries outside the pool.
+ * total < 0 or of more than MP pages, entries outside the pool from first's page on
+ * (those before it are not looked at).
  */
 SPEC_API int spec_page_reserve(int32_t *table, int32_t *held, int32_t *refs, int N, int MP, int P, int page,
                       int B, const int32_t *first, const int32_t *total, const int32_t *idx,
@@ -688,8 +692,9 @@ SPEC_API int spec_load_pages(const void *pool, int L_pool, int P, int page, int 
                  const int32_t *pos, const int32_t *count, const int32_t *slot, const int32_t *idx,
                  const int32_t *row, uint32_t *flags, void *cuda_stream);
 
-/* Workspace of spec_attend_pages; what spec_attend_workspace_bytes says of
- * its own holds for it, and the two calls may share one that is large enough for both. */
+/* Workspace of spec_attend_pages, the same for all T and numbers of heads; what
+ * spec_attend_workspace_bytes says of its own holds for it, and the two calls may share
+ * one that is large enough for both. */
 SPEC_API size_t spec_attend_pages_workspace_bytes(int T, int Hq, int H, int D);
 
 /*
@@ -700,6 +705,10 @@ SPEC_API size_t spec_attend_pages_workspace_bytes(int T, int Hq, int H, int D);
  * What lies in pages behind the prefix may be anything.  Flagged: len < 1 or
  * past MP pages, a row outside [0, R), n_nodes outside [0, T]; and pages of
  * the prefix outside the pool, where the outputs of the sequence are undefined.
+ * Work is counted in 31 bits by what the table could hold, not by lengths, which
+ * only the device knows: SPEC_EINVAL where B * H * ceil(T * (Hq / H) / 8) *
+ * (ceil(MP * page / 64) + 9) is 2^31 or more (512 sequences of 8 heads with 32 query
+ * rows may have tables of 7 million tokens).
  */
 SPEC_API int spec_attend_pages(const void *q, spec_dtype dt, int B, int T, int Hq, const void *pool, int L, int P,
                          int H, int page, int D, int layer, const int32_t *table, int R, int MP,

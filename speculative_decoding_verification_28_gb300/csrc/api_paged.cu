@@ -225,7 +225,7 @@ size_t spec_attend_pages_workspace_bytes(int T, int Hq, int H, int D)
 {
     if (T < 1 || Hq < 1 || H < 1 || D < 1)
         return 0;
-    return attend_q4_workspace(T, Hq, H, D);
+    return attend_q4_workspace(D);
 }
 
 int spec_attend_pages(const void *q, spec_dtype dt, int B, int T, int Hq, const void *pool, int L, int P, int H,
@@ -263,7 +263,7 @@ int spec_attend_pages(const void *q, spec_dtype dt, int B, int T, int Hq, const 
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(pool, 16) || !aligned(staged, 16) || !aligned(tree_mask, 8) ||
         !int_arrays_ok(table, len, idx, n_nodes, flags))
         return SPEC_EALIGN;
-    if (!workspace || workspace_bytes < attend_q4_workspace(T, Hq, H, D) || !aligned(workspace, 256))
+    if (!workspace || workspace_bytes < attend_q4_workspace(D) || !aligned(workspace, 256))
         return SPEC_EWORKSPACE;
     AttendQ4Args x{};
     x.pool = pool_view(const_cast<void *>(pool), L, P, H, page, D, table, R, MP);

@@ -758,9 +758,8 @@ cudaError_t launch_attend_q4(const AttendQ4Args &a, spec_dtype dt, cudaStream_t 
     return dt == SPEC_BF16 ? launch_q4_d<__nv_bfloat16, 128>(a, st) : launch_q4_d<__half, 128>(a, st);
 }
 
-size_t attend_q4_workspace(int T, int Hq, int H, int D)
+size_t attend_q4_workspace(int D)
 {
-    (void)T, (void)Hq, (void)H;
     const size_t one = 2 * 3 * kAttendCtas * part_floats<8>(D), many = 2 * 2 * kAttendCtas * part_floats<16>(D);
     const size_t few = align256(kPartHead + (one > many ? one : many) * sizeof(float)), tc = attend_q4_tc_workspace(D);
     return few > tc ? few : tc;

@@ -81,6 +81,6 @@ struct AttendQ4Args {
 cudaError_t launch_attend_q4(const AttendQ4Args &a, spec_dtype dt, cudaStream_t st);
 cudaError_t launch_attend_q4_tc(const AttendQ4Args &a, spec_dtype dt, cudaStream_t st);
 size_t attend_q4_tc_workspace(int D);
-size_t attend_q4_workspace(int T, int Hq, int H, int D);
+size_t attend_q4_workspace(int D);
 
 }  // namespace spec

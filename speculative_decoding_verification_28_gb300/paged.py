@@ -208,7 +208,7 @@ def spec_load_pages(pool, dst, table, pos, count, layer=0, slot=None, idx=None, 
     return flags
 
 
-_attend_bytes = {}  # spec_attend_pages_workspace_bytes by its arguments
+_attend_bytes = {}  # spec_attend_pages_workspace_bytes by D, the only argument that it depends on
 
 
 def spec_attend_pages_workspace_bytes(T, Hq, H, D):
@@ -237,9 +237,11 @@ def spec_attend_pages(q, pool, layer, table, length, staged, tree_mask=None, n_n
     out = _out(out, shape, dt, dev, "out", q)
     flags = _out(flags, rows, _I32, dev, "flags", length)
     lib = _lib.load()
-    need = _attend_bytes.get((T, Hq, H, D))
+    need = _attend_bytes.get(D)
     if need is None:
-        need = _attend_bytes[T, Hq, H, D] = lib.spec_attend_pages_workspace_bytes(T, Hq, H, D)
+        need = lib.spec_attend_pages_workspace_bytes(T, Hq, H, D)
+        if need:
+            _attend_bytes[D] = need
     ws = _ws(workspace, "attend", need, dev, ATTEND_ZERO)
     _call(lib.spec_attend_pages, dev, q.data_ptr(), _DT[dt], B, T, Hq, pool_at, L, P, H, page, D, layer,
           table_at, R, MP, length_at, _rows_of(idx, B, R, dev, "idx"), _at(n_nodes, _I32, "n_nodes", dev, rows),

@@ -40,3 +40,21 @@ def test_pages_copied_are_counted_by_the_chunks_of_a_launch(lib):  # noqa: F811
     assert copy(slabs=most, size=464) == -5 and copy(slabs=most, size=480) == -1  # 10^12 bytes of a page
     assert copy(slabs=465, size=1 << 31) == -5 and copy(slabs=466, size=1 << 31) == -1
     assert copy(size=(1 << 31) + 16) == -1 and copy(P=1 << 24) == -5 and copy(M=1 << 24) == -5 and copy(M=(1 << 24) + 1) == -1
+
+
+def test_work_is_counted_by_what_tables_can_hold(lib):  # noqa: F811
+    """B H ceil(T G / 8) (ceil(MP page / 64) + 9) below 2^31, whatever the lengths are."""
+    far = dict(q=at(1 << 44), out=at(1 << 45), staged=at(1 << 46), L=1, layer=0, P=9, wsb=16)
+    for B, H, G, T, page, MP in ((512, 8, 4, 8, 64, 112500), (1, 1, 1, 1, 256, (1 << 23) - 600), (4096, 2, 9, 7, 256, 1000),
+                                 (60000, 8, 1, 64, 16, 4)):
+        count = lambda mp: B * H * -(-T * G // 8) * (-(-mp * page // 64) + 9)  # noqa: E731, B023
+        while count(MP + 64) < 1 << 31 and (MP + 64) * page <= (1 << 31) - 1 - 8192:
+            MP += 64
+        assert attend(lib, B=B, R=B, H=H, Hq=H * G, T=T, page=page, MP=MP, **far) == (-3 if count(MP) < 1 << 31 else -1)
+        if (MP + 64) * page <= (1 << 31) - 1 - 8192:
+            assert attend(lib, B=B, R=B, H=H, Hq=H * G, T=T, page=page, MP=MP + 64, **far) == -1
+    assert attend(lib, **dict(far, MP=1 << 24, R=2, P=1 << 24)) == -3
+    assert attend(lib, **dict(far, MP=(1 << 24) + 1)) == -1 and attend(lib, **dict(far, MP=4, P=(1 << 24) + 1)) == -1
+    # one size of scratch for all rounds of a head size
+    sizes = {lib.spec_attend_pages_workspace_bytes(T, Hq, H, 128) for T, Hq, H in ((1, 1, 1), (64, 64, 8), (9, 28, 4))}
+    assert len(sizes) == 1
