@@ -494,7 +494,10 @@ __global__ void __launch_bounds__(kQ4Threads, Q4Shape<D, NQ>::kCtas) attend_q4_k
     Q4Shared<D, NQ> &s = *reinterpret_cast<Q4Shared<D, NQ> *>(base);
     const AttendArgs &a = x.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // a unit's start and end cost about eight tiles (128 sequences 97 us; counted as none 117)
+    // A unit's start and end cost about eight tiles.  Counted as none / 4 / 8 / 16, us (8 key heads, 500 .. 4000
+    // keys unless said): 128 sequences of 4 rows 117 / 107 / 98 / 97; 64 of 12 rows 125 / 106 / 96 / 94, of 16
+    // with heads of 64 77 / 65 / 59 / 56; 32 of 1 row, 2000 keys 31 / 29 / 27 / 29; long ones 112 / 110 / 110 / 107.
+    // Only 64 of 4 rows with heads of 64 would rather have none, 53 / 55 / 59 / 64.
     const UnitShape<8> sh{kQ4Keys, Sh::kRows, a.G};
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
@@ -740,9 +743,12 @@ template <typename T, int D>
 cudaError_t launch_q4_d(const AttendQ4Args &a, cudaStream_t st)
 {
     // Query rows of a key head decide.  Measured on both sides (500 .. 4000 keys, 8 key heads of 128, us):
-    //   1 .. 8 rows   one query tile here 97 (128 sequences of 4 rows), two 153, tcgen05 180
-    //   9 .. 16       two tiles 91 (64 of 12), one (two units) 96, tcgen05 99; heads of 64 (16 rows) 58, 67, 83
-    //   17 and more   tcgen05 101 (64 of 20), units of 16 rows here 160
+    //   1 .. 8 rows   one query tile here 97 (128 sequences of 4 rows), two 153, tcgen05 180; heads of 64 59, 72, 105
+    //   9 .. 16       two tiles 91 (64 of 12), one (two units) 96, tcgen05 99; heads of 64 (16 rows) 58, 67, 84
+    //   17 and more   tcgen05 100 (64 of 20), units of 16 rows here 168, of 8 136
+    // Batches of 8 and 16 over 50 .. 400 keys and 2 key heads take 18 .. 21 in any form.  The rule is made for
+    // batches: 4 sequences over 20000 .. 40000 keys, 2 key heads of 64, would rather have tcgen05 from 8 rows on
+    // (8 rows 45, 39, 33; 16 rows 40, 37, 33; 20 rows 37 in all).
     const int rows = a.a.seq.T * a.a.G;
     if (rows > 16)
         return launch_attend_q4_tc(a, std::is_same<T, __half>::value ? SPEC_F16 : SPEC_BF16, st);

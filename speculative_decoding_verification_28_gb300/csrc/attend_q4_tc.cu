@@ -282,7 +282,9 @@ __global__ void __launch_bounds__(kQtThreads, 1) attend_q4_tc_kernel(const __gri
     const AttendArgs &a = x.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int kRows = kQtLanes / COPIES;  // of a unit
-    // a unit's start and end cost about two tiles (256 chains 340 us; counted as none 377, one 355, four 348)
+    // A unit's start and end cost about two tiles.  Counted as none / 1 / 2 / 4, us: 256 chains of 9 374 / 357 / 335 /
+    // 339, 32 trees of 64 nodes 130 / 120 / 115 / 114, of heads of 64 105 / 97 / 92 / 94; 64 chains of 20 rows 115 /
+    // 104 / 100 / 102, 32 of 80 82 / 76 / 72 / 73, 128 of 36 rows and heads of 64 171 / 161 / 154 / 158.
     const UnitShape<2> sh{kKeys, kRows, a.G};
     constexpr int kMmaWarp = kQtSoftmax, kLoadWarp = kMmaWarp + 1, kFirstExpand = kMmaWarp + 4;
     constexpr bool kHalf = std::is_same<T, __half>::value;
